@@ -100,9 +100,20 @@ typedef enum moe_expert_copy {   /* which experts the streamed prefill moves to 
   MOE_COPY_AUTO = 2              /* ROUTED when T <= routed_copy_max_tokens, else ALL */
 } moe_expert_copy;
 
+typedef enum moe_float_dtype {   /* tensors of the dense projections */
+  MOE_FLOAT_BF16 = 0,
+  MOE_FLOAT_FP16 = 1,
+  MOE_FLOAT_FP32 = 2
+} moe_float_dtype;
+
+typedef enum moe_gate_act {      /* the activation of the dense projections' gated epilogue */
+  MOE_GATE_SILU = 0,             /* z / (1 + e^-z) */
+  MOE_GATE_GELU = 1              /* tanh form: z/2 * (1 + tanh(sqrt(2/pi) * (z + 0.044715 z^3))) */
+} moe_gate_act;
+
 typedef enum moe_enum_kind {
   MOE_ENUM_STATUS = 0, MOE_ENUM_ACT = 1, MOE_ENUM_OUT = 2, MOE_ENUM_EPI = 3, MOE_ENUM_CHAIN = 4,
-  MOE_ENUM_WFORMAT = 5, MOE_ENUM_COPY = 6
+  MOE_ENUM_WFORMAT = 5, MOE_ENUM_COPY = 6, MOE_ENUM_FLOAT = 7, MOE_ENUM_GATE = 8
 } moe_enum_kind;
 
 /* ------------------------------------------------------------ queries -- */
@@ -404,6 +415,118 @@ size_t     moe_streamed_workspace_size(int32_t T, int32_t H, int32_t I, int32_t 
  */
 moe_status moe_layer_prefill_streamed(const moe_streamed_args* args, void* compute_stream,
                                       void* copy_stream);
+
+/* ------------------------------- gated feed-forward block, 16-bit weights -- */
+
+/* The dense block that runs beside the routed experts (a shared expert) or in
+ * their place (a dense layer), for bf16 or fp16 activations and weights:
+ *   gate_up = x * w1^T                          [T][2I], in w1's row order
+ *   h[:, i] = act(gate_i) * up_i                [T][I]
+ *   out     = (add +) h * w2^T                  [T][H]
+ * Products accumulate in fp32, the gate is applied to the fp32 sums; h is
+ * rounded once to `dtype` (the matrix cores' operand), out once to out_dtype.
+ *
+ * Sizes: T >= 0 (T == 0 enqueues nothing), H and I multiples of 8, both in
+ * [8, 262144].  Row strides are in elements, multiples of 8, at least the row
+ * and at most 2^22; every pointer is 16-byte aligned.  w1, w2 and gate_up are
+ * contiguous.  `out` may be `add` itself (same pointer and stride); apart
+ * from that no output may overlap an input or another output. */
+typedef struct moe_ffn_args {
+  int32_t     T, H, I;
+  int32_t     layout;            /* MOE_EPI_SWIGLU_SPLIT or _INTERLEAVED: w1's row order */
+  int32_t     gate_act;          /* moe_gate_act */
+  int32_t     dtype;             /* x, w1, w2: MOE_FLOAT_BF16 or MOE_FLOAT_FP16 */
+  int32_t     out_dtype;         /* out and add: `dtype` or MOE_FLOAT_FP32 */
+  int32_t     save_dtype;        /* gate_up: `dtype` or MOE_FLOAT_FP32 */
+  const void* x;                 /* device [T][H] */
+  const void* w1;                /* device [2I][H] */
+  const void* w2;                /* device [H][I] */
+  const void* add;               /* device [T][H] or NULL */
+  void*       out;               /* device out [T][H] */
+  void*       gate_up;           /* device out [T][2I], kept for the backward pass, or NULL */
+  int64_t     x_stride, add_stride, out_stride;
+  void*       workspace;         /* device, >= moe_gated_ffn_workspace_size() */
+  size_t      workspace_bytes;
+} moe_ffn_args;
+
+size_t     moe_gated_ffn_workspace_size(int32_t T, int32_t H, int32_t I);
+moe_status moe_gated_ffn_forward(const moe_ffn_args* args, void* stream);
+
+/* The block's gradients from dout and the gate_up that forward kept:
+ *   dh = dout * w2;  d_gate = dh * up * act'(gate);  d_up = dh * act(gate)
+ *   dx = d_gate_up * w1;  dw1 = d_gate_up^T * x;  dw2 = dout^T * h
+ * (the gradient of `add` is dout).  Any of dx, dw1, dw2 may be NULL: it is not
+ * computed.  d_gate_up and h are rounded once to `dtype`.  With accumulate
+ * dw1 and dw2 hold earlier gradients and are added to, in fp32, before their
+ * rounding.  T == 0 writes zeros to dw1 and dw2 (leaves them with accumulate).
+ * Deterministic: no atomics.  Size, stride and overlap rules as above. */
+typedef struct moe_ffn_grad_args {
+  int32_t     T, H, I;
+  int32_t     layout, gate_act;
+  int32_t     dtype;             /* dout, x, w1, w2 */
+  int32_t     save_dtype;        /* gate_up: `dtype` or MOE_FLOAT_FP32 */
+  int32_t     dx_dtype;          /* `dtype` or MOE_FLOAT_FP32 */
+  int32_t     dw_dtype;          /* dw1 and dw2: `dtype` or MOE_FLOAT_FP32 */
+  int32_t     accumulate;        /* 0 or 1 */
+  const void* dout;              /* device [T][H] */
+  const void* x;                 /* device [T][H] (read for dw1 only) */
+  const void* w1;                /* device [2I][H] (read for dx only) */
+  const void* w2;                /* device [H][I] */
+  const void* gate_up;           /* device [T][2I] */
+  void*       dx;                /* device out [T][H] or NULL */
+  void*       dw1;               /* device out [2I][H] or NULL */
+  void*       dw2;               /* device out [H][I] or NULL */
+  int64_t     dout_stride, x_stride, dx_stride;
+  void*       workspace;         /* device, >= moe_gated_ffn_grad_workspace_size() */
+  size_t      workspace_bytes;
+} moe_ffn_grad_args;
+
+size_t     moe_gated_ffn_grad_workspace_size(int32_t T, int32_t H, int32_t I);
+moe_status moe_gated_ffn_backward(const moe_ffn_grad_args* args, void* stream);
+
+/* ------------- low-rank adapters of many requests beside a projection -- */
+
+/* One projection shared by all tokens plus each token's own adapter:
+ *   y[t] = (add[t] +) x[t] * w^T + scales[a] * (x[t] * A[a]^T) * B[a]^T,  a = ids[t]
+ *   out  = y, or for a SWIGLU epilogue act(gate columns of y) * up columns
+ * An id outside [0, num_adapters) means no adapter: that token gets the shared
+ * projection alone.  Tokens may come in any order and share adapters.  With
+ * ranks, adapter a uses its first ranks[a] (clamped to [0, R]) rows of A and
+ * columns of B; what lies behind them is not used.  w may be NULL (MOE_EPI_NONE
+ * only): the adapters' part alone, added to what another projection gave
+ * (a grouped GEMM with MXFP4 weights, say) through `add`.
+ * A token's result depends on its own row and adapter only: infinities or NaN
+ * in one adapter or token do not reach the others.
+ * The low-rank row scales[a] * x A^T is rounded once to `dtype`.
+ *
+ * Sizes: T >= 0 (T == 0 enqueues nothing), K, N multiples of 8 in [8, 262144],
+ * N % 16 == 0 for SWIGLU; 0 <= num_adapters <= 65536; R a multiple of 8 in
+ * [8, 256].  Strides, alignment and overlap as for moe_gated_ffn_forward
+ * (ids, scales and ranks: 4-byte aligned).  With a SWIGLU epilogue add has N
+ * columns (it is added before the gate) and cannot be `out`. */
+typedef struct moe_adapter_args {
+  int32_t        T, K, N;
+  int32_t        num_adapters, R;
+  int32_t        epilogue;       /* moe_epilogue */
+  int32_t        gate_act;       /* moe_gate_act (SWIGLU epilogues) */
+  int32_t        dtype;          /* x, w, a, b: MOE_FLOAT_BF16 or MOE_FLOAT_FP16 */
+  int32_t        out_dtype;      /* out and add: `dtype` or MOE_FLOAT_FP32 */
+  const void*    x;              /* device [T][K] */
+  const void*    w;              /* device [N][K] or NULL */
+  const int32_t* ids;            /* device [T] */
+  const void*    a;              /* device [num_adapters][R][K] */
+  const void*    b;              /* device [num_adapters][N][R] */
+  const float*   scales;         /* device [num_adapters] or NULL: 1 */
+  const int32_t* ranks;          /* device [num_adapters] or NULL: R */
+  const void*    add;            /* device [T][N] or NULL */
+  void*          out;            /* device out [T][N], or [T][N/2] for SWIGLU */
+  int64_t        x_stride, add_stride, out_stride;
+  void*          workspace;      /* device, >= moe_adapter_workspace_size() */
+  size_t         workspace_bytes;
+} moe_adapter_args;
+
+size_t     moe_adapter_workspace_size(int32_t T, int32_t K, int32_t N, int32_t num_adapters, int32_t R);
+moe_status moe_adapter_linear(const moe_adapter_args* args, void* stream);
 
 #ifdef __cplusplus
 }

@@ -28,13 +28,19 @@ EPI = {"MOE_EPI_NONE": 0, "MOE_EPI_SWIGLU_SPLIT": 1, "MOE_EPI_SWIGLU_INTERLEAVED
 CHAIN = {"MOE_CHAIN_RMS": 0, "MOE_CHAIN_INDEPENDENT": 1}
 WFORMAT = {"MOE_W_CANONICAL": 0, "MOE_W_TILED": 1}
 COPY = {"MOE_COPY_ALL": 0, "MOE_COPY_ROUTED": 1, "MOE_COPY_AUTO": 2}
-ENUM_KINDS = {0: STATUS, 1: ACT, 2: OUT, 3: EPI, 4: CHAIN, 5: WFORMAT, 6: COPY}
+FLOAT = {"MOE_FLOAT_BF16": 0, "MOE_FLOAT_FP16": 1, "MOE_FLOAT_FP32": 2}
+GATE = {"MOE_GATE_SILU": 0, "MOE_GATE_GELU": 1}
+ENUM_KINDS = {0: STATUS, 1: ACT, 2: OUT, 3: EPI, 4: CHAIN, 5: WFORMAT, 6: COPY, 7: FLOAT, 8: GATE}
 EXPERT_COPY = {"all": COPY["MOE_COPY_ALL"], "routed": COPY["MOE_COPY_ROUTED"], "auto": COPY["MOE_COPY_AUTO"]}
 W_FORMAT = {"canonical": WFORMAT["MOE_W_CANONICAL"], "tiled": WFORMAT["MOE_W_TILED"]}
 
+GATE_ACT = {"silu": GATE["MOE_GATE_SILU"], "gelu": GATE["MOE_GATE_GELU"]}
+FLOAT_DTYPE = {torch.bfloat16: FLOAT["MOE_FLOAT_BF16"], torch.float16: FLOAT["MOE_FLOAT_FP16"],
+               torch.float32: FLOAT["MOE_FLOAT_FP32"]}
+
 LAYOUT = {"split": EPI["MOE_EPI_SWIGLU_SPLIT"], "interleaved": EPI["MOE_EPI_SWIGLU_INTERLEAVED"]}
 
-_vp, _i32, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
+_vp, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
 
 
 class MoeError(RuntimeError):
@@ -67,6 +73,29 @@ class StreamedArgs(ctypes.Structure):
                 ("routed_copy_max_tokens", _i32)]
 
 
+class FfnArgs(ctypes.Structure):
+    _fields_ = [("T", _i32), ("H", _i32), ("I", _i32), ("layout", _i32), ("gate_act", _i32), ("dtype", _i32),
+                ("out_dtype", _i32), ("save_dtype", _i32), ("x", _vp), ("w1", _vp), ("w2", _vp), ("add", _vp),
+                ("out", _vp), ("gate_up", _vp), ("x_stride", _i64), ("add_stride", _i64), ("out_stride", _i64),
+                ("workspace", _vp), ("workspace_bytes", _sz)]
+
+
+class FfnGradArgs(ctypes.Structure):
+    _fields_ = [("T", _i32), ("H", _i32), ("I", _i32), ("layout", _i32), ("gate_act", _i32), ("dtype", _i32),
+                ("save_dtype", _i32), ("dx_dtype", _i32), ("dw_dtype", _i32), ("accumulate", _i32), ("dout", _vp),
+                ("x", _vp), ("w1", _vp), ("w2", _vp), ("gate_up", _vp), ("dx", _vp), ("dw1", _vp), ("dw2", _vp),
+                ("dout_stride", _i64), ("x_stride", _i64), ("dx_stride", _i64), ("workspace", _vp),
+                ("workspace_bytes", _sz)]
+
+
+class AdapterArgs(ctypes.Structure):
+    _fields_ = [("T", _i32), ("K", _i32), ("N", _i32), ("num_adapters", _i32), ("R", _i32), ("epilogue", _i32),
+                ("gate_act", _i32), ("dtype", _i32), ("out_dtype", _i32), ("x", _vp), ("w", _vp), ("ids", _vp),
+                ("a", _vp), ("b", _vp), ("scales", _vp), ("ranks", _vp), ("add", _vp), ("out", _vp),
+                ("x_stride", _i64), ("add_stride", _i64), ("out_stride", _i64), ("workspace", _vp),
+                ("workspace_bytes", _sz)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is not built; run `python -m mxfp4_weight_mixture_amd.build`")
@@ -97,6 +126,12 @@ def _load():
         "moe_layer_graph_create": (ctypes.c_int, [ctypes.POINTER(LayerArgs), _vp, ctypes.POINTER(_vp)]),
         "moe_layer_graph_launch": (ctypes.c_int, [_vp, _vp]),
         "moe_layer_graph_destroy": (ctypes.c_int, [_vp]),
+        "moe_gated_ffn_workspace_size": (_sz, [_i32, _i32, _i32]),
+        "moe_gated_ffn_forward": (ctypes.c_int, [ctypes.POINTER(FfnArgs), _vp]),
+        "moe_gated_ffn_grad_workspace_size": (_sz, [_i32, _i32, _i32]),
+        "moe_gated_ffn_backward": (ctypes.c_int, [ctypes.POINTER(FfnGradArgs), _vp]),
+        "moe_adapter_workspace_size": (_sz, [_i32, _i32, _i32, _i32, _i32]),
+        "moe_adapter_linear": (ctypes.c_int, [ctypes.POINTER(AdapterArgs), _vp]),
     }
     for name, (res, args) in sigs.items():
         fn = getattr(lib, name)
@@ -266,6 +301,237 @@ def combine(y: torch.Tensor, dest_row: torch.Tensor, topk_w: torch.Tensor, *, rm
                            _stream(stream)))
     _keep_until_done(stream, out, xn)
     return (out, xn) if rms_next else out
+
+
+# --------------------------------------------- dense 16-bit projections
+
+def _rows(name, t, rows, cols, dtypes, device):
+    """Check a [rows][cols] tensor whose rows are contiguous; returns its row stride in elements."""
+    if t.dim() != 2 or t.shape[1] != cols or (rows is not None and t.shape[0] != rows):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not ({'T' if rows is None else rows}, {cols})")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} is {t.dtype}, not {' or '.join(str(d) for d in dtypes)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the weights on {device}")
+    if t.stride(1) != 1:
+        raise ValueError(f"{name}'s rows are not contiguous (strides {t.stride()})")
+    return t.stride(0) if t.shape[0] > 1 else cols
+
+
+def _flat(name, t, shape, dtypes, device):
+    """Check a contiguous tensor of a given shape."""
+    if tuple(t.shape) != tuple(shape) or t.dtype not in dtypes or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {' or '.join(str(d) for d in dtypes)} tensor of shape "
+                         f"{tuple(shape)} on {device}: got {t.dtype} {tuple(t.shape)}, strides {t.stride()}, "
+                         f"on {t.device}")
+    return t
+
+
+def _on_current_device(device, stream):
+    """The library enqueues on the current device: refuse tensors and streams of another."""
+    if torch.cuda.current_device() != device.index:
+        raise ValueError(f"the weights are on {device}, the current device is cuda:{torch.cuda.current_device()}")
+    if stream is not None and stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the weights on {device}")
+
+
+def _weight(name, w):
+    if w.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError(f"{name} is {w.dtype}, not torch.bfloat16 or torch.float16")
+    if not w.is_cuda or not w.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous device tensor")
+
+
+class GatedFFN:
+    """The gated feed-forward block with 16-bit weights: a shared expert beside the routed ones, or a dense layer.
+
+    out = (add +) (act(x Wg^T) * (x Wu^T)) W2^T with w1 [2I][H] holding Wg and Wu ("split": Wg's rows, then
+    Wu's; "interleaved": row 2i of Wg, then of Wu), w2 [H][I]; act "silu" or "gelu" (tanh form).  bf16 or
+    fp16; fp32 accumulation; h = act(..) * (..) is rounded once to the weights' type.
+
+    The object holds no buffers of its own: calls from several streams or threads, and calls captured into
+    graphs, are independent of each other.
+    """
+
+    def __init__(self, w1: torch.Tensor, w2: torch.Tensor, layout: str = "split", act: str = "silu"):
+        _weight("w1", w1)
+        _weight("w2", w2)
+        if w1.dim() != 2 or w2.dim() != 2 or w1.shape != (2 * w2.shape[1], w2.shape[0]):
+            raise ValueError(f"w1 {tuple(w1.shape)} and w2 {tuple(w2.shape)} are not [2I][H] and [H][I]")
+        if w1.dtype != w2.dtype or w1.device != w2.device:
+            raise ValueError("w1 and w2 differ in type or device")
+        if layout not in LAYOUT or act not in GATE_ACT:
+            raise ValueError(f"layout {layout!r} / act {act!r}: not {list(LAYOUT)} / {list(GATE_ACT)}")
+        self.w1, self.w2, self.layout, self.act = w1, w2, layout, act
+        self.H, self.I = w2.shape
+        self.dtype, self.device = w1.dtype, w1.device
+        self._dtypes = (self.dtype, torch.float32)
+        dt = FLOAT_DTYPE[self.dtype]
+        self._fwd = FfnArgs(H=self.H, I=self.I, layout=LAYOUT[layout], gate_act=GATE_ACT[act], dtype=dt)
+        self._bwd = FfnGradArgs(H=self.H, I=self.I, layout=LAYOUT[layout], gate_act=GATE_ACT[act], dtype=dt)
+
+    def forward(self, x: torch.Tensor, add: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None, *,
+                out_dtype: Optional[torch.dtype] = None, save=False, stream=None):
+        """moe_gated_ffn_forward: x [T][H] -> out [T][H], or (out, gate_up) with save.
+
+        add: [T][H], added to the result; `out` may be `add` itself.  out_dtype: the weights' type (default)
+        or torch.float32; `add`'s and `out`'s type if they are given.  save: keep the pre-activations
+        gate_up [T][2I] for backward(), True in fp32, "half" in the weights' type (half the memory, one more
+        rounding in the gradients).
+        """
+        _on_current_device(self.device, stream)
+        a = FfnArgs.from_buffer_copy(self._fwd)
+        a.x_stride = _rows("x", x, None, self.H, (self.dtype,), self.device)
+        T = a.T = x.shape[0]
+        if out is None:
+            out = torch.empty((T, self.H), device=self.device,
+                              dtype=out_dtype or (add.dtype if add is not None else self.dtype))
+        a.out_stride = _rows("out", out, T, self.H, self._dtypes, self.device)
+        if out_dtype is not None and out.dtype != out_dtype:
+            raise ValueError(f"out is {out.dtype}, out_dtype {out_dtype}")
+        a.out_dtype = FLOAT_DTYPE[out.dtype]
+        if add is not None:
+            a.add_stride = _rows("add", add, T, self.H, (out.dtype,), self.device)
+            a.add = add.data_ptr()
+        gate_up = None
+        if save:
+            gate_up = torch.empty((T, 2 * self.I), device=self.device,
+                                  dtype=self.dtype if save == "half" else torch.float32)
+            a.save_dtype, a.gate_up = FLOAT_DTYPE[gate_up.dtype], gate_up.data_ptr()
+        else:
+            a.save_dtype = a.dtype
+        n = lib.moe_gated_ffn_workspace_size(T, self.H, self.I)
+        ws = _u8(n, self.device)
+        a.x, a.w1, a.w2, a.out = x.data_ptr(), self.w1.data_ptr(), self.w2.data_ptr(), out.data_ptr()
+        a.workspace, a.workspace_bytes = ws.data_ptr(), n
+        _check(lib.moe_gated_ffn_forward(ctypes.byref(a), _stream(stream)))
+        _keep_until_done(stream, out, gate_up, ws)
+        return (out, gate_up) if save else out
+
+    def backward(self, dout: torch.Tensor, x: torch.Tensor, gate_up: torch.Tensor, *, dx=True, dw1=True, dw2=True,
+                 dw_dtype: Optional[torch.dtype] = None, accumulate: bool = False, stream=None):
+        """moe_gated_ffn_backward: (dx, dw1, dw2) from dout [T][H], x and forward's gate_up.
+
+        dx, dw1, dw2: True allocates the gradient, a tensor receives it, False or None skips it.  dw_dtype:
+        type of the weight gradients made here, the weights' (default) or torch.float32.  accumulate: the
+        given dw1 and dw2 are added to.
+        """
+        _on_current_device(self.device, stream)
+        a = FfnGradArgs.from_buffer_copy(self._bwd)
+        a.dout_stride = _rows("dout", dout, None, self.H, (self.dtype,), self.device)
+        T = a.T = dout.shape[0]
+        a.x_stride = _rows("x", x, T, self.H, (self.dtype,), self.device)
+        _flat("gate_up", gate_up, (T, 2 * self.I), self._dtypes, self.device)
+
+        def grad(g, shape, dtype):
+            if g is True:
+                return torch.empty(shape, dtype=dtype, device=self.device)
+            return None if g is None or g is False else g
+
+        if accumulate and (dw1 is True or dw2 is True):
+            raise ValueError("accumulate needs the tensors to add to")
+        dw_dtype = dw_dtype or next((g.dtype for g in (dw1, dw2) if isinstance(g, torch.Tensor)), self.dtype)
+        dx = grad(dx, (T, self.H), self.dtype)
+        dw1 = grad(dw1, (2 * self.I, self.H), dw_dtype)
+        dw2 = grad(dw2, (self.H, self.I), dw_dtype)
+        a.dx_dtype = a.dtype
+        if dx is not None:
+            a.dx_stride = _rows("dx", dx, T, self.H, self._dtypes, self.device)
+            a.dx_dtype, a.dx = FLOAT_DTYPE[dx.dtype], dx.data_ptr()
+        a.dw_dtype = FLOAT_DTYPE.get(dw_dtype, -1)
+        if dw1 is not None:
+            a.dw1 = _flat("dw1", dw1, (2 * self.I, self.H), (dw_dtype,), self.device).data_ptr()
+        if dw2 is not None:
+            a.dw2 = _flat("dw2", dw2, (self.H, self.I), (dw_dtype,), self.device).data_ptr()
+        a.accumulate = int(accumulate)
+        a.save_dtype = FLOAT_DTYPE[gate_up.dtype]
+        n = lib.moe_gated_ffn_grad_workspace_size(T, self.H, self.I)
+        ws = _u8(n, self.device)
+        a.dout, a.x, a.w1, a.w2 = dout.data_ptr(), x.data_ptr(), self.w1.data_ptr(), self.w2.data_ptr()
+        a.gate_up, a.workspace, a.workspace_bytes = gate_up.data_ptr(), ws.data_ptr(), n
+        _check(lib.moe_gated_ffn_backward(ctypes.byref(a), _stream(stream)))
+        _keep_until_done(stream, dx, dw1, dw2, ws)
+        return dx, dw1, dw2
+
+
+class AdapterLinear:
+    """One projection shared by all tokens, plus each token's own low-rank adapter (many requests in a batch).
+
+    y[t] = (add[t] +) x[t] w^T + scales[a] (x[t] lora_a[a]^T) lora_b[a]^T with a = ids[t]; an id outside
+    [0, num_adapters) means no adapter.  w [N][K] (None: the adapters' part alone, for projections computed
+    elsewhere), lora_a [num_adapters][R][K], lora_b [num_adapters][N][R], scales fp32 and ranks int32
+    [num_adapters].  epilogue "split" or "interleaved": w's rows are gate and up, out = act(gate) * up.
+
+    Adapters may be replaced in place between calls.  No buffers are held (see GatedFFN).
+    """
+
+    def __init__(self, w: Optional[torch.Tensor], lora_a: torch.Tensor, lora_b: torch.Tensor, *,
+                 scales: Optional[torch.Tensor] = None, ranks: Optional[torch.Tensor] = None, epilogue: str = "none",
+                 act: str = "silu"):
+        _weight("lora_a", lora_a)
+        _weight("lora_b", lora_b)
+        if lora_a.dim() != 3 or lora_b.dim() != 3 or lora_a.shape[0] != lora_b.shape[0] \
+                or lora_a.shape[1] != lora_b.shape[2]:
+            raise ValueError(f"lora_a {tuple(lora_a.shape)} and lora_b {tuple(lora_b.shape)} are not [n][R][K] "
+                             "and [n][N][R]")
+        self.n, self.R, self.K = lora_a.shape
+        self.N = lora_b.shape[1]
+        self.dtype, self.device = lora_a.dtype, lora_a.device
+        if lora_b.dtype != self.dtype or lora_b.device != self.device:
+            raise ValueError("lora_a and lora_b differ in type or device")
+        if w is not None:
+            _flat("w", w, (self.N, self.K), (self.dtype,), self.device)
+        if scales is not None:
+            _flat("scales", scales, (self.n,), (torch.float32,), self.device)
+        if ranks is not None:
+            _flat("ranks", ranks, (self.n,), (torch.int32,), self.device)
+        epi = {"none": 0, **LAYOUT}
+        if epilogue not in epi or act not in GATE_ACT:
+            raise ValueError(f"epilogue {epilogue!r} / act {act!r}: not {list(epi)} / {list(GATE_ACT)}")
+        if epilogue != "none" and w is None:
+            raise ValueError("a gated epilogue needs w")
+        self.w, self.lora_a, self.lora_b, self.scales, self.ranks = w, lora_a, lora_b, scales, ranks
+        self.n_out = self.N if epilogue == "none" else self.N // 2
+        self._dtypes = (self.dtype, torch.float32)
+        self._tmpl = AdapterArgs(K=self.K, N=self.N, num_adapters=self.n, R=self.R, epilogue=epi[epilogue],
+                                 gate_act=GATE_ACT[act], dtype=FLOAT_DTYPE[self.dtype])
+
+    def forward(self, x: torch.Tensor, ids: torch.Tensor, add: Optional[torch.Tensor] = None,
+                out: Optional[torch.Tensor] = None, *, out_dtype: Optional[torch.dtype] = None, stream=None):
+        """moe_adapter_linear: x [T][K], ids int32 [T] -> out [T][N] ([T][N/2] for a gated epilogue).
+
+        add: [T][N], added before the epilogue; without one, `out` may be `add` itself.  out_dtype: the
+        weights' type (default) or torch.float32; `add`'s and `out`'s type if they are given.
+        """
+        _on_current_device(self.device, stream)
+        a = AdapterArgs.from_buffer_copy(self._tmpl)
+        a.x_stride = _rows("x", x, None, self.K, (self.dtype,), self.device)
+        T = a.T = x.shape[0]
+        _flat("ids", ids, (T,), (torch.int32,), self.device)
+        if out is None:
+            out = torch.empty((T, self.n_out), device=self.device,
+                              dtype=out_dtype or (add.dtype if add is not None else self.dtype))
+        a.out_stride = _rows("out", out, T, self.n_out, self._dtypes, self.device)
+        if out_dtype is not None and out.dtype != out_dtype:
+            raise ValueError(f"out is {out.dtype}, out_dtype {out_dtype}")
+        a.out_dtype = FLOAT_DTYPE[out.dtype]
+        if add is not None:
+            a.add_stride = _rows("add", add, T, self.N, (out.dtype,), self.device)
+            a.add = add.data_ptr()
+        n = lib.moe_adapter_workspace_size(T, self.K, self.N, self.n, self.R)
+        ws = _u8(n, self.device)
+        a.x, a.ids, a.out, a.a, a.b = (x.data_ptr(), ids.data_ptr(), out.data_ptr(), self.lora_a.data_ptr(),
+                                       self.lora_b.data_ptr())
+        if self.w is not None:
+            a.w = self.w.data_ptr()
+        if self.scales is not None:
+            a.scales = self.scales.data_ptr()
+        if self.ranks is not None:
+            a.ranks = self.ranks.data_ptr()
+        a.workspace, a.workspace_bytes = ws.data_ptr(), n
+        _check(lib.moe_adapter_linear(ctypes.byref(a), _stream(stream)))
+        _keep_until_done(stream, out, ws)
+        return out
 
 
 class Layer:

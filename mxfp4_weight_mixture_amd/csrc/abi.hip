@@ -110,6 +110,12 @@ const char* moe_enum_name(int kind, int v) {
       return v == MOE_COPY_ALL ? "MOE_COPY_ALL"
              : v == MOE_COPY_ROUTED ? "MOE_COPY_ROUTED"
              : v == MOE_COPY_AUTO ? "MOE_COPY_AUTO" : nullptr;
+    case MOE_ENUM_FLOAT:
+      return v == MOE_FLOAT_BF16 ? "MOE_FLOAT_BF16"
+             : v == MOE_FLOAT_FP16 ? "MOE_FLOAT_FP16"
+             : v == MOE_FLOAT_FP32 ? "MOE_FLOAT_FP32" : nullptr;
+    case MOE_ENUM_GATE:
+      return v == MOE_GATE_SILU ? "MOE_GATE_SILU" : v == MOE_GATE_GELU ? "MOE_GATE_GELU" : nullptr;
     default: return nullptr;
   }
 }

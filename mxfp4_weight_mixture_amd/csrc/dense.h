@@ -1,0 +1,174 @@
+// Dense products with 16-bit operands: what the gated feed-forward block
+// (ffn.hip) and the many-adapter projection (adapter.hip) share.
+#pragma once
+
+#include "internal.h"
+
+namespace mxmoe {
+
+// One product C[m][n] = epilogue(sum_k A(m, k) B(n, k)), fp32 accumulation.
+// An operand is stored [rows][K] (t == false) or [K][rows] (t == true).
+enum DenseEpi { kEpiPlain = 0, kEpiGate = 1, kEpiGateGrad = 2 };
+
+struct DenseJob {
+  const void* a;            // M rows
+  const void* b;            // N rows (for kEpiGate: the 2I gate and up rows)
+  int64_t lda, ldb;         // elements
+  int ta, tb;
+  int M, N, K;
+  int dtype;                // moe_float_dtype of a and b
+  int epi;                  // DenseEpi
+  int interleaved;          // gate / up order of w1's rows and gate_up's columns
+  int act;                  // moe_gate_act
+  const void* add;          // [M][N] of c_dtype or null: added to the sum before the epilogue
+  int64_t ldadd;
+  void* c;                  // plain: [M][N]; gate: h [M][N/2]; gate gradient: d_gate_up [M][2N], stride ldc
+  int64_t ldc;
+  int c_dtype;
+  void* gu;                 // gate: gate_up [M][N] out or null; gate gradient: gate_up [M][2N] in (contiguous)
+  int gu_dtype;
+  void* h;                  // gate gradient: h [M][N] out, `dtype`, contiguous
+  // adapters (null ids: none): += s[m] * lb[ids[m]][n], over R terms
+  const int32_t* ids;
+  const int32_t* ranks;
+  const void* s;            // [M][R], `dtype`
+  const void* lb;           // [num_adapters][N][R]
+  int num_adapters, R;
+};
+
+size_t dense_ws_bytes(int M, int N, int K);
+moe_status launch_dense(const DenseJob& j, void* ws, hipStream_t s);
+
+// ---- argument checks shared by the entry points -------------------------
+constexpr int kMaxWidth = 1 << 18;
+constexpr int64_t kMaxStride = 1 << 22;
+
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+inline size_t float_bytes(int dtype) { return dtype == MOE_FLOAT_FP32 ? 4 : 2; }
+
+// The bytes a [rows][cols] tensor with a row stride covers, from its start.
+struct Span {
+  const char* name;
+  const void* p;
+  size_t bytes;
+};
+inline Span span(const char* name, const void* p, int64_t rows, int64_t cols, int64_t stride, int dtype) {
+  return {name, p, p && rows > 0 ? (size_t)((rows - 1) * stride + cols) * float_bytes(dtype) : 0};
+}
+inline bool overlap(const Span& a, const Span& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return a.bytes && b.bytes && x < y + b.bytes && y < x + a.bytes;
+}
+// Every span 16-byte aligned; no output overlaps another span.
+inline moe_status check_spans(const char* what, const Span* out, int n_out, const Span* in, int n_in) {
+  for (int i = 0; i < n_out + n_in; ++i) {
+    const Span& s = i < n_out ? out[i] : in[i - n_out];
+    if (!aligned16(s.p)) return fail(MOE_ERR_INVALID_ARG, "%s: %s is not 16-byte aligned", what, s.name);
+  }
+  for (int i = 0; i < n_out; ++i) {
+    for (int j = i + 1; j < n_out; ++j)
+      if (overlap(out[i], out[j]))
+        return fail(MOE_ERR_INVALID_ARG, "%s: %s and %s overlap", what, out[i].name, out[j].name);
+    for (int j = 0; j < n_in; ++j)
+      if (overlap(out[i], in[j]))
+        return fail(MOE_ERR_INVALID_ARG, "%s: %s overlaps %s", what, out[i].name, in[j].name);
+  }
+  return MOE_OK;
+}
+inline moe_status check_width(const char* what, const char* name, int v) {
+  if (v < 8 || v > kMaxWidth || v % 8)
+    return fail(MOE_ERR_SHAPE, "%s: %s = %d must be a multiple of 8 in [8, %d]", what, name, v, kMaxWidth);
+  return MOE_OK;
+}
+inline moe_status check_stride(const char* what, const char* name, int64_t stride, int64_t cols) {
+  if (stride < cols || stride > kMaxStride || stride % 8)
+    return fail(MOE_ERR_SHAPE, "%s: %s = %lld must be a multiple of 8 in [%lld, %lld]", what, name, (long long)stride,
+                (long long)cols, (long long)kMaxStride);
+  return MOE_OK;
+}
+inline moe_status check_dtype16(const char* what, int dtype) {
+  if (dtype != MOE_FLOAT_BF16 && dtype != MOE_FLOAT_FP16)
+    return fail(MOE_ERR_INVALID_ARG, "%s: dtype %d must be MOE_FLOAT_BF16 or MOE_FLOAT_FP16", what, dtype);
+  return MOE_OK;
+}
+inline moe_status check_dtype_or_fp32(const char* what, const char* name, int v, int dtype) {
+  if (v != dtype && v != MOE_FLOAT_FP32)
+    return fail(MOE_ERR_INVALID_ARG, "%s: %s %d must be dtype or MOE_FLOAT_FP32", what, name, v);
+  return MOE_OK;
+}
+
+#ifdef __HIPCC__
+// ---- device helpers -------------------------------------------------------
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef float v4f __attribute__((ext_vector_type(4)));
+
+template <typename E>
+struct Vec;
+template <>
+struct Vec<__bf16> {
+  typedef __bf16 v8 __attribute__((ext_vector_type(8)));
+  typedef __bf16 v4 __attribute__((ext_vector_type(4)));
+};
+template <>
+struct Vec<_Float16> {
+  typedef _Float16 v8 __attribute__((ext_vector_type(8)));
+  typedef _Float16 v4 __attribute__((ext_vector_type(4)));
+};
+
+__device__ __forceinline__ v16f mfma32(Vec<__bf16>::v8 a, Vec<__bf16>::v8 b, v16f c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ v16f mfma32(Vec<_Float16>::v8 a, Vec<_Float16>::v8 b, v16f c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ v4f mfma16(Vec<__bf16>::v8 a, Vec<__bf16>::v8 b, v4f c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ v4f mfma16(Vec<_Float16>::v8 a, Vec<_Float16>::v8 b, v4f c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
+// sigmoid, exact at both ends: e^-z overflows to infinity and the reciprocal is 0
+__device__ __forceinline__ float sigmoid(float z) { return __builtin_amdgcn_rcpf(1.0f + __expf(-z)); }
+
+// act(g) and act'(g).  The tanh GELU is g * sigmoid(2 p(g)) with
+// p(g) = sqrt(2/pi) (g + 0.044715 g^3), since (1 + tanh p) / 2 = sigmoid(2p);
+// the polynomial's argument is clamped where the sigmoid is 0 or 1 anyway, so
+// that g^3 stays finite.
+__device__ __forceinline__ float gate_act(int act, float g) {
+  if (act == MOE_GATE_SILU) return g * sigmoid(g);
+  const float c = fminf(fmaxf(g, -1e4f), 1e4f);
+  return g * sigmoid(1.5957691216057308f * c * (1.0f + 0.044715f * c * c));
+}
+__device__ __forceinline__ void gate_act_grad(int act, float g, float* a, float* da) {
+  if (act == MOE_GATE_SILU) {
+    const float s = sigmoid(g);
+    *a = g * s;
+    *da = s * (1.0f + g * (1.0f - s));
+  } else {
+    const float c = fminf(fmaxf(g, -1e4f), 1e4f);
+    const float s = sigmoid(1.5957691216057308f * c * (1.0f + 0.044715f * c * c));
+    *a = g * s;
+    *da = s + g * s * (1.0f - s) * 1.5957691216057308f * (1.0f + 0.134145f * c * c);
+  }
+}
+
+// Four consecutive values of a row; dtype is uniform.
+template <typename E>
+__device__ __forceinline__ v4f load4(const void* base, int dtype, size_t i) {
+  if (dtype == MOE_FLOAT_FP32) return *reinterpret_cast<const v4f*>(static_cast<const float*>(base) + i);
+  const typename Vec<E>::v4 v = *reinterpret_cast<const typename Vec<E>::v4*>(static_cast<const E*>(base) + i);
+  return v4f{(float)v[0], (float)v[1], (float)v[2], (float)v[3]};
+}
+template <typename E>
+__device__ __forceinline__ void store4(void* base, int dtype, size_t i, v4f v) {
+  if (dtype == MOE_FLOAT_FP32) {
+    *reinterpret_cast<v4f*>(static_cast<float*>(base) + i) = v;
+  } else {
+    typename Vec<E>::v4 o = {(E)v[0], (E)v[1], (E)v[2], (E)v[3]};
+    *reinterpret_cast<typename Vec<E>::v4*>(static_cast<E*>(base) + i) = o;
+  }
+}
+#endif
+
+}  // namespace mxmoe
