@@ -428,7 +428,7 @@ moe_status moe_layer_prefill_streamed(const moe_streamed_args* args, void* compu
  *
  * Sizes: T >= 0 (T == 0 enqueues nothing), H and I multiples of 8, both in
  * [8, 262144].  Row strides are in elements, multiples of 8, at least the row
- * and at most 2^22; every pointer is 16-byte aligned.  w1, w2 and gate_up are
+ * and at most 2^21; every pointer is 16-byte aligned.  w1, w2 and gate_up are
  * contiguous.  `out` may be `add` itself (same pointer and stride); apart
  * from that no output may overlap an input or another output. */
 typedef struct moe_ffn_args {

@@ -41,7 +41,7 @@ moe_status launch_dense(const DenseJob& j, void* ws, hipStream_t s);
 
 // ---- argument checks shared by the entry points -------------------------
 constexpr int kMaxWidth = 1 << 18;
-constexpr int64_t kMaxStride = 1 << 22;
+constexpr int64_t kMaxStride = 1 << 21;
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 inline size_t float_bytes(int dtype) { return dtype == MOE_FLOAT_FP32 ? 4 : 2; }

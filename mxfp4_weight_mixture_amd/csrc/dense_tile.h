@@ -1,0 +1,491 @@
+// The LDS-tiled dense kernel: one block of four waves per C tile.
+//
+// What bounds it is the matrix cores (32x32x16 MFMA, 32 clocks each on a
+// SIMD) next to the LDS: a wave's 32 FM x 32 FN tile reads FM + FN fragments
+// (1 KB each) per FM * FN products.  At 256 x 256 with four waves of 128 x 128
+// that is 64 bytes a clock of the LDS's 128, beside 32 for the incoming tiles;
+// eight waves of 128 x 64 would need 96 + 32 and are LDS-bound.  One wave per
+// SIMD then holds 256 accumulators and hides latency by itself: fragments are
+// read one 16-deep step ahead of their products.
+//
+// Tiles move global -> LDS without passing registers (buffer loads to LDS, 16
+// bytes a lane) in stages of 32 k, through a ring of kStages buffers.  In
+// stage s the block meets once, between its two 16-deep steps: by then every
+// wave has read all of stage s, so stage s + kStages may overwrite it, and
+// every wave's part of stage s + 1 has landed.
+//
+// LDS layout of a stage.  An operand stored [rows][K]: 64 bytes per row, its
+// four 16-byte chunks permuted by row (chunk ^ (row / 4) % 4), so that the 16
+// lanes that share a chunk cover all 64 banks.  An operand stored [K][rows]
+// (the weights in the backward products, both operands of a weight
+// gradient): 32 k-rows of BM or BN values, read through the transposing LDS
+// read, which hands lane i of 16 the column i of a 4 x 16 patch; 32-byte
+// column groups are permuted by k ((k % 4) + 4 (k / 8 % 2)), which spreads the
+// eight k-rows one read touches over the banks.
+//
+// Rows, columns and k past the end read as zeros: their lanes' offsets lie
+// behind the buffer resource's range, so no memory is touched.
+#pragma once
+
+#include <type_traits>
+
+#include "dense.h"
+
+namespace mxmoe {
+namespace {
+
+constexpr int kBK = 32;          // k per stage
+constexpr int kStages = 4;
+constexpr uint32_t kOut = 0x80000000u;   // an offset behind every resource's range
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_at(const void* base) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, 0x7fffffff, 0x00020000);
+}
+// 16 bytes per lane, global -> LDS (lane i writes dst + 16 i)
+__device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t r, uint32_t voff, void* dst) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)dst, 16, voff, 0, 0, 0);
+}
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
+}
+__device__ __forceinline__ void wait_lgkm0() { __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4)); }
+__device__ __forceinline__ void block_barrier() {
+  asm volatile("" ::: "memory");
+  wait_lgkm0();
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// First row of B behind tile columns [32 j, 32 j + 32) of n-tile nt, and the
+// distance of consecutive columns' rows; base is advanced for up rows.
+__device__ __forceinline__ void b_block(const DenseJob& p, int nt, int bn, int j, int* first, int* step, int* up) {
+  if (p.epi != kEpiGate) {
+    *first = nt * bn + 32 * j, *step = 1, *up = 0;
+    return;
+  }
+  *first = nt * (bn >> 1) + (j >> 1) * 32;   // index within gate or up
+  *step = p.interleaved ? 2 : 1;
+  *up = j & 1;
+}
+
+// Eight consecutive fp32 values.
+struct F8 {
+  float v[8];
+};
+template <typename E>
+__device__ __forceinline__ F8 load8(const void* base, int dtype, size_t i) {
+  F8 r;
+  if (dtype == MOE_FLOAT_FP32) {
+    const v4f* q = reinterpret_cast<const v4f*>(static_cast<const float*>(base) + i);
+    const v4f a = q[0], b = q[1];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) r.v[e] = a[e], r.v[4 + e] = b[e];
+  } else {
+    const typename Vec<E>::v8 a = *reinterpret_cast<const typename Vec<E>::v8*>(static_cast<const E*>(base) + i);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) r.v[e] = (float)a[e];
+  }
+  return r;
+}
+template <typename E>
+__device__ __forceinline__ void store8(void* base, int dtype, size_t i, const F8& r) {
+  if (dtype == MOE_FLOAT_FP32) {
+    v4f* q = reinterpret_cast<v4f*>(static_cast<float*>(base) + i);
+    q[0] = v4f{r.v[0], r.v[1], r.v[2], r.v[3]};
+    q[1] = v4f{r.v[4], r.v[5], r.v[6], r.v[7]};
+  } else {
+    typename Vec<E>::v8 o;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] = (E)r.v[e];
+    *reinterpret_cast<typename Vec<E>::v8*>(static_cast<E*>(base) + i) = o;
+  }
+}
+// Eight gate and eight up values of row m, gate index i, from gate_up-shaped memory.
+template <typename E>
+__device__ __forceinline__ void load_pair(const void* base, int dtype, size_t row, int I, int i, int interleaved,
+                                          F8* g, F8* u) {
+  if (!interleaved) {
+    *g = load8<E>(base, dtype, row + i);
+    *u = load8<E>(base, dtype, row + I + i);
+  } else {
+    const F8 a = load8<E>(base, dtype, row + 2 * i), b = load8<E>(base, dtype, row + 2 * i + 8);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      g->v[e] = a.v[2 * e], u->v[e] = a.v[2 * e + 1];
+      g->v[4 + e] = b.v[2 * e], u->v[4 + e] = b.v[2 * e + 1];
+    }
+  }
+}
+template <typename E>
+__device__ __forceinline__ void store_pair(void* base, int dtype, size_t row, int I, int i, int interleaved,
+                                           const F8& g, const F8& u) {
+  if (!interleaved) {
+    store8<E>(base, dtype, row + i, g);
+    store8<E>(base, dtype, row + I + i, u);
+  } else {
+    F8 a, b;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      a.v[2 * e] = g.v[e], a.v[2 * e + 1] = u.v[e];
+      b.v[2 * e] = g.v[4 + e], b.v[2 * e + 1] = u.v[4 + e];
+    }
+    store8<E>(base, dtype, row + 2 * i, a);
+    store8<E>(base, dtype, row + 2 * i + 8, b);
+  }
+}
+
+// What follows the sums, on eight consecutive columns of one row.
+// Plain: v are columns [n, n + 8) of C.
+template <typename E>
+__device__ __forceinline__ void finish_plain(const DenseJob& p, int m, int n, F8 v) {
+  if (p.add) {
+    const F8 a = load8<E>(p.add, p.c_dtype, (size_t)m * p.ldadd + n);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v.v[e] += a.v[e];
+  }
+  store8<E>(p.c, p.c_dtype, (size_t)m * p.ldc + n, v);
+}
+// Gate: g, u are the pre-activations of gate indices [i, i + 8).
+template <typename E>
+__device__ __forceinline__ void finish_gate(const DenseJob& p, int m, int i, F8 g, F8 u) {
+  const int I = p.N >> 1;
+  if (p.add) {
+    F8 a, b;
+    load_pair<E>(p.add, p.c_dtype, (size_t)m * p.ldadd, I, i, p.interleaved, &a, &b);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) g.v[e] += a.v[e], u.v[e] += b.v[e];
+  }
+  if (p.gu) store_pair<E>(p.gu, p.gu_dtype, (size_t)m * p.N, I, i, p.interleaved, g, u);
+  F8 h;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) h.v[e] = gate_act(p.act, g.v[e]) * u.v[e];
+  store8<E>(p.c, p.c_dtype, (size_t)m * p.ldc + i, h);
+}
+// Gate gradient: d are dh's columns [i, i + 8).
+template <typename E>
+__device__ __forceinline__ void finish_gate_grad(const DenseJob& p, int m, int i, F8 d) {
+  F8 g, u, h;
+  load_pair<E>(p.gu, p.gu_dtype, (size_t)m * 2 * p.N, p.N, i, p.interleaved, &g, &u);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    float a, da;
+    gate_act_grad(p.act, g.v[e], &a, &da);
+    h.v[e] = a * u.v[e];
+    g.v[e] = d.v[e] * u.v[e] * da;
+    u.v[e] = d.v[e] * a;
+  }
+  store8<E>(p.h, p.dtype, (size_t)m * p.N + i, h);
+  store_pair<E>(p.c, p.c_dtype, (size_t)m * p.ldc, p.N, i, p.interleaved, g, u);
+}
+
+// One operand's way from memory to the products: DMA of a stage, fragment reads.
+// ROWS: rows of the tile; T: stored [K][rows].
+template <typename E, int ROWS, bool T>
+struct Operand {
+  static constexpr int BYTES = ROWS * kBK * 2;            // of a stage
+  static constexpr int LOADS = BYTES / 1024 / 4;          // DMA instructions per wave
+  static_assert(LOADS >= 1, "at least 64 rows");
+  const char* base;      // of the tile's first row (or column), k = 0
+  int64_t stage_step;    // bytes from stage to stage
+  uint32_t off[LOADS];
+  int64_t up_off;        // bytes from gate to up rows (gate epilogue, split order)
+  uint32_t up_mask;      // loads that take up rows
+  int kk;                // this lane's k within a stage (of its chunk, or its k-row of load 0)
+
+  static __device__ __forceinline__ int swz_t(int k) { return (k & 3) + ((k >> 3) & 1) * 4; }
+
+  // rows [r0, r0 + ROWS) of an operand with `rows` rows
+  __device__ __forceinline__ void init(const void* p, int64_t ld, int rows, int r0, int wave, int lane) {
+    up_mask = 0;
+    up_off = 0;
+    if constexpr (!T) {
+      base = static_cast<const char*>(p) + (int64_t)r0 * ld * 2;
+      stage_step = kBK * 2;
+      const int c = (lane & 3) ^ ((lane >> 4) & 3);       // row = 16 j + lane / 4: (row / 4) % 4
+      kk = c * 8;
+#pragma unroll
+      for (int j = 0; j < LOADS; ++j) {
+        const int r = (wave * LOADS + j) * 16 + (lane >> 2);
+        off[j] = r0 + r < rows ? (uint32_t)(r * ld * 2 + c * 16) : kOut;
+      }
+    } else {
+      // ROWS * 2 bytes per k-row; a load covers 1024 bytes of them
+      base = static_cast<const char*>(p) + (int64_t)r0 * 2;
+      stage_step = (int64_t)kBK * ld * 2;
+      constexpr int CPR = ROWS / 8;                       // 16-byte chunks per k-row
+      const int slot = lane % CPR;
+      kk = (wave * LOADS) * (64 / CPR) + lane / CPR;
+#pragma unroll
+      for (int j = 0; j < LOADS; ++j) {
+        const int k = (wave * LOADS + j) * (64 / CPR) + lane / CPR;
+        const int c = slot ^ (swz_t(k) << 1);
+        off[j] = r0 + c * 8 < rows ? (uint32_t)(k * ld * 2 + c * 16) : kOut;
+      }
+    }
+  }
+  // rows of B in gate / up blocks of 32
+  __device__ __forceinline__ void init_gate(const DenseJob& p, int nt, int wave, int lane) {
+    const int I = p.N >> 1, i0 = nt * (ROWS / 2);
+    base = static_cast<const char*>(p.b) + (int64_t)i0 * p.ldb * 2 * (p.interleaved ? 2 : 1);
+    stage_step = kBK * 2;
+    up_off = p.interleaved ? p.ldb * 2 : (int64_t)I * p.ldb * 2;
+    up_mask = 0;
+    const int c = (lane & 3) ^ ((lane >> 4) & 3);
+    kk = c * 8;
+#pragma unroll
+    for (int j = 0; j < LOADS; ++j) {
+      const int r16 = wave * LOADS + j;                   // 16-row group: four per gate/up block pair
+      const int i = (r16 >> 2) * 32 + (r16 & 1) * 16 + (lane >> 2);
+      if (r16 & 2) up_mask |= 1u << j;
+      off[j] = i0 + i < I ? (uint32_t)(i * p.ldb * 2 * (p.interleaved ? 2 : 1) + c * 16) : kOut;
+    }
+  }
+  // load j of stage s into buf (this operand's part of the stage's buffer)
+  __device__ __forceinline__ void issue(int j, int s, int K, int wave, char* buf) const {
+    const char* b = base + s * stage_step + ((up_mask >> j) & 1 ? up_off : 0);
+    int k = kk;
+    if constexpr (T) k += j * (64 / (ROWS / 8));
+    const uint32_t o = k < K - s * kBK ? off[j] : kOut;
+    dma16(rsrc_at(b), o, buf + (wave * LOADS + j) * 1024);
+  }
+  // fragment of rows [r, r + 32), k [16 ks, 16 ks + 16)
+  static __device__ __forceinline__ typename Vec<E>::v8 frag(const char* buf, int r, int ks, int lane) {
+    typedef typename Vec<E>::v8 v8;
+    if constexpr (!T) {
+      const int row = r + (lane & 31), c = 2 * ks + (lane >> 5);
+      return *reinterpret_cast<const v8*>(buf + row * 64 + ((c ^ ((row >> 2) & 3)) << 4));
+    } else {
+      typedef short v4s __attribute__((ext_vector_type(4)));
+      typedef short v8s __attribute__((ext_vector_type(8)));
+      // 16-lane group q: columns 16 (q % 2), k half q / 2; lane i: k-row i / 4, columns 4 (i % 4)
+      const int i = lane & 15, q = (lane >> 4) & 1, g = lane >> 5;
+      const int k = 16 * ks + 8 * g + (i >> 2);           // second read: k + 4, same swizzle
+      const int col32 = ((r >> 4) + q) ^ swz_t(k);
+      const char* a = buf + k * (ROWS * 2) + col32 * 32 + (i & 3) * 8;
+      const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)a);
+      const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)(a + 4 * ROWS * 2));
+      const v8s both = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+      return __builtin_bit_cast(v8, both);
+    }
+  }
+};
+
+// C tile index of a block.  Consecutive blocks go round the 8 XCDs; each XCD
+// takes one contiguous run of tiles, in groups of kGroup m-tiles by all n, so
+// that the blocks that share its L2 share operand tiles.
+constexpr int kGroup = 4;
+__device__ __forceinline__ void tile_of(int b, int blocks, int mt, int nt, int* m, int* n) {
+  const int xcd = b & 7, per = blocks >> 3, more = blocks & 7;
+  const int t = xcd * per + min(xcd, more) + (b >> 3);
+  const int full = kGroup * nt, grp = t / full, in = t - grp * full;
+  const int rows = min(kGroup, mt - grp * kGroup);
+  *m = grp * kGroup + in % rows;
+  *n = in / rows;
+}
+
+template <typename E, bool TA, bool TB, int EPI, int FM, int FN>
+__global__ __launch_bounds__(256, (FM * FN > 8 ? 1 : 2)) void dense_kernel(DenseJob p) {
+  typedef typename Vec<E>::v8 v8;
+  constexpr int BM = 64 * FM, BN = 64 * FN;
+  using A = Operand<E, BM, TA>;
+  using B = Operand<E, BN, TB>;
+  constexpr int STAGE = A::BYTES + B::BYTES;
+  constexpr int STAGING = 32 * FN * 32 * 4;               // a wave's 32 rows of fp32 sums
+  static_assert(4 * STAGING <= kStages * STAGE, "the epilogue fits the stages' LDS");
+  __shared__ __attribute__((aligned(1024))) char lds[kStages * STAGE];
+
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int l32 = lane & 31, g = lane >> 5;
+  const int wm = (wave >> 1) * 32 * FM, wn = (wave & 1) * 32 * FN;
+  const int mts = (p.M + BM - 1) / BM;
+  const int cols = EPI == kEpiGate ? BN / 2 : BN, width = EPI == kEpiGate ? p.N >> 1 : p.N;
+  const int nts = (width + cols - 1) / cols;
+  int mt, nt;
+  tile_of(blockIdx.x, gridDim.x, mts, nts, &mt, &nt);
+  const int m0 = mt * BM;
+
+  A a;
+  B b;
+  a.init(p.a, p.lda, p.M, m0, wave, lane);
+  if constexpr (EPI == kEpiGate) b.init_gate(p, nt, wave, lane);
+  else b.init(p.b, p.ldb, p.N, nt * BN, wave, lane);
+  const int K = p.K, nst = (K + kBK - 1) / kBK;
+  constexpr int LOADS = A::LOADS + B::LOADS;
+  auto issue = [&](int j, int s) {
+    char* buf = lds + __builtin_amdgcn_readfirstlane((s & (kStages - 1)) * STAGE);
+    if (j < A::LOADS) a.issue(j, s, K, wave, buf);
+    else b.issue(j - A::LOADS, s, K, wave, buf + A::BYTES);
+  };
+
+  v16f acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+      for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.0f;
+
+  if (nst > 0) {
+#pragma unroll
+    for (int s = 0; s < kStages; ++s)
+#pragma unroll
+      for (int j = 0; j < LOADS; ++j) issue(j, s);
+
+    v8 fa[2][FM], fb[2][FN];
+    // fragment r of step ks of stage s
+    auto read = [&](int s, int ks, int r, v8 (&xa)[FM], v8 (&xb)[FN]) {
+      const char* buf = lds + __builtin_amdgcn_readfirstlane((s & (kStages - 1)) * STAGE);
+      if (r < FN) xb[r] = B::frag(buf + A::BYTES, wn + r * 32, ks, lane);
+      else xa[r - FN] = A::frag(buf, wm + (r - FN) * 32, ks, lane);
+    };
+    constexpr int NR = FM + FN, MF = FM * FN;
+    constexpr int RP = (NR + MF - 1) / MF;      // reads after each product
+    constexpr int DP = (LOADS + MF - 1) / MF;   // DMA instructions after each product
+    wait_vm<(kStages - 1) * LOADS>();
+    block_barrier();
+#pragma unroll
+    for (int r = 0; r < NR; ++r) read(0, 0, r, fa[0], fb[0]);
+    for (int s = 0; s < nst; ++s) {
+#pragma unroll
+      for (int i = 0; i < MF; ++i) {
+        acc[i % FM][i / FM] = mfma32(fb[0][i / FM], fa[0][i % FM], acc[i % FM][i / FM]);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int r = RP * i; r < RP * i + RP; ++r)
+          if (r < NR) read(s, 1, r, fa[1], fb[1]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      // all of stage s is in this wave's registers; its part of stage s + 1 has landed
+      wait_lgkm0();
+      wait_vm<(kStages - 2) * LOADS>();
+      block_barrier();
+#pragma unroll
+      for (int i = 0; i < MF; ++i) {
+        acc[i % FM][i / FM] = mfma32(fb[1][i / FM], fa[1][i % FM], acc[i % FM][i / FM]);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int r = RP * i; r < RP * i + RP; ++r)
+          if (r < NR) read(s + 1, 0, r, fa[0], fb[0]);
+#pragma unroll
+        for (int j = DP * i; j < DP * i + DP; ++j)
+          if (j < LOADS) issue(j, s + kStages);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    // the epilogue reuses the stages' LDS
+    wait_vm<0>();
+    block_barrier();
+  }
+
+  // ---- epilogue: 32 rows of the wave's tile at a time ----
+  char* const st = lds + wave * STAGING;
+  constexpr int PITCH = FN * 32 * 4;          // bytes of a staged row
+  constexpr int CH = PITCH / 16;              // its 16-byte chunks
+  auto finish_rows = [&](auto FMI) {
+    constexpr int fm = decltype(FMI)::value;
+    const int r0 = m0 + wm + fm * 32;
+    if (r0 >= p.M) return;
+    // each adapter present in these rows in turn: its product goes to sums of
+    // its own, which only that adapter's rows take up
+    if (EPI != kEpiGateGrad && !TB && p.ids) {
+      const int m = r0 + l32;
+      const int id = m < p.M ? p.ids[m] : -1;
+      bool open = id >= 0 && id < p.num_adapters;
+      uint64_t left = __ballot(open);
+      while (left) {
+        const int cur = __builtin_amdgcn_readlane(id, __ffsll((unsigned long long)left) - 1);
+        const bool mine = open && id == cur;
+        int rank = p.R;
+        if (p.ranks) rank = min(max(p.ranks[cur], 0), p.R);
+        const E* const sp = static_cast<const E*>(p.s) + (size_t)m * p.R;
+        const E* const lb = static_cast<const E*>(p.lb) + (size_t)cur * p.N * p.R;
+        v16f t[FN];
+#pragma unroll
+        for (int fn = 0; fn < FN; ++fn)
+#pragma unroll
+          for (int q = 0; q < 16; ++q) t[fn][q] = 0.0f;
+        for (int r = 0; r < rank; r += 16) {
+          const int k = r + 8 * g;
+          v8 sv = {}, bv[FN] = {};
+          if (mine && k < rank) sv = *reinterpret_cast<const v8*>(sp + k);
+#pragma unroll
+          for (int fn = 0; fn < FN; ++fn) {
+            int first, step, up;
+            b_block(p, nt, BN, (wn >> 5) + fn, &first, &step, &up);
+            const int i = first + l32;
+            const int row = EPI == kEpiGate ? (p.interleaved ? 2 * i + up : up * width + i) : i;
+            if (i < width && k < rank) bv[fn] = *reinterpret_cast<const v8*>(lb + (size_t)row * p.R + k);
+          }
+          if (k < rank && k + 8 > rank) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (k + e >= rank) {
+                sv[e] = (E)0.0f;
+#pragma unroll
+                for (int fn = 0; fn < FN; ++fn) bv[fn][e] = (E)0.0f;
+              }
+          }
+#pragma unroll
+          for (int fn = 0; fn < FN; ++fn) t[fn] = mfma32(bv[fn], sv, t[fn]);
+        }
+#pragma unroll
+        for (int fn = 0; fn < FN; ++fn)
+#pragma unroll
+          for (int q = 0; q < 16; ++q) acc[fm][fn][q] += mine ? t[fn][q] : 0.0f;
+        open = open && !mine;
+        left = __ballot(open);
+      }
+    }
+    // stage: lane = row l32, four columns at a time, chunks permuted by row
+#pragma unroll
+    for (int fn = 0; fn < FN; ++fn)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int c = fn * 8 + 2 * q + g;
+        *reinterpret_cast<v4f*>(st + l32 * PITCH + ((c ^ (l32 & (CH - 1))) << 4)) =
+            v4f{acc[fm][fn][4 * q], acc[fm][fn][4 * q + 1], acc[fm][fn][4 * q + 2], acc[fm][fn][4 * q + 3]};
+      }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    auto staged8 = [&](int row, int c) {
+      const v4f x = *reinterpret_cast<const v4f*>(st + row * PITCH + ((c ^ (row & (CH - 1))) << 4));
+      const v4f y = *reinterpret_cast<const v4f*>(st + row * PITCH + (((c + 1) ^ (row & (CH - 1))) << 4));
+      return F8{{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]}};
+    };
+    if constexpr (EPI == kEpiGate) {
+      constexpr int LPR = FN * 32 / 16;       // lanes per row: eight gate indices each
+#pragma unroll
+      for (int it = 0; it < 32 * LPR / 64; ++it) {
+        const int row = it * (64 / LPR) + lane / LPR, x = lane % LPR;
+        const int blk = x >> 2, c = blk * 16 + (x & 3) * 2;       // 64-column block: gate, then up
+        const int i = nt * (BN / 2) + (wn >> 1) + blk * 32 + (x & 3) * 8;
+        const F8 gt = staged8(row, c), up = staged8(row, c + 8);
+        if (r0 + row < p.M && i < width) finish_gate<E>(p, r0 + row, i, gt, up);
+      }
+    } else {
+      constexpr int LPR = FN * 32 / 8;
+#pragma unroll
+      for (int it = 0; it < 32 * LPR / 64; ++it) {
+        const int row = it * (64 / LPR) + lane / LPR, x = lane % LPR;
+        const int n = nt * BN + wn + x * 8;
+        const F8 v = staged8(row, 2 * x);
+        if (r0 + row < p.M && n < width) {
+          if constexpr (EPI == kEpiPlain) finish_plain<E>(p, r0 + row, n, v);
+          else finish_gate_grad<E>(p, r0 + row, n, v);
+        }
+      }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  };
+  // (a loop this long would not be unrolled, and the sums would leave their registers)
+  finish_rows(std::integral_constant<int, 0>());
+  finish_rows(std::integral_constant<int, 1>());
+  if constexpr (FM > 2) finish_rows(std::integral_constant<int, 2>());
+  if constexpr (FM > 3) finish_rows(std::integral_constant<int, 3>());
+}
+
+}  // namespace
+}  // namespace mxmoe
