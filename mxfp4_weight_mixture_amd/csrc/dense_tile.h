@@ -20,8 +20,8 @@
 // (the weights in the backward products, both operands of a weight
 // gradient): 32 k-rows of BM or BN values, read through the transposing LDS
 // read, which hands lane i of 16 the column i of a 4 x 16 patch; 32-byte
-// column groups are permuted by k ((k % 4) + 4 (k / 8 % 2)), which spreads the
-// eight k-rows one read touches over the banks.
+// column groups are permuted by k (^ 2 (k % 4)), so that the 2 x 4 patches'
+// rows that 32 lanes read together cover all 64 banks.
 //
 // Rows, columns and k past the end read as zeros: their lanes' offsets lie
 // behind the buffer resource's range, so no memory is touched.
@@ -57,6 +57,15 @@ __device__ __forceinline__ void block_barrier() {
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 }
+
+// Transposing LDS read: lane i of 16 gets column i of the 4 x 16 patch whose row
+// r the lanes 4 r .. 4 r + 3 address, 8 bytes each.  `restrict` gives the read
+// alias information; without any, the compiler takes it to depend on every
+// LDS DMA in flight and drains them first.
+typedef short v4s __attribute__((ext_vector_type(4)));
+typedef short v8s __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) v4s lds_v4s;
+__device__ __forceinline__ v4s read_tr(lds_v4s* __restrict__ a) { return __builtin_amdgcn_ds_read_tr16_b64_v4i16(a); }
 
 // First row of B behind tile columns [32 j, 32 j + 32) of n-tile nt, and the
 // distance of consecutive columns' rows; base is advanced for up rows.
@@ -194,7 +203,7 @@ struct Operand {
   uint32_t up_mask;      // loads that take up rows
   int kk;                // this lane's k within a stage (of its chunk, or its k-row of load 0)
 
-  static __device__ __forceinline__ int swz_t(int k) { return (k & 3) + ((k >> 3) & 1) * 4; }
+  static __device__ __forceinline__ int swz_t(int k) { return (k & 3) * 2; }
 
   // rows [r0, r0 + ROWS) of an operand with `rows` rows
   __device__ __forceinline__ void init(const void* p, int64_t ld, int rows, int r0, int wave, int lane) {
@@ -257,15 +266,12 @@ struct Operand {
       const int row = r + (lane & 31), c = 2 * ks + (lane >> 5);
       return *reinterpret_cast<const v8*>(buf + row * 64 + ((c ^ ((row >> 2) & 3)) << 4));
     } else {
-      typedef short v4s __attribute__((ext_vector_type(4)));
-      typedef short v8s __attribute__((ext_vector_type(8)));
       // 16-lane group q: columns 16 (q % 2), k half q / 2; lane i: k-row i / 4, columns 4 (i % 4)
       const int i = lane & 15, q = (lane >> 4) & 1, g = lane >> 5;
       const int k = 16 * ks + 8 * g + (i >> 2);           // second read: k + 4, same swizzle
       const int col32 = ((r >> 4) + q) ^ swz_t(k);
       const char* a = buf + k * (ROWS * 2) + col32 * 32 + (i & 3) * 8;
-      const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)a);
-      const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)(a + 4 * ROWS * 2));
+      const v4s lo = read_tr((lds_v4s*)a), hi = read_tr((lds_v4s*)(a + 4 * ROWS * 2));
       const v8s both = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
       return __builtin_bit_cast(v8, both);
     }
