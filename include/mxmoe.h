@@ -497,7 +497,8 @@ moe_status moe_gated_ffn_backward(const moe_ffn_grad_args* args, void* stream);
  * (a grouped GEMM with MXFP4 weights, say) through `add`.
  * A token's result depends on its own row and adapter only: infinities or NaN
  * in one adapter or token do not reach the others.
- * The low-rank row scales[a] * x A^T is rounded once to `dtype`.
+ * The low-rank row scales[a] * x A^T is held in fp32 and enters the second
+ * product as the sum of two numbers of type `dtype`.
  *
  * Sizes: T >= 0 (T == 0 enqueues nothing), K, N multiples of 8 in [8, 262144],
  * N % 16 == 0 for SWIGLU; 0 <= num_adapters <= 65536; R a multiple of 8 in

@@ -2,9 +2,8 @@
 //
 //   y[t] = (add[t] +) x[t] W^T + s[t] B[a]^T,  s[t] = scales[a] x[t] A[a]^T,
 //   a = ids[t] (none outside [0, num_adapters))
-// Two launches: the first gives s [T][R] (rounded to the operands' type, as
-// the second product's matrix-core operand), the second the shared projection
-// with s B^T added to its fp32 sums and the epilogue.
+// Two launches: the first gives s [T][R] in fp32, the second the shared
+// projection with s B^T added to its fp32 sums and the epilogue.
 #include "dense.h"
 
 namespace mxmoe {
@@ -12,7 +11,7 @@ namespace {
 
 // One wave per (token, row of A): 64 lanes stride over K.
 template <typename E>
-__global__ __launch_bounds__(256) void shrink_kernel(moe_adapter_args p, E* s) {
+__global__ __launch_bounds__(256) void shrink_kernel(moe_adapter_args p, float* s) {
   typedef typename Vec<E>::v8 v8;
   const int lane = threadIdx.x & 63;
   const int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
@@ -29,15 +28,15 @@ __global__ __launch_bounds__(256) void shrink_kernel(moe_adapter_args p, E* s) {
     for (int i = 0; i < 8; ++i) sum += (float)xv[i] * (float)av[i];
   }
   for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d);
-  if (lane == 0) s[(size_t)t * p.R + r] = (E)(p.scales ? sum * p.scales[id] : sum);
+  if (lane == 0) s[(size_t)t * p.R + r] = p.scales ? sum * p.scales[id] : sum;
 }
 
 moe_status launch_shrink(const moe_adapter_args& a, void* s, hipStream_t st) {
   const dim3 grid((unsigned)(((int64_t)a.T * a.R + 3) / 4));
   if (a.dtype == MOE_FLOAT_BF16)
-    hipLaunchKernelGGL((shrink_kernel<__bf16>), grid, dim3(256), 0, st, a, static_cast<__bf16*>(s));
+    hipLaunchKernelGGL((shrink_kernel<__bf16>), grid, dim3(256), 0, st, a, static_cast<float*>(s));
   else
-    hipLaunchKernelGGL((shrink_kernel<_Float16>), grid, dim3(256), 0, st, a, static_cast<_Float16*>(s));
+    hipLaunchKernelGGL((shrink_kernel<_Float16>), grid, dim3(256), 0, st, a, static_cast<float*>(s));
   MXMOE_HIP(hipGetLastError());
   return MOE_OK;
 }
@@ -48,7 +47,7 @@ struct AdapterWs {
 AdapterWs adapter_ws(int T, int K, int N, int R) {
   AdapterWs w;
   w.s = 0;
-  w.gemm = align_up((size_t)T * R * 2, 256);
+  w.gemm = align_up((size_t)T * R * 4, 256);
   w.total = w.gemm + dense_ws_bytes(T, N, K) + 256;
   return w;
 }
@@ -130,7 +129,7 @@ moe_status moe_adapter_linear(const moe_adapter_args* a, void* stream) {
   if (n > 0) {
     MXMOE_TRY(launch_shrink(*a, ws + w.s, s));
     j.ids = a->ids, j.ranks = a->ranks;
-    j.s = ws + w.s, j.lb = a->b;
+    j.s = reinterpret_cast<const float*>(ws + w.s), j.lb = a->b;
     j.num_adapters = a->num_adapters, j.R = a->R;
   }
   return launch_dense(j, ws + w.gemm, s);

@@ -31,7 +31,7 @@ struct DenseJob {
   // adapters (null ids: none): += s[m] * lb[ids[m]][n], over R terms
   const int32_t* ids;
   const int32_t* ranks;
-  const void* s;            // [M][R], `dtype`
+  const float* s;           // [M][R]
   const void* lb;           // [num_adapters][N][R]
   int num_adapters, R;
 };
@@ -153,22 +153,16 @@ __device__ __forceinline__ void gate_act_grad(int act, float g, float* a, float*
   }
 }
 
-// Four consecutive values of a row; dtype is uniform.
+// x = hi + lo in two 16-bit numbers: 16 (bf16) or 22 (fp16) bits of it.  An
+// overflowing hi stays infinite.
 template <typename E>
-__device__ __forceinline__ v4f load4(const void* base, int dtype, size_t i) {
-  if (dtype == MOE_FLOAT_FP32) return *reinterpret_cast<const v4f*>(static_cast<const float*>(base) + i);
-  const typename Vec<E>::v4 v = *reinterpret_cast<const typename Vec<E>::v4*>(static_cast<const E*>(base) + i);
-  return v4f{(float)v[0], (float)v[1], (float)v[2], (float)v[3]};
+__device__ __forceinline__ void split16(float x, E* hi, E* lo) {
+  const E h = (E)x;
+  const float d = x - (float)h;
+  *hi = h;
+  *lo = (E)(fabsf(d) < 3e38f ? d : 0.0f);
 }
-template <typename E>
-__device__ __forceinline__ void store4(void* base, int dtype, size_t i, v4f v) {
-  if (dtype == MOE_FLOAT_FP32) {
-    *reinterpret_cast<v4f*>(static_cast<float*>(base) + i) = v;
-  } else {
-    typename Vec<E>::v4 o = {(E)v[0], (E)v[1], (E)v[2], (E)v[3]};
-    *reinterpret_cast<typename Vec<E>::v4*>(static_cast<E*>(base) + i) = o;
-  }
-}
+
 #endif
 
 }  // namespace mxmoe

@@ -1,4 +1,5 @@
 // Dense products with 16-bit operands: choice of kernel and launch.
+#include "dense_few.h"
 #include "dense_tile.h"
 
 namespace mxmoe {
@@ -25,8 +26,23 @@ moe_status launch_tile_kernel(const DenseJob& j, hipStream_t s) {
   return MOE_OK;
 }
 
+template <typename E, int MB>
+moe_status launch_few(const DenseJob& j, hipStream_t s) {
+  const dim3 block(64 * kFewWaves);
+  if (j.epi == kEpiGate)
+    hipLaunchKernelGGL((few_kernel<E, MB, kEpiGate>), dim3(j.N / 16), block, 0, s, j);
+  else
+    hipLaunchKernelGGL((few_kernel<E, MB, kEpiPlain>), dim3((j.N + 15) / 16), block, 0, s, j);
+  MXMOE_HIP(hipGetLastError());
+  return MOE_OK;
+}
+
 template <typename E>
 moe_status launch_typed(const DenseJob& j, void* ws, hipStream_t s) {
+  if (j.M <= 64 && j.epi != kEpiGateGrad && !j.ta && !j.tb) {
+    if (j.M <= 16) return launch_few<E, 1>(j, s);
+    return j.M <= 32 ? launch_few<E, 2>(j, s) : launch_few<E, 4>(j, s);
+  }
   const int64_t big = (int64_t)((j.M + 255) / 256) * ((j.N + 255) / 256);
   if (big >= 200) return launch_tile_kernel<E, 4, 4>(j, s);
   return launch_tile_kernel<E, 2, 2>(j, s);
