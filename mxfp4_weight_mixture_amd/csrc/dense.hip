@@ -26,22 +26,28 @@ moe_status launch_tile_kernel(const DenseJob& j, hipStream_t s) {
   return MOE_OK;
 }
 
-template <typename E, int MB>
+template <typename E, int MB, int NB, bool XLDS, int D>
 moe_status launch_few(const DenseJob& j, hipStream_t s) {
-  const dim3 block(64 * kFewWaves);
+  const dim3 grid((j.N + 16 * NB - 1) / (16 * NB)), block(64 * kFewWaves);
   if (j.epi == kEpiGate)
-    hipLaunchKernelGGL((few_kernel<E, MB, kEpiGate>), dim3(j.N / 16), block, 0, s, j);
+    hipLaunchKernelGGL((few_kernel<E, MB, NB, kEpiGate, XLDS, D>), grid, block, 0, s, j);
   else
-    hipLaunchKernelGGL((few_kernel<E, MB, kEpiPlain>), dim3((j.N + 15) / 16), block, 0, s, j);
+    hipLaunchKernelGGL((few_kernel<E, MB, NB, kEpiPlain, XLDS, D>), grid, block, 0, s, j);
   MXMOE_HIP(hipGetLastError());
   return MOE_OK;
 }
 
 template <typename E>
 moe_status launch_typed(const DenseJob& j, void* ws, hipStream_t s) {
-  if (j.M <= 64 && j.epi != kEpiGateGrad && !j.ta && !j.tb) {
-    if (j.M <= 16) return launch_few<E, 1>(j, s);
-    return j.M <= 32 ? launch_few<E, 2>(j, s) : launch_few<E, 4>(j, s);
+  // (the few-row kernel addresses a block's rows with 31 bits from the first;
+  // a split gate's up rows lie I rows behind)
+  const int64_t reach = j.epi == kEpiGate ? (int64_t)(j.N / 2 + 16) * j.ldb * 2 : 0;
+  if (j.M <= 64 && j.epi != kEpiGateGrad && !j.ta && !j.tb && reach < (1ll << 30)) {
+    const bool wide = (j.N + 15) / 16 > num_cus();
+    if (j.M <= 4) return launch_few<E, 1, 1, false, 4>(j, s);
+    if (j.M <= 16) return wide ? launch_few<E, 1, 2, true, 4>(j, s) : launch_few<E, 1, 1, true, 4>(j, s);
+    if (j.M <= 32) return wide ? launch_few<E, 2, 2, true, 4>(j, s) : launch_few<E, 2, 1, true, 4>(j, s);
+    return wide ? launch_few<E, 4, 2, true, 2>(j, s) : launch_few<E, 4, 1, true, 2>(j, s);
   }
   const int64_t big = (int64_t)((j.M + 255) / 256) * ((j.N + 255) / 256);
   if (big >= 200) return launch_tile_kernel<E, 4, 4>(j, s);

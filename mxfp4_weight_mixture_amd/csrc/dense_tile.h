@@ -29,6 +29,7 @@
 
 #include <type_traits>
 
+#include "dense_dma.h"
 #include "dense_rows.h"
 
 namespace mxmoe {
@@ -36,28 +37,6 @@ namespace {
 
 constexpr int kBK = 32;          // k per stage
 constexpr int kStages = 4;
-constexpr uint32_t kOut = 0x80000000u;   // an offset behind every resource's range
-
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_at(const void* base) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, 0x7fffffff, 0x00020000);
-}
-// 16 bytes per lane, global -> LDS (lane i writes dst + 16 i)
-__device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t r, uint32_t voff, void* dst) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)dst, 16, voff, 0, 0, 0);
-}
-template <int N>
-__device__ __forceinline__ void wait_vm() {
-  static_assert(N >= 0 && N < 64, "vmcnt range");
-  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
-}
-__device__ __forceinline__ void wait_lgkm0() { __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4)); }
-__device__ __forceinline__ void block_barrier() {
-  asm volatile("" ::: "memory");
-  wait_lgkm0();
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-}
-
 // Transposing LDS read: lane i of 16 gets column i of the 4 x 16 patch whose row
 // r the lanes 4 r .. 4 r + 3 address, 8 bytes each.  `restrict` gives the read
 // alias information; without any, the compiler takes it to depend on every
