@@ -36,6 +36,11 @@ struct DenseJob {
   int num_adapters, R;
 };
 
+// Token counts up to this are decode batches: their adapters differ from token
+// to token.  (By size, not by what the ids hold: a row's result does not depend
+// on its neighbours'.)
+constexpr int kFewTokens = 256;
+
 size_t dense_ws_bytes(int M, int N, int K);
 moe_status launch_dense(const DenseJob& j, void* ws, hipStream_t s);
 

@@ -15,6 +15,12 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_at(const void* base) {
 __device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t r, uint32_t voff, void* dst) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)dst, 16, voff, 0, 0, 0);
 }
+// 16 bytes per lane to registers
+template <typename E>
+__device__ __forceinline__ typename Vec<E>::v8 load16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+  return __builtin_bit_cast(typename Vec<E>::v8, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+}
+
 // LDS read beside DMA in flight.  `restrict` gives it alias information; without
 // any, the compiler may take it to depend on every LDS DMA and drain them first.
 template <typename V>

@@ -29,11 +29,6 @@ namespace {
 
 constexpr int kFewWaves = 8;
 
-template <typename E>
-__device__ __forceinline__ typename Vec<E>::v8 load16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
-  return __builtin_bit_cast(typename Vec<E>::v8, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
-}
-
 template <typename E, int MB, int NB, int EPI, bool XLDS, int D>
 __global__ __launch_bounds__(64 * kFewWaves) void few_kernel(DenseJob p) {
   typedef typename Vec<E>::v8 v8;
