@@ -1,0 +1,179 @@
+// The dense kernel for small products: 64 x 64 tiles, four waves that split K.
+//
+// Where few tiles exist a block's time is the latency of its K loop, and
+// barriers between short stages are most of it.  Here no wave waits for
+// another before the end: wave w takes the 32-deep stages w, w + 4, ..., with a
+// DMA ring of its own, and holds the whole 64 x 64 tile (2 x 2 fragments of
+// 32x32x16); the four sums meet in the LDS.  Bound by the L2 -> LDS rate, 8 KB
+// per stage at about 50 bytes a clock and CU: 164 clocks, against 64 of matrix
+// work.
+//
+// Adapters: each thread adds its row's low-rank product to its eight columns,
+// so mixed adapters cost no more than equal ones.
+#pragma once
+
+#include "dense_tile.h"
+
+namespace mxmoe {
+namespace {
+
+// sum over r of s[r] B[row][r] for eight rows of B, `step` rows apart
+template <typename E>
+__device__ __forceinline__ void add_low_rank(F8& v, const float* s, const E* lb, int64_t step, int rank) {
+  typedef typename Vec<E>::v8 v8;
+  for (int r = 0; r < rank; r += 8) {
+    F8 sv = load8<E>(s, MOE_FLOAT_FP32, r);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      const v8 b = *reinterpret_cast<const v8*>(lb + c * step + r);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (r + e < rank) v.v[c] += sv.v[e] * (float)b[e];
+    }
+  }
+}
+
+template <typename E, bool TA, bool TB, int EPI, int NST>
+__global__ __launch_bounds__(256, 1) void small_kernel(DenseJob p) {
+  typedef typename Vec<E>::v8 v8;
+  using A = Operand<E, 64, TA, 1>;
+  using B = Operand<E, 64, TB, 1>;
+  constexpr int STAGE = A::BYTES + B::BYTES, LOADS = A::LOADS + B::LOADS;
+  constexpr int TILE = 64 * 64 * 4, RING = NST * STAGE > TILE ? NST * STAGE : TILE;
+  __shared__ __attribute__((aligned(1024))) char lds[4 * RING];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int l32 = lane & 31, g = lane >> 5;
+  const int cols = EPI == kEpiGate ? 32 : 64, width = EPI == kEpiGate ? p.N >> 1 : p.N;
+  int mt, nt;
+  tile_of(blockIdx.x, gridDim.x, (p.M + 63) >> 6, (width + cols - 1) / cols, &mt, &nt);
+  const int m0 = mt * 64, n0 = nt * cols;
+
+  A a;
+  B b;
+  a.init(p.a, p.lda, p.M, m0, 0, lane);
+  if constexpr (EPI == kEpiGate) b.init_gate(p, nt, 0, lane);
+  else b.init(p.b, p.ldb, p.N, n0, 0, lane);
+  const int K = p.K, turns = ((K + kBK - 1) / kBK - wave + 3) >> 2;
+  char* const ring = lds + wave * RING;
+  auto issue = [&](int t, int buf) {
+    const int s = wave + 4 * t;
+#pragma unroll
+    for (int j = 0; j < A::LOADS; ++j) a.issue(j, s, K, 0, ring + buf * STAGE);
+#pragma unroll
+    for (int j = 0; j < B::LOADS; ++j) b.issue(j, s, K, 0, ring + buf * STAGE + A::BYTES);
+  };
+  v8 fa[2][2][2], fb[2][2][2];   // [turn parity][k step][fragment]
+  auto read = [&](int buf, int d) {
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+      for (int f = 0; f < 2; ++f) {
+        fa[d][ks][f] = A::frag(ring + buf * STAGE, f * 32, ks, lane);
+        fb[d][ks][f] = B::frag(ring + buf * STAGE + A::BYTES, f * 32, ks, lane);
+      }
+  };
+  v16f acc[2][2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int q = 0; q < 16; ++q) acc[i >> 1][i & 1][q] = 0.0f;
+#pragma unroll
+  for (int t = 0; t < NST; ++t) issue(t, t);
+  wait_vm<(NST - 1) * LOADS>();
+  __builtin_amdgcn_sched_barrier(0);
+  read(0, 0);
+  // NST turns per step without a way out: turns past the end read zeros
+  for (int t0 = 0; t0 < turns; t0 += NST) {
+#pragma unroll
+    for (int u = 0; u < NST; ++u) {
+      // this turn is in registers: its buffer takes turn t + NST, and the next
+      // turn, which has landed, is read beside the products
+      wait_lgkm0();
+      __builtin_amdgcn_sched_barrier(0);
+      issue(t0 + u + NST, u);
+      wait_vm<(NST - 1) * LOADS>();
+      __builtin_amdgcn_sched_barrier(0);
+      read((u + 1) % NST, (u + 1) & 1);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+        for (int f = 0; f < 4; ++f)
+          acc[f & 1][f >> 1] = mfma32(fb[u & 1][ks][f >> 1], fa[u & 1][ks][f & 1], acc[f & 1][f >> 1]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+  wait_vm<0>();
+  wait_lgkm0();
+  __builtin_amdgcn_sched_barrier(0);
+  // stage this wave's sums over its ring: lane = row, 16-byte chunks permuted by row
+#pragma unroll
+  for (int fm = 0; fm < 2; ++fm)
+#pragma unroll
+    for (int fn = 0; fn < 2; ++fn)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int row = fm * 32 + l32, c = fn * 8 + 2 * q + g;
+        *reinterpret_cast<v4f*>(ring + row * 256 + ((c ^ (row & 15)) << 4)) =
+            v4f{acc[fm][fn][4 * q], acc[fm][fn][4 * q + 1], acc[fm][fn][4 * q + 2], acc[fm][fn][4 * q + 3]};
+      }
+  __syncthreads();
+  auto sum8 = [&](int row, int c) {
+    F8 r;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const char* base = lds + w * RING + row * 256;
+      const v4f x = *reinterpret_cast<const v4f*>(base + ((c ^ (row & 15)) << 4));
+      const v4f y = *reinterpret_cast<const v4f*>(base + (((c + 1) ^ (row & 15)) << 4));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        r.v[e] = w ? r.v[e] + x[e] : x[e];
+        r.v[4 + e] = w ? r.v[4 + e] + y[e] : y[e];
+      }
+    }
+    return r;
+  };
+  // an adapter's rank, 0 for none
+  auto rank_of = [&](int id) {
+    if (id < 0 || id >= p.num_adapters) return 0;
+    return p.ranks ? min(max(p.ranks[id], 0), p.R) : p.R;
+  };
+  if constexpr (EPI == kEpiGate) {
+    const int row = threadIdx.x >> 2, x = threadIdx.x & 3, m = m0 + row, i = n0 + x * 8;
+    if (m < p.M && i < width) {
+      F8 gt = sum8(row, 2 * x), up = sum8(row, 8 + 2 * x);
+      if (p.ids) {
+        const int id = p.ids[m], rank = rank_of(id);
+        if (rank > 0) {
+          const float* s = p.s + (size_t)m * p.R;
+          const E* lb = static_cast<const E*>(p.lb) + ((size_t)id * p.N + (p.interleaved ? 2 * i : i)) * p.R;
+          const int64_t step = p.interleaved ? 2 * p.R : p.R;
+          add_low_rank<E>(gt, s, lb, step, rank);
+          add_low_rank<E>(up, s, lb + (p.interleaved ? p.R : (int64_t)width * p.R), step, rank);
+        }
+      }
+      finish_gate<E>(p, m, i, gt, up);
+    }
+  } else {
+#pragma unroll
+    for (int it = 0; it < 2; ++it) {
+      const int row = it * 32 + (threadIdx.x >> 3), x = threadIdx.x & 7, m = m0 + row, n = n0 + x * 8;
+      if (m >= p.M || n >= width) continue;
+      F8 v = sum8(row, 2 * x);
+      if constexpr (EPI == kEpiGateGrad) {
+        finish_gate_grad<E>(p, m, n, v);
+      } else {
+        if (!TB && p.ids) {
+          const int id = p.ids[m], rank = rank_of(id);
+          if (rank > 0)
+            add_low_rank<E>(v, p.s + (size_t)m * p.R, static_cast<const E*>(p.lb) + ((size_t)id * p.N + n) * p.R, p.R,
+                            rank);
+        }
+        finish_plain<E>(p, m, n, v);
+      }
+    }
+  }
+}
+
+}  // namespace
+}  // namespace mxmoe

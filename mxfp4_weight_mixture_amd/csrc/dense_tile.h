@@ -9,9 +9,9 @@
 // read one 16-deep step ahead of their products.
 //
 // Tiles move global -> LDS without passing registers (buffer loads to LDS, 16
-// bytes a lane) in stages of 32 k, through a ring of kStages buffers.  In
+// bytes a lane) in stages of 32 k, through a ring of NST buffers.  In
 // stage s the block meets once, between its two 16-deep steps: by then every
-// wave has read all of stage s, so stage s + kStages may overwrite it, and
+// wave has read all of stage s, so stage s + NST may overwrite it, and
 // every wave's part of stage s + 1 has landed.
 //
 // LDS layout of a stage.  An operand stored [rows][K]: 64 bytes per row, its
@@ -36,7 +36,6 @@ namespace mxmoe {
 namespace {
 
 constexpr int kBK = 32;          // k per stage
-constexpr int kStages = 4;
 // Transposing LDS read: lane i of 16 gets column i of the 4 x 16 patch whose row
 // r the lanes 4 r .. 4 r + 3 address, 8 bytes each.  `restrict` gives the read
 // alias information; without any, the compiler takes it to depend on every
@@ -59,12 +58,12 @@ __device__ __forceinline__ void b_block(const DenseJob& p, int nt, int bn, int j
 }
 
 // One operand's way from memory to the products: DMA of a stage, fragment reads.
-// ROWS: rows of the tile; T: stored [K][rows].
-template <typename E, int ROWS, bool T>
+// ROWS: rows of the tile; T: stored [K][rows]; PARTS: waves that share a stage's loads.
+template <typename E, int ROWS, bool T, int PARTS>
 struct Operand {
   static constexpr int BYTES = ROWS * kBK * 2;            // of a stage
-  static constexpr int LOADS = BYTES / 1024 / 4;          // DMA instructions per wave
-  static_assert(LOADS >= 1, "at least 64 rows");
+  static constexpr int LOADS = BYTES / 1024 / PARTS;      // DMA instructions per wave
+  static_assert(LOADS >= 1, "at least 16 rows per wave");
   const char* base;      // of the tile's first row (or column), k = 0
   int64_t stage_step;    // bytes from stage to stage
   uint32_t off[LOADS];
@@ -72,7 +71,7 @@ struct Operand {
   uint32_t up_mask;      // loads that take up rows
   int kk;                // this lane's k within a stage (of its chunk, or its k-row of load 0)
 
-  static __device__ __forceinline__ int swz_t(int k) { return (k & 3) * 2; }
+  static __device__ __forceinline__ int swz_t(int k) { return ((k & 3) * 2) & (ROWS / 16 - 1); }
 
   // rows [r0, r0 + ROWS) of an operand with `rows` rows
   __device__ __forceinline__ void init(const void* p, int64_t ld, int rows, int r0, int wave, int lane) {
@@ -160,16 +159,16 @@ __device__ __forceinline__ void tile_of(int b, int blocks, int mt, int nt, int* 
   *n = in / rows;
 }
 
-template <typename E, bool TA, bool TB, int EPI, int FM, int FN>
-__global__ __launch_bounds__(256, (FM * FN > 8 ? 1 : 2)) void dense_kernel(DenseJob p) {
+template <typename E, bool TA, bool TB, int EPI, int FM, int FN, int NST>
+__global__ __launch_bounds__(256, 1) void dense_kernel(DenseJob p) {
   typedef typename Vec<E>::v8 v8;
   constexpr int BM = 64 * FM, BN = 64 * FN;
-  using A = Operand<E, BM, TA>;
-  using B = Operand<E, BN, TB>;
+  using A = Operand<E, BM, TA, 4>;
+  using B = Operand<E, BN, TB, 4>;
   constexpr int STAGE = A::BYTES + B::BYTES;
   constexpr int STAGING = 32 * FN * 32 * 4;               // a wave's 32 rows of fp32 sums
-  static_assert(4 * STAGING <= kStages * STAGE, "the epilogue fits the stages' LDS");
-  __shared__ __attribute__((aligned(1024))) char lds[kStages * STAGE];
+  static_assert(4 * STAGING <= NST * STAGE, "the epilogue fits the stages' LDS");
+  __shared__ __attribute__((aligned(1024))) char lds[NST * STAGE];
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l32 = lane & 31, g = lane >> 5;
@@ -189,7 +188,7 @@ __global__ __launch_bounds__(256, (FM * FN > 8 ? 1 : 2)) void dense_kernel(Dense
   const int K = p.K, nst = (K + kBK - 1) / kBK;
   constexpr int LOADS = A::LOADS + B::LOADS;
   auto issue = [&](int j, int s) {
-    char* buf = lds + __builtin_amdgcn_readfirstlane((s & (kStages - 1)) * STAGE);
+    char* buf = lds + __builtin_amdgcn_readfirstlane((s & (NST - 1)) * STAGE);
     if (j < A::LOADS) a.issue(j, s, K, wave, buf);
     else b.issue(j - A::LOADS, s, K, wave, buf + A::BYTES);
   };
@@ -204,21 +203,21 @@ __global__ __launch_bounds__(256, (FM * FN > 8 ? 1 : 2)) void dense_kernel(Dense
 
   if (nst > 0) {
 #pragma unroll
-    for (int s = 0; s < kStages; ++s)
+    for (int s = 0; s < NST; ++s)
 #pragma unroll
       for (int j = 0; j < LOADS; ++j) issue(j, s);
 
     v8 fa[2][FM], fb[2][FN];
     // fragment r of step ks of stage s
     auto read = [&](int s, int ks, int r, v8 (&xa)[FM], v8 (&xb)[FN]) {
-      const char* buf = lds + __builtin_amdgcn_readfirstlane((s & (kStages - 1)) * STAGE);
+      const char* buf = lds + __builtin_amdgcn_readfirstlane((s & (NST - 1)) * STAGE);
       if (r < FN) xb[r] = B::frag(buf + A::BYTES, wn + r * 32, ks, lane);
       else xa[r - FN] = A::frag(buf, wm + (r - FN) * 32, ks, lane);
     };
     constexpr int NR = FM + FN, MF = FM * FN;
     constexpr int RP = (NR + MF - 1) / MF;      // reads after each product
     constexpr int DP = (LOADS + MF - 1) / MF;   // DMA instructions after each product
-    wait_vm<(kStages - 1) * LOADS>();
+    wait_vm<(NST - 1) * LOADS>();
     block_barrier();
 #pragma unroll
     for (int r = 0; r < NR; ++r) read(0, 0, r, fa[0], fb[0]);
@@ -234,7 +233,7 @@ __global__ __launch_bounds__(256, (FM * FN > 8 ? 1 : 2)) void dense_kernel(Dense
       }
       // all of stage s is in this wave's registers; its part of stage s + 1 has landed
       wait_lgkm0();
-      wait_vm<(kStages - 2) * LOADS>();
+      wait_vm<(NST - 2) * LOADS>();
       block_barrier();
 #pragma unroll
       for (int i = 0; i < MF; ++i) {
@@ -245,7 +244,7 @@ __global__ __launch_bounds__(256, (FM * FN > 8 ? 1 : 2)) void dense_kernel(Dense
           if (r < NR) read(s + 1, 0, r, fa[0], fb[0]);
 #pragma unroll
         for (int j = DP * i; j < DP * i + DP; ++j)
-          if (j < LOADS) issue(j, s + kStages);
+          if (j < LOADS) issue(j, s + NST);
         __builtin_amdgcn_sched_barrier(0);
       }
     }
@@ -365,7 +364,7 @@ __global__ __launch_bounds__(256, (FM * FN > 8 ? 1 : 2)) void dense_kernel(Dense
   };
   // (a loop this long would not be unrolled, and the sums would leave their registers)
   finish_rows(std::integral_constant<int, 0>());
-  finish_rows(std::integral_constant<int, 1>());
+  if constexpr (FM > 1) finish_rows(std::integral_constant<int, 1>());
   if constexpr (FM > 2) finish_rows(std::integral_constant<int, 2>());
   if constexpr (FM > 3) finish_rows(std::integral_constant<int, 3>());
 }
