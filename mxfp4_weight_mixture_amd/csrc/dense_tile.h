@@ -187,6 +187,7 @@ __global__ __launch_bounds__(256, 1) void dense_kernel(DenseJob p) {
   else b.init(p.b, p.ldb, p.N, nt * BN, wave, lane);
   const int K = p.K, nst = (K + kBK - 1) / kBK;
   constexpr int LOADS = A::LOADS + B::LOADS;
+  constexpr int EARLY = LOADS / 2;   // of them, issued half a stage before the rest
   auto issue = [&](int j, int s) {
     char* buf = lds + __builtin_amdgcn_readfirstlane((s & (NST - 1)) * STAGE);
     if (j < A::LOADS) a.issue(j, s, K, wave, buf);
@@ -205,7 +206,7 @@ __global__ __launch_bounds__(256, 1) void dense_kernel(DenseJob p) {
 #pragma unroll
     for (int s = 0; s < NST; ++s)
 #pragma unroll
-      for (int j = 0; j < LOADS; ++j) issue(j, s);
+      for (int j = 0; j < (s + 1 < NST ? LOADS : EARLY); ++j) issue(j, s);
 
     v8 fa[2][FM], fb[2][FN];
     // fragment r of step ks of stage s
@@ -216,8 +217,14 @@ __global__ __launch_bounds__(256, 1) void dense_kernel(DenseJob p) {
     };
     constexpr int NR = FM + FN, MF = FM * FN;
     constexpr int RP = (NR + MF - 1) / MF;      // reads after each product
-    constexpr int DP = (LOADS + MF - 1) / MF;   // DMA instructions after each product
-    wait_vm<(NST - 1) * LOADS>();
+    // the DMA of a stage is spread over a whole stage's products: issued in a
+    // lump, it takes longer to accept (20 clocks per KB) than the products last
+    auto spread = [&](int i, int j0, int j1, int s) {
+#pragma unroll
+      for (int j = j0; j < j1; ++j)
+        if ((j - j0) * MF / (j1 - j0) == i) issue(j, s);
+    };
+    wait_vm<(NST - 2) * LOADS + EARLY>();
     block_barrier();
 #pragma unroll
     for (int r = 0; r < NR; ++r) read(0, 0, r, fa[0], fb[0]);
@@ -229,6 +236,7 @@ __global__ __launch_bounds__(256, 1) void dense_kernel(DenseJob p) {
 #pragma unroll
         for (int r = RP * i; r < RP * i + RP; ++r)
           if (r < NR) read(s, 1, r, fa[1], fb[1]);
+        spread(i, EARLY, LOADS, s + NST - 1);
         __builtin_amdgcn_sched_barrier(0);
       }
       // all of stage s is in this wave's registers; its part of stage s + 1 has landed
@@ -242,9 +250,7 @@ __global__ __launch_bounds__(256, 1) void dense_kernel(DenseJob p) {
 #pragma unroll
         for (int r = RP * i; r < RP * i + RP; ++r)
           if (r < NR) read(s + 1, 0, r, fa[0], fb[0]);
-#pragma unroll
-        for (int j = DP * i; j < DP * i + DP; ++j)
-          if (j < LOADS) issue(j, s + NST);
+        spread(i, 0, EARLY, s + NST);
         __builtin_amdgcn_sched_barrier(0);
       }
     }
