@@ -19,20 +19,35 @@ int64_t tiles(const DenseJob& j, int bm, int bn) {
   else if (j.tb) LAUNCH(false, true, kEpiPlain);              \
   else LAUNCH(false, false, kEpiPlain)
 
-template <typename E, int FM, int FN, int NST>
-moe_status launch_tile_kernel(const DenseJob& j, hipStream_t s) {
-  const dim3 grid((unsigned)tiles(j, 64 * FM, 64 * FN)), block(256);
-#define MXMOE_LAUNCH(TA, TB, EPI) hipLaunchKernelGGL((dense_kernel<E, TA, TB, EPI, FM, FN, NST>), grid, block, 0, s, j)
+// Whole 256 x 256 tiles in full rounds of the CUs, the rest whole or in parts.
+struct TilePlan {
+  int64_t full, rest, parts;
+};
+TilePlan plan_tiles(const DenseJob& j, int cus) {
+  TilePlan t;
+  const int64_t n = tiles(j, 256, 256);
+  t.full = n / cus * cus;
+  t.rest = n - t.full;
+  t.parts = 4 * t.rest <= cus ? 4 : 2 * t.rest <= cus ? 2 : 1;
+  return t;
+}
+
+template <typename E>
+moe_status launch_tiles(const DenseJob& j, hipStream_t s) {
+  const TilePlan t = plan_tiles(j, num_cus() / 8 * 8);
+  const dim3 grid((unsigned)(t.full + t.rest * t.parts)), block(256);
+#define MXMOE_LAUNCH(TA, TB, EPI) \
+  hipLaunchKernelGGL((tile_kernel<E, TA, TB, EPI>), grid, block, 0, s, j, (int)t.full, (int)t.rest, (int)t.parts)
   MXMOE_DENSE_FORMS(MXMOE_LAUNCH);
 #undef MXMOE_LAUNCH
   MXMOE_HIP(hipGetLastError());
   return MOE_OK;
 }
 
-template <typename E, int NST>
+template <typename E>
 moe_status launch_small(const DenseJob& j, hipStream_t s) {
   const dim3 grid((unsigned)tiles(j, 64, 64)), block(256);
-#define MXMOE_LAUNCH(TA, TB, EPI) hipLaunchKernelGGL((small_kernel<E, TA, TB, EPI, NST>), grid, block, 0, s, j)
+#define MXMOE_LAUNCH(TA, TB, EPI) hipLaunchKernelGGL((small_kernel<E, TA, TB, EPI>), grid, block, 0, s, j)
   MXMOE_DENSE_FORMS(MXMOE_LAUNCH);
 #undef MXMOE_LAUNCH
   MXMOE_HIP(hipGetLastError());
@@ -50,13 +65,20 @@ moe_status launch_few(const DenseJob& j, hipStream_t s) {
   return MOE_OK;
 }
 
-int choose_tile(const DenseJob& j) {
-#ifdef FORCE_TILE
-  return g_force;
-#endif
-  if (j.ids && j.M <= kFewTokens) return 0;
-  if (tiles(j, 256, 256) >= 200) return 2;
-  return tiles(j, 128, 128) >= 200 ? 1 : 0;
+// Whether 64 x 64 tiles are expected to take less time.  In microseconds per
+// 32-deep stage, measured on a filled chip: 0.84 a round of whole 256 x 256
+// tiles, 0.55 of halves, 0.28 of quarters; 0.22 a round of 64 x 64 tiles, two
+// per CU, 0.11 of up to one per CU.  About 4 a round for its ends.
+bool small_is_faster(const DenseJob& j) {
+  const int cus = num_cus() / 8 * 8;
+  const double stages = (j.K + 31) / 32;
+  const TilePlan t = plan_tiles(j, cus);
+  const double tail = t.rest == 0 ? 0.0 : t.parts == 4 ? stages * 0.28 + 4 : t.parts == 2 ? stages * 0.55 + 4
+                                                                                         : stages * 0.84 + 4;
+  const double big = (double)(t.full / cus) * (stages * 0.84 + 4) + tail;
+  const int64_t n = tiles(j, 64, 64);
+  const double small = n <= cus ? stages * 0.11 + 4 : (double)((n + 2 * cus - 1) / (2 * cus)) * (stages * 0.22 + 4);
+  return small < big;
 }
 
 template <typename E>
@@ -73,11 +95,12 @@ moe_status launch_typed(const DenseJob& j, void* ws, hipStream_t s) {
   }
   if (tiles(j, 64, 64) > 0x7fffffff)
     return fail(MOE_ERR_SHAPE, "dense product: %d x %d is too large for one launch", j.M, j.N);
-  switch (choose_tile(j)) {
-    case 0: return launch_small<E, 4>(j, s);
-    case 1: return launch_tile_kernel<E, 2, 2, 8>(j, s);
-    default: return launch_tile_kernel<E, 4, 4, 4>(j, s);
-  }
+  // (a decode batch's mixed adapters are the small kernel's)
+#ifdef FORCE_TILE
+  return g_force ? launch_tiles<E>(j, s) : launch_small<E>(j, s);
+#endif
+  if ((j.ids && j.M <= kFewTokens) || small_is_faster(j)) return launch_small<E>(j, s);
+  return launch_tiles<E>(j, s);
 }
 
 }  // namespace

@@ -6,7 +6,9 @@
 // DMA ring of its own, and holds the whole 64 x 64 tile (2 x 2 fragments of
 // 32x32x16); the four sums meet in the LDS.  Bound by the L2 -> LDS rate, 8 KB
 // per stage at about 50 bytes a clock and CU: 164 clocks, against 64 of matrix
-// work.
+// work.  A ring of two stages a wave leaves room for two blocks per CU, which
+// measured faster than one block with rings of four (64 KB of LDS each way in
+// flight: 512 x 4096 x 4096 32 against 34 us, 1552 x 1096 x 517 9.0 against 11.9).
 //
 // Adapters: each thread adds its row's low-rank product to its eight columns,
 // so mixed adapters cost no more than equal ones.
@@ -33,11 +35,12 @@ __device__ __forceinline__ void add_low_rank(F8& v, const float* s, const E* lb,
   }
 }
 
-template <typename E, bool TA, bool TB, int EPI, int NST>
-__global__ __launch_bounds__(256, 1) void small_kernel(DenseJob p) {
+template <typename E, bool TA, bool TB, int EPI>
+__global__ __launch_bounds__(256, 2) void small_kernel(DenseJob p) {
   typedef typename Vec<E>::v8 v8;
   using A = Operand<E, 64, TA, 1>;
   using B = Operand<E, 64, TB, 1>;
+  constexpr int NST = 2;
   constexpr int STAGE = A::BYTES + B::BYTES, LOADS = A::LOADS + B::LOADS;
   constexpr int TILE = 64 * 64 * 4, RING = NST * STAGE > TILE ? NST * STAGE : TILE;
   __shared__ __attribute__((aligned(1024))) char lds[4 * RING];
@@ -45,7 +48,7 @@ __global__ __launch_bounds__(256, 1) void small_kernel(DenseJob p) {
   const int l32 = lane & 31, g = lane >> 5;
   const int cols = EPI == kEpiGate ? 32 : 64, width = EPI == kEpiGate ? p.N >> 1 : p.N;
   int mt, nt;
-  tile_of(blockIdx.x, gridDim.x, (p.M + 63) >> 6, (width + cols - 1) / cols, &mt, &nt);
+  tile_at(xcd_run(blockIdx.x, gridDim.x), (p.M + 63) >> 6, (width + cols - 1) / cols, &mt, &nt);
   const int m0 = mt * 64, n0 = nt * cols;
 
   A a;

@@ -36,6 +36,7 @@ namespace mxmoe {
 namespace {
 
 constexpr int kBK = 32;          // k per stage
+constexpr int kTileLds = 128 << 10;
 // Transposing LDS read: lane i of 16 gets column i of the 4 x 16 patch whose row
 // r the lanes 4 r .. 4 r + 3 address, 8 bytes each.  `restrict` gives the read
 // alias information; without any, the compiler takes it to depend on every
@@ -146,39 +147,37 @@ struct Operand {
   }
 };
 
-// C tile index of a block.  Consecutive blocks go round the 8 XCDs; each XCD
-// takes one contiguous run of tiles, in groups of kGroup m-tiles by all n, so
-// that the blocks that share its L2 share operand tiles.
-constexpr int kGroup = 4;
-__device__ __forceinline__ void tile_of(int b, int blocks, int mt, int nt, int* m, int* n) {
+// Consecutive blocks go round the 8 XCDs; each XCD takes one contiguous run of
+// the work items.
+__device__ __forceinline__ int xcd_run(int b, int blocks) {
   const int xcd = b & 7, per = blocks >> 3, more = blocks & 7;
-  const int t = xcd * per + min(xcd, more) + (b >> 3);
+  return xcd * per + min(xcd, more) + (b >> 3);
+}
+// C tile number t, of mt x nt: groups of kGroup m-tiles by all n, so that the
+// tiles in work on an XCD at one time share operand rows in its L2.
+constexpr int kGroup = 4;
+__device__ __forceinline__ void tile_at(int t, int mt, int nt, int* m, int* n) {
   const int full = kGroup * nt, grp = t / full, in = t - grp * full;
   const int rows = min(kGroup, mt - grp * kGroup);
   *m = grp * kGroup + in % rows;
   *n = in / rows;
 }
 
+// The C tile of 64 FM rows from m0 and the nt-th 64 FN columns of B.
 template <typename E, bool TA, bool TB, int EPI, int FM, int FN, int NST>
-__global__ __launch_bounds__(256, 1) void dense_kernel(DenseJob p) {
+__device__ __forceinline__ void dense_tile(const DenseJob& p, int m0, int nt, char* lds) {
   typedef typename Vec<E>::v8 v8;
   constexpr int BM = 64 * FM, BN = 64 * FN;
   using A = Operand<E, BM, TA, 4>;
   using B = Operand<E, BN, TB, 4>;
   constexpr int STAGE = A::BYTES + B::BYTES;
   constexpr int STAGING = 32 * FN * 32 * 4;               // a wave's 32 rows of fp32 sums
-  static_assert(4 * STAGING <= NST * STAGE, "the epilogue fits the stages' LDS");
-  __shared__ __attribute__((aligned(1024))) char lds[NST * STAGE];
+  static_assert(NST * STAGE <= kTileLds && 4 * STAGING <= kTileLds, "LDS of a tile");
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l32 = lane & 31, g = lane >> 5;
   const int wm = (wave >> 1) * 32 * FM, wn = (wave & 1) * 32 * FN;
-  const int mts = (p.M + BM - 1) / BM;
-  const int cols = EPI == kEpiGate ? BN / 2 : BN, width = EPI == kEpiGate ? p.N >> 1 : p.N;
-  const int nts = (width + cols - 1) / cols;
-  int mt, nt;
-  tile_of(blockIdx.x, gridDim.x, mts, nts, &mt, &nt);
-  const int m0 = mt * BM;
+  const int width = EPI == kEpiGate ? p.N >> 1 : p.N;
 
   A a;
   B b;
@@ -189,7 +188,7 @@ __global__ __launch_bounds__(256, 1) void dense_kernel(DenseJob p) {
   constexpr int LOADS = A::LOADS + B::LOADS;
   constexpr int EARLY = LOADS / 2;   // of them, issued half a stage before the rest
   auto issue = [&](int j, int s) {
-    char* buf = lds + __builtin_amdgcn_readfirstlane((s & (NST - 1)) * STAGE);
+    char* buf = lds + __builtin_amdgcn_readfirstlane((uint32_t)s % NST * STAGE);
     if (j < A::LOADS) a.issue(j, s, K, wave, buf);
     else b.issue(j - A::LOADS, s, K, wave, buf + A::BYTES);
   };
@@ -211,7 +210,7 @@ __global__ __launch_bounds__(256, 1) void dense_kernel(DenseJob p) {
     v8 fa[2][FM], fb[2][FN];
     // fragment r of step ks of stage s
     auto read = [&](int s, int ks, int r, v8 (&xa)[FM], v8 (&xb)[FN]) {
-      const char* buf = lds + __builtin_amdgcn_readfirstlane((s & (NST - 1)) * STAGE);
+      const char* buf = lds + __builtin_amdgcn_readfirstlane((uint32_t)s % NST * STAGE);
       if (r < FN) xb[r] = B::frag(buf + A::BYTES, wn + r * 32, ks, lane);
       else xa[r - FN] = A::frag(buf, wm + (r - FN) * 32, ks, lane);
     };
@@ -373,6 +372,33 @@ __global__ __launch_bounds__(256, 1) void dense_kernel(DenseJob p) {
   if constexpr (FM > 1) finish_rows(std::integral_constant<int, 1>());
   if constexpr (FM > 2) finish_rows(std::integral_constant<int, 2>());
   if constexpr (FM > 3) finish_rows(std::integral_constant<int, 3>());
+}
+
+// 256 x 256 tiles, of which the last (fewer than one per CU) may be split into
+// 128 x 256 halves or 128 x 128 quarters: a part takes 0.65 or 0.33 of a whole
+// tile's time where a whole one takes 1 on a chip that is partly idle.
+// `full` whole tiles, then `rest` tiles in `parts` blocks each.
+template <typename E, bool TA, bool TB, int EPI>
+__global__ __launch_bounds__(256, 1) void tile_kernel(DenseJob p, int full, int rest, int parts) {
+  __shared__ __attribute__((aligned(1024))) char lds[kTileLds];
+  const int cols = EPI == kEpiGate ? 128 : 256, width = EPI == kEpiGate ? p.N >> 1 : p.N;
+  const int mts = (p.M + 255) >> 8, nts = (width + cols - 1) / cols;
+  const int b = blockIdx.x;
+  int mt, nt;
+  if (b < full) {
+    tile_at(xcd_run(b, full), mts, nts, &mt, &nt);
+    dense_tile<E, TA, TB, EPI, 4, 4, 4>(p, mt * 256, nt, lds);
+    return;
+  }
+  const int u = xcd_run(b - full, rest * parts), part = u % parts;
+  tile_at(full + u / parts, mts, nts, &mt, &nt);
+  if (parts == 1) {
+    dense_tile<E, TA, TB, EPI, 4, 4, 4>(p, mt * 256, nt, lds);
+  } else if (parts == 2) {
+    if (mt * 256 + part * 128 < p.M) dense_tile<E, TA, TB, EPI, 2, 4, 5>(p, mt * 256 + part * 128, nt, lds);
+  } else if (mt * 256 + (part & 1) * 128 < p.M && (2 * nt + (part >> 1)) * (cols / 2) < width) {
+    dense_tile<E, TA, TB, EPI, 2, 2, 8>(p, mt * 256 + (part & 1) * 128, 2 * nt + (part >> 1), lds);
+  }
 }
 
 }  // namespace
