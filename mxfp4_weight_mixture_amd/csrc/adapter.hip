@@ -6,144 +6,105 @@
 // will), more for prompts (adapters in runs); either way any order is right.
 // Two launches: the first gives s [T][R] in fp32, the second the shared
 // projection with s B^T added to its fp32 sums and the epilogue.
-#include "dense_dma.h"
+#include "dense_small.h"
 
 namespace mxmoe {
 namespace {
 
-// s of few tokens: one wave per (token, row of A), 64 lanes along K.  Tokens of
-// a decode batch have adapters of their own, so there is nothing to share.
+// s of few tokens.  A block takes one token and four rows of its adapter's A,
+// its four waves a quarter of K each: tokens of a decode batch have adapters
+// of their own, so there is little to share, and the time is one trip to memory.
 template <typename E>
 __global__ __launch_bounds__(256) void shrink_token_kernel(moe_adapter_args p, float* s) {
   typedef typename Vec<E>::v8 v8;
-  const int lane = threadIdx.x & 63;
-  const int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int t = (int)(w / p.R), r = (int)(w % p.R);
-  if (t >= p.T) return;
+  __shared__ float part[4][4];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int groups = p.R >> 2, t = blockIdx.x / groups, r0 = blockIdx.x % groups * 4;
   const int id = p.ids[t];
   if (id < 0 || id >= p.num_adapters) return;   // its row of s is not read
-  if (p.ranks && r >= p.ranks[id]) return;
-  const E* x = static_cast<const E*>(p.x) + (size_t)t * p.x_stride;
-  const E* a = static_cast<const E*>(p.a) + ((size_t)id * p.R + r) * p.K;
-  float sum = 0.0f;
-  for (int k = lane * 8; k < p.K; k += 512) {
-    const v8 xv = *reinterpret_cast<const v8*>(x + k), av = *reinterpret_cast<const v8*>(a + k);
+  if (p.ranks && r0 >= p.ranks[id]) return;
+  const E* const x = static_cast<const E*>(p.x) + (size_t)t * p.x_stride;
+  const E* const a = static_cast<const E*>(p.a) + ((size_t)id * p.R + r0) * p.K;
+  float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 2
+  for (int k = threadIdx.x * 8; k < p.K; k += 2048) {
+    const v8 xv = *reinterpret_cast<const v8*>(x + k);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sum += (float)xv[i] * (float)av[i];
+    for (int r = 0; r < 4; ++r) {
+      const v8 av = *reinterpret_cast<const v8*>(a + (size_t)r * p.K + k);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[r] += (float)xv[i] * (float)av[i];
+    }
   }
 #pragma unroll
-  for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d);
-  if (lane == 0) s[(size_t)t * p.R + r] = p.scales ? sum * p.scales[id] : sum;
+  for (int r = 0; r < 4; ++r) {
+#pragma unroll
+    for (int d = 32; d; d >>= 1) sum[r] += __shfl_xor(sum[r], d);
+    if (lane == 0) part[wave][r] = sum[r];
+  }
+  __syncthreads();
+  if (threadIdx.x < 4) {
+    const int r = threadIdx.x;
+    const float v = part[0][r] + part[1][r] + part[2][r] + part[3][r];
+    s[(size_t)t * p.R + r0 + r] = p.scales ? v * p.scales[id] : v;
+  }
 }
 
-// s of many tokens, whose requests come in runs: a block takes 16 TB tokens
-// and, for each adapter among them (one, mostly), 16 RB rows of A at a time.
-// Bound by reading x; eight waves split K in turns of 64 and add their sums up
-// through the LDS.  16x16x32 MFMA, A's rows first, so that a lane's sums are
-// one token's; loads run two turns ahead, past the end they read zeros.
-template <typename E, int TB, int RB>
-__global__ __launch_bounds__(512) void shrink_runs_kernel(moe_adapter_args p, float* s) {
-  typedef typename Vec<E>::v8 v8;
-  constexpr int WAVES = 8, D = 2;
-  __shared__ __attribute__((aligned(16))) v4f part[WAVES][RB * TB][64];
+// s of many tokens, whose requests come in runs: a block takes 32 tokens and,
+// for each adapter among them (one, mostly), 32 FN rows of A at a time; its
+// four waves split K.  Bound by reading x, which a ring of four stages a wave
+// keeps in flight.
+template <typename E, int FN>
+__global__ __launch_bounds__(256, 1) void shrink_runs_kernel(moe_adapter_args p, float* s) {
+  using A = Operand<E, 32, false, 1>;
+  using B = Operand<E, 32 * FN, false, 1>;
+  constexpr int NST = 4, RING = NST * (A::BYTES + B::BYTES);
+  static_assert(RING >= 32 * 32 * FN * 4, "the sums fit the ring");
+  __shared__ __attribute__((aligned(1024))) char lds[4 * RING];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int l16 = lane & 15, kl = 8 * (lane >> 4), t0 = blockIdx.x * 16 * TB;
-  const int K = p.K, turns = (((K + 63) >> 6) - wave + WAVES - 1) / WAVES;
-  const char* const xbase = static_cast<const char*>(p.x) + (int64_t)t0 * p.x_stride * 2;
-  uint32_t xoff[TB];
-#pragma unroll
-  for (int i = 0; i < TB; ++i)
-    xoff[i] = (uint32_t)((min(t0 + 16 * i + l16, p.T - 1) - t0) * (p.x_stride * 2)) + kl * 2;
-  const int mine = t0 + (lane & (16 * TB - 1)) < p.T ? p.ids[t0 + (lane & (16 * TB - 1))] : -1;
-  uint64_t left = __ballot(lane < 16 * TB && mine >= 0 && mine < p.num_adapters);
+  const int t0 = blockIdx.x * 32;
+  char* const ring = lds + wave * RING;
+  A a;
+  a.init(p.x, p.x_stride, p.T, t0, 0, lane);
+  const int mine = t0 + (lane & 31) < p.T ? p.ids[t0 + (lane & 31)] : -1;
+  uint64_t left = __ballot(lane < 32 && mine >= 0 && mine < p.num_adapters);
   while (left) {
     const int cur = __builtin_amdgcn_readlane(mine, __ffsll((unsigned long long)left) - 1);
     left &= ~__ballot(mine == cur);
     int rank = p.R;
     if (p.ranks) rank = min(max(p.ranks[cur], 0), p.R);
     const float scale = p.scales ? p.scales[cur] : 1.0f;
-    for (int r0 = 0; r0 < rank; r0 += 16 * RB) {
-      const char* const abase = static_cast<const char*>(p.a) + ((int64_t)cur * p.R + r0) * K * 2;
-      uint32_t aoff[RB];
+    for (int r0 = 0; r0 < rank; r0 += 32 * FN) {
+      B b;
+      b.init(static_cast<const E*>(p.a) + (size_t)cur * p.R * p.K, p.K, rank, r0, 0, lane);
+      v16f acc[1][FN];
 #pragma unroll
-      for (int i = 0; i < RB; ++i)
-        aoff[i] = r0 + 16 * i + l16 < rank ? (uint32_t)((16 * i + l16) * (K * 2) + kl * 2) : kOut;
-      v8 a[D][2][RB], x[D][2][TB];
-      auto load = [&](int t, int u) {
-        const int k = (wave + t * WAVES) * 64;
-        const auto ra = rsrc_at(abase + (int64_t)k * 2), rx = rsrc_at(xbase + (int64_t)k * 2);
+      for (int f = 0; f < FN; ++f)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const bool in = k + 32 * h + kl < K;
-#pragma unroll
-          for (int i = 0; i < TB; ++i) x[u][h][i] = load16<E>(rx, in ? xoff[i] + 64 * h : kOut);
-#pragma unroll
-          for (int i = 0; i < RB; ++i) a[u][h][i] = load16<E>(ra, in && aoff[i] != kOut ? aoff[i] + 64 * h : kOut);
-        }
-      };
-      v4f acc[RB][TB];
-#pragma unroll
-      for (int i = 0; i < RB; ++i)
-#pragma unroll
-        for (int j = 0; j < TB; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int u = 0; u < D; ++u) load(u, u);
-      for (int tt = 0; tt < turns; tt += D) {
-#pragma unroll
-        for (int u = 0; u < D; ++u) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int i = 0; i < RB; ++i)
-#pragma unroll
-              for (int j = 0; j < TB; ++j) acc[i][j] = mfma16(a[u][h][i], x[u][h][j], acc[i][j]);
-          __builtin_amdgcn_sched_barrier(0);
-          load(tt + D + u, u);
-          __builtin_amdgcn_sched_barrier(0);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < RB; ++i)
-#pragma unroll
-        for (int j = 0; j < TB; ++j) part[wave][i * TB + j][lane] = acc[i][j];
+        for (int q = 0; q < 16; ++q) acc[0][f][q] = 0.0f;
+      split_k_product<E, 1, FN, NST>(a, b, p.K, wave, lane, ring, acc);
+      put_sums<1, FN>(ring, lane, acc);
       __syncthreads();
-      // accumulator q of lane l: token l % 16, row 4 (l / 16) + q
-      for (int e = threadIdx.x; e < RB * TB * 64; e += 512) {
-        const int f = e >> 6, l = e & 63;
-        const int t = t0 + f % TB * 16 + (l & 15), r = r0 + f / TB * 16 + 4 * (l >> 4);
-        if (t < p.T && r < p.R && p.ids[t] == cur) {
-          v4f v = part[0][f][l];
+      const int row = threadIdx.x / (4 * FN), x = threadIdx.x % (4 * FN), t = t0 + row, r = r0 + 8 * x;
+      if (row < 32 && t < p.T && r < p.R && p.ids[t] == cur) {
+        F8 v = get_sum8<FN>(lds, RING, row, 2 * x);
 #pragma unroll
-          for (int w = 1; w < WAVES; ++w) v += part[w][f][l];
-          *reinterpret_cast<v4f*>(s + (size_t)t * p.R + r) = v * scale;
-        }
+        for (int e = 0; e < 8; ++e) v.v[e] *= scale;
+        store8<E>(s, MOE_FLOAT_FP32, (size_t)t * p.R + r, v);
       }
       __syncthreads();
     }
   }
 }
 
-template <typename E, int RB>
-void launch_runs(const moe_adapter_args& a, float* s, hipStream_t st) {
-  // 32 tokens a block read A half as often, where that leaves enough blocks
-  if ((a.T + 31) / 32 >= num_cus() / 2)
-    hipLaunchKernelGGL((shrink_runs_kernel<E, 2, RB>), dim3((a.T + 31) / 32), dim3(512), 0, st, a, s);
-  else
-    hipLaunchKernelGGL((shrink_runs_kernel<E, 1, RB>), dim3((a.T + 15) / 16), dim3(512), 0, st, a, s);
-}
-
 template <typename E>
 moe_status launch_shrink(const moe_adapter_args& a, float* s, hipStream_t st) {
-  if (a.T <= kFewTokens) {
-    const dim3 grid((unsigned)((a.T * a.R + 3) / 4));
-    hipLaunchKernelGGL((shrink_token_kernel<E>), grid, dim3(256), 0, st, a, s);
-  } else if (a.R <= 16) {
-    launch_runs<E, 1>(a, s, st);
-  } else if (a.R <= 32) {
-    launch_runs<E, 2>(a, s, st);
-  } else {
-    launch_runs<E, 4>(a, s, st);
-  }
+  if (a.T <= kFewTokens)
+    hipLaunchKernelGGL((shrink_token_kernel<E>), dim3(a.T * (a.R / 4)), dim3(256), 0, st, a, s);
+  else if (a.R <= 32)
+    hipLaunchKernelGGL((shrink_runs_kernel<E, 1>), dim3((a.T + 31) / 32), dim3(256), 0, st, a, s);
+  else
+    hipLaunchKernelGGL((shrink_runs_kernel<E, 2>), dim3((a.T + 31) / 32), dim3(256), 0, st, a, s);
   MXMOE_HIP(hipGetLastError());
   return MOE_OK;
 }

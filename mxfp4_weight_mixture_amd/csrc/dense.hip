@@ -99,6 +99,11 @@ moe_status launch_typed(const DenseJob& j, void* ws, hipStream_t s) {
 #ifdef FORCE_TILE
   return g_force ? launch_tiles<E>(j, s) : launch_small<E>(j, s);
 #endif
+  if (j.ids && j.K == 0 && j.M > kFewTokens) {
+    hipLaunchKernelGGL((adapters_only_kernel<E>), dim3((unsigned)tiles(j, 128, 128)), dim3(256), 0, s, j);
+    MXMOE_HIP(hipGetLastError());
+    return MOE_OK;
+  }
   if ((j.ids && j.M <= kFewTokens) || small_is_faster(j)) return launch_small<E>(j, s);
   return launch_tiles<E>(j, s);
 }

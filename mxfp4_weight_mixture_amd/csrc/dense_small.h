@@ -35,29 +35,15 @@ __device__ __forceinline__ void add_low_rank(F8& v, const float* s, const E* lb,
   }
 }
 
-template <typename E, bool TA, bool TB, int EPI>
-__global__ __launch_bounds__(256, 2) void small_kernel(DenseJob p) {
+// This wave's share of a K loop: stages wave, wave + 4, ... of 32 k, through a
+// ring of NST stages of its own.  acc[fm][fn] += A fragments x B fragments.
+template <typename E, int FM, int FN, int NST, typename A, typename B>
+__device__ __forceinline__ void split_k_product(const A& a, const B& b, int K, int wave, int lane, char* ring,
+                                                v16f (&acc)[FM][FN]) {
   typedef typename Vec<E>::v8 v8;
-  using A = Operand<E, 64, TA, 1>;
-  using B = Operand<E, 64, TB, 1>;
-  constexpr int NST = 2;
   constexpr int STAGE = A::BYTES + B::BYTES, LOADS = A::LOADS + B::LOADS;
-  constexpr int TILE = 64 * 64 * 4, RING = NST * STAGE > TILE ? NST * STAGE : TILE;
-  __shared__ __attribute__((aligned(1024))) char lds[4 * RING];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int l32 = lane & 31, g = lane >> 5;
-  const int cols = EPI == kEpiGate ? 32 : 64, width = EPI == kEpiGate ? p.N >> 1 : p.N;
-  int mt, nt;
-  tile_at(xcd_run(blockIdx.x, gridDim.x), (p.M + 63) >> 6, (width + cols - 1) / cols, &mt, &nt);
-  const int m0 = mt * 64, n0 = nt * cols;
-
-  A a;
-  B b;
-  a.init(p.a, p.lda, p.M, m0, 0, lane);
-  if constexpr (EPI == kEpiGate) b.init_gate(p, nt, 0, lane);
-  else b.init(p.b, p.ldb, p.N, n0, 0, lane);
-  const int K = p.K, turns = ((K + kBK - 1) / kBK - wave + 3) >> 2;
-  char* const ring = lds + wave * RING;
+  static_assert(NST % 2 == 0, "fragment registers alternate by turn");
+  const int turns = ((K + kBK - 1) / kBK - wave + 3) >> 2;
   auto issue = [&](int t, int buf) {
     const int s = wave + 4 * t;
 #pragma unroll
@@ -65,21 +51,16 @@ __global__ __launch_bounds__(256, 2) void small_kernel(DenseJob p) {
 #pragma unroll
     for (int j = 0; j < B::LOADS; ++j) b.issue(j, s, K, 0, ring + buf * STAGE + A::BYTES);
   };
-  v8 fa[2][2][2], fb[2][2][2];   // [turn parity][k step][fragment]
+  v8 fa[2][2][FM], fb[2][2][FN];   // [turn parity][k step][fragment]
   auto read = [&](int buf, int d) {
 #pragma unroll
-    for (int ks = 0; ks < 2; ++ks)
+    for (int ks = 0; ks < 2; ++ks) {
 #pragma unroll
-      for (int f = 0; f < 2; ++f) {
-        fa[d][ks][f] = A::frag(ring + buf * STAGE, f * 32, ks, lane);
-        fb[d][ks][f] = B::frag(ring + buf * STAGE + A::BYTES, f * 32, ks, lane);
-      }
+      for (int f = 0; f < FM; ++f) fa[d][ks][f] = A::frag(ring + buf * STAGE, f * 32, ks, lane);
+#pragma unroll
+      for (int f = 0; f < FN; ++f) fb[d][ks][f] = B::frag(ring + buf * STAGE + A::BYTES, f * 32, ks, lane);
+    }
   };
-  v16f acc[2][2];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int q = 0; q < 16; ++q) acc[i >> 1][i & 1][q] = 0.0f;
 #pragma unroll
   for (int t = 0; t < NST; ++t) issue(t, t);
   wait_vm<(NST - 1) * LOADS>();
@@ -101,41 +82,80 @@ __global__ __launch_bounds__(256, 2) void small_kernel(DenseJob p) {
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-        for (int f = 0; f < 4; ++f)
-          acc[f & 1][f >> 1] = mfma32(fb[u & 1][ks][f >> 1], fa[u & 1][ks][f & 1], acc[f & 1][f >> 1]);
+        for (int f = 0; f < FM * FN; ++f)
+          acc[f % FM][f / FM] = mfma32(fb[u & 1][ks][f / FM], fa[u & 1][ks][f % FM], acc[f % FM][f / FM]);
       __builtin_amdgcn_sched_barrier(0);
     }
   }
   wait_vm<0>();
   wait_lgkm0();
   __builtin_amdgcn_sched_barrier(0);
-  // stage this wave's sums over its ring: lane = row, 16-byte chunks permuted by row
+}
+
+// A wave's sums to its LDS area: lane = row, rows of 32 FN values, 16-byte
+// chunks permuted by row.
+template <int FM, int FN>
+__device__ __forceinline__ void put_sums(char* area, int lane, const v16f (&acc)[FM][FN]) {
+  constexpr int CH = FN * 8;
 #pragma unroll
-  for (int fm = 0; fm < 2; ++fm)
+  for (int fm = 0; fm < FM; ++fm)
 #pragma unroll
-    for (int fn = 0; fn < 2; ++fn)
+    for (int fn = 0; fn < FN; ++fn)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int row = fm * 32 + l32, c = fn * 8 + 2 * q + g;
-        *reinterpret_cast<v4f*>(ring + row * 256 + ((c ^ (row & 15)) << 4)) =
+        const int row = fm * 32 + (lane & 31), c = fn * 8 + 2 * q + (lane >> 5);
+        *reinterpret_cast<v4f*>(area + row * (CH * 16) + ((c ^ (row & (CH - 1))) << 4)) =
             v4f{acc[fm][fn][4 * q], acc[fm][fn][4 * q + 1], acc[fm][fn][4 * q + 2], acc[fm][fn][4 * q + 3]};
       }
-  __syncthreads();
-  auto sum8 = [&](int row, int c) {
-    F8 r;
+}
+// The four waves' sums of eight columns, from chunk c on, in wave order.
+template <int FN>
+__device__ __forceinline__ F8 get_sum8(const char* areas, int area_bytes, int row, int c) {
+  constexpr int CH = FN * 8;
+  F8 r;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      const char* base = lds + w * RING + row * 256;
-      const v4f x = *reinterpret_cast<const v4f*>(base + ((c ^ (row & 15)) << 4));
-      const v4f y = *reinterpret_cast<const v4f*>(base + (((c + 1) ^ (row & 15)) << 4));
+  for (int w = 0; w < 4; ++w) {
+    const char* base = areas + w * area_bytes + row * (CH * 16);
+    const v4f x = *reinterpret_cast<const v4f*>(base + ((c ^ (row & (CH - 1))) << 4));
+    const v4f y = *reinterpret_cast<const v4f*>(base + (((c + 1) ^ (row & (CH - 1))) << 4));
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        r.v[e] = w ? r.v[e] + x[e] : x[e];
-        r.v[4 + e] = w ? r.v[4 + e] + y[e] : y[e];
-      }
+    for (int e = 0; e < 4; ++e) {
+      r.v[e] = w ? r.v[e] + x[e] : x[e];
+      r.v[4 + e] = w ? r.v[4 + e] + y[e] : y[e];
     }
-    return r;
-  };
+  }
+  return r;
+}
+
+template <typename E, bool TA, bool TB, int EPI>
+__global__ __launch_bounds__(256, 2) void small_kernel(DenseJob p) {
+  using A = Operand<E, 64, TA, 1>;
+  using B = Operand<E, 64, TB, 1>;
+  constexpr int NST = 2;
+  constexpr int STAGE = A::BYTES + B::BYTES;
+  constexpr int TILE = 64 * 64 * 4, RING = NST * STAGE > TILE ? NST * STAGE : TILE;
+  __shared__ __attribute__((aligned(1024))) char lds[4 * RING];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int cols = EPI == kEpiGate ? 32 : 64, width = EPI == kEpiGate ? p.N >> 1 : p.N;
+  int mt, nt;
+  tile_at(xcd_run(blockIdx.x, gridDim.x), (p.M + 63) >> 6, (width + cols - 1) / cols, &mt, &nt);
+  const int m0 = mt * 64, n0 = nt * cols;
+
+  A a;
+  B b;
+  a.init(p.a, p.lda, p.M, m0, 0, lane);
+  if constexpr (EPI == kEpiGate) b.init_gate(p, nt, 0, lane);
+  else b.init(p.b, p.ldb, p.N, n0, 0, lane);
+  v16f acc[2][2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int q = 0; q < 16; ++q) acc[i >> 1][i & 1][q] = 0.0f;
+  char* const ring = lds + wave * RING;
+  split_k_product<E, 2, 2, NST>(a, b, p.K, wave, lane, ring, acc);
+  put_sums<2, 2>(ring, lane, acc);
+  __syncthreads();
+  auto sum8 = [&](int row, int c) { return get_sum8<2>(lds, RING, row, c); };
   // an adapter's rank, 0 for none
   auto rank_of = [&](int id) {
     if (id < 0 || id >= p.num_adapters) return 0;

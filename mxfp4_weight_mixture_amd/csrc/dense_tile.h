@@ -401,5 +401,16 @@ __global__ __launch_bounds__(256, 1) void tile_kernel(DenseJob p, int full, int 
   }
 }
 
+// The adapters' part alone (no shared projection): bound by reading `add` and
+// writing C, so small tiles, several blocks per CU.
+template <typename E>
+__global__ __launch_bounds__(256, 3) void adapters_only_kernel(DenseJob p) {
+  __shared__ __attribute__((aligned(1024))) char lds[32 << 10];
+  int mt, nt;
+  const int mts = (p.M + 127) >> 7, nts = (p.N + 127) >> 7;
+  tile_at(xcd_run(blockIdx.x, gridDim.x), mts, nts, &mt, &nt);
+  dense_tile<E, false, false, kEpiPlain, 2, 2, 2>(p, mt * 128, nt, lds);
+}
+
 }  // namespace
 }  // namespace mxmoe
