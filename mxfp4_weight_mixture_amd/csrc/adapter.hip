@@ -53,7 +53,8 @@ __global__ __launch_bounds__(256) void shrink_token_kernel(moe_adapter_args p, f
 // s of many tokens, whose requests come in runs: a block takes 32 tokens and,
 // for each adapter among them (one, mostly), 32 FN rows of A at a time; its
 // four waves split K.  Bound by reading x, which a ring of four stages a wave
-// keeps in flight.
+// keeps in flight.  gridDim.y blocks share a tile's adapters, so that a tile
+// where several requests meet takes no longer than the others.
 template <typename E, int FN>
 __global__ __launch_bounds__(256, 1) void shrink_runs_kernel(moe_adapter_args p, float* s) {
   using A = Operand<E, 32, false, 1>;
@@ -68,9 +69,10 @@ __global__ __launch_bounds__(256, 1) void shrink_runs_kernel(moe_adapter_args p,
   a.init(p.x, p.x_stride, p.T, t0, 0, lane);
   const int mine = t0 + (lane & 31) < p.T ? p.ids[t0 + (lane & 31)] : -1;
   uint64_t left = __ballot(lane < 32 && mine >= 0 && mine < p.num_adapters);
-  while (left) {
+  for (int turn = 0; left; ++turn) {
     const int cur = __builtin_amdgcn_readlane(mine, __ffsll((unsigned long long)left) - 1);
     left &= ~__ballot(mine == cur);
+    if (turn % gridDim.y != blockIdx.y) continue;
     int rank = p.R;
     if (p.ranks) rank = min(max(p.ranks[cur], 0), p.R);
     const float scale = p.scales ? p.scales[cur] : 1.0f;
@@ -102,9 +104,9 @@ moe_status launch_shrink(const moe_adapter_args& a, float* s, hipStream_t st) {
   if (a.T <= kFewTokens)
     hipLaunchKernelGGL((shrink_token_kernel<E>), dim3(a.T * (a.R / 4)), dim3(256), 0, st, a, s);
   else if (a.R <= 32)
-    hipLaunchKernelGGL((shrink_runs_kernel<E, 1>), dim3((a.T + 31) / 32), dim3(256), 0, st, a, s);
+    hipLaunchKernelGGL((shrink_runs_kernel<E, 1>), dim3((a.T + 31) / 32, 4), dim3(256), 0, st, a, s);
   else
-    hipLaunchKernelGGL((shrink_runs_kernel<E, 2>), dim3((a.T + 31) / 32), dim3(256), 0, st, a, s);
+    hipLaunchKernelGGL((shrink_runs_kernel<E, 2>), dim3((a.T + 31) / 32, 4), dim3(256), 0, st, a, s);
   MXMOE_HIP(hipGetLastError());
   return MOE_OK;
 }

@@ -11,13 +11,15 @@ int64_t tiles(const DenseJob& j, int bm, int bn) {
   return (int64_t)((j.M + bm - 1) / bm) * ((width + cols - 1) / cols);
 }
 
-// One instance per operand storage and epilogue that a caller uses.
-#define MXMOE_DENSE_FORMS(LAUNCH)                             \
-  if (j.epi == kEpiGate) LAUNCH(false, false, kEpiGate);       \
-  else if (j.epi == kEpiGateGrad) LAUNCH(false, true, kEpiGateGrad); \
-  else if (j.ta) LAUNCH(true, true, kEpiPlain);               \
-  else if (j.tb) LAUNCH(false, true, kEpiPlain);              \
-  else LAUNCH(false, false, kEpiPlain)
+// One instance per operand storage, epilogue and adapters that a caller uses.
+#define MXMOE_DENSE_FORMS(LAUNCH)                                             \
+  if (j.epi == kEpiGateGrad) LAUNCH(false, true, kEpiGateGrad, false);        \
+  else if (j.ta) LAUNCH(true, true, kEpiPlain, false);                        \
+  else if (j.tb) LAUNCH(false, true, kEpiPlain, false);                       \
+  else if (j.epi == kEpiGate && j.ids) LAUNCH(false, false, kEpiGate, true);  \
+  else if (j.epi == kEpiGate) LAUNCH(false, false, kEpiGate, false);          \
+  else if (j.ids) LAUNCH(false, false, kEpiPlain, true);                      \
+  else LAUNCH(false, false, kEpiPlain, false)
 
 // Whole 256 x 256 tiles in full rounds of the CUs, the rest whole or in parts.
 struct TilePlan {
@@ -36,8 +38,8 @@ template <typename E>
 moe_status launch_tiles(const DenseJob& j, hipStream_t s) {
   const TilePlan t = plan_tiles(j, num_cus() / 8 * 8);
   const dim3 grid((unsigned)(t.full + t.rest * t.parts)), block(256);
-#define MXMOE_LAUNCH(TA, TB, EPI) \
-  hipLaunchKernelGGL((tile_kernel<E, TA, TB, EPI>), grid, block, 0, s, j, (int)t.full, (int)t.rest, (int)t.parts)
+#define MXMOE_LAUNCH(TA, TB, EPI, LORA) \
+  hipLaunchKernelGGL((tile_kernel<E, TA, TB, EPI, LORA>), grid, block, 0, s, j, (int)t.full, (int)t.rest, (int)t.parts)
   MXMOE_DENSE_FORMS(MXMOE_LAUNCH);
 #undef MXMOE_LAUNCH
   MXMOE_HIP(hipGetLastError());
@@ -47,7 +49,7 @@ moe_status launch_tiles(const DenseJob& j, hipStream_t s) {
 template <typename E>
 moe_status launch_small(const DenseJob& j, hipStream_t s) {
   const dim3 grid((unsigned)tiles(j, 64, 64)), block(256);
-#define MXMOE_LAUNCH(TA, TB, EPI) hipLaunchKernelGGL((small_kernel<E, TA, TB, EPI>), grid, block, 0, s, j)
+#define MXMOE_LAUNCH(TA, TB, EPI, LORA) hipLaunchKernelGGL((small_kernel<E, TA, TB, EPI, LORA>), grid, block, 0, s, j)
   MXMOE_DENSE_FORMS(MXMOE_LAUNCH);
 #undef MXMOE_LAUNCH
   MXMOE_HIP(hipGetLastError());
@@ -100,7 +102,7 @@ moe_status launch_typed(const DenseJob& j, void* ws, hipStream_t s) {
   return g_force ? launch_tiles<E>(j, s) : launch_small<E>(j, s);
 #endif
   if (j.ids && j.K == 0 && j.M > kFewTokens) {
-    hipLaunchKernelGGL((adapters_only_kernel<E>), dim3((unsigned)tiles(j, 128, 128)), dim3(256), 0, s, j);
+    hipLaunchKernelGGL((adapters_only_kernel<E>), dim3((unsigned)tiles(j, 64, 128)), dim3(256), 0, s, j);
     MXMOE_HIP(hipGetLastError());
     return MOE_OK;
   }

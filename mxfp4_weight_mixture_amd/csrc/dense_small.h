@@ -127,7 +127,7 @@ __device__ __forceinline__ F8 get_sum8(const char* areas, int area_bytes, int ro
   return r;
 }
 
-template <typename E, bool TA, bool TB, int EPI>
+template <typename E, bool TA, bool TB, int EPI, bool LORA>
 __global__ __launch_bounds__(256, 2) void small_kernel(DenseJob p) {
   using A = Operand<E, 64, TA, 1>;
   using B = Operand<E, 64, TB, 1>;
@@ -165,7 +165,7 @@ __global__ __launch_bounds__(256, 2) void small_kernel(DenseJob p) {
     const int row = threadIdx.x >> 2, x = threadIdx.x & 3, m = m0 + row, i = n0 + x * 8;
     if (m < p.M && i < width) {
       F8 gt = sum8(row, 2 * x), up = sum8(row, 8 + 2 * x);
-      if (p.ids) {
+      if constexpr (LORA) {
         const int id = p.ids[m], rank = rank_of(id);
         if (rank > 0) {
           const float* s = p.s + (size_t)m * p.R;
@@ -186,7 +186,7 @@ __global__ __launch_bounds__(256, 2) void small_kernel(DenseJob p) {
       if constexpr (EPI == kEpiGateGrad) {
         finish_gate_grad<E>(p, m, n, v);
       } else {
-        if (!TB && p.ids) {
+        if constexpr (LORA) {
           const int id = p.ids[m], rank = rank_of(id);
           if (rank > 0)
             add_low_rank<E>(v, p.s + (size_t)m * p.R, static_cast<const E*>(p.lb) + ((size_t)id * p.N + n) * p.R, p.R,

@@ -164,7 +164,7 @@ __device__ __forceinline__ void tile_at(int t, int mt, int nt, int* m, int* n) {
 }
 
 // The C tile of 64 FM rows from m0 and the nt-th 64 FN columns of B.
-template <typename E, bool TA, bool TB, int EPI, int FM, int FN, int NST>
+template <typename E, bool TA, bool TB, int EPI, bool LORA, int FM, int FN, int NST>
 __device__ __forceinline__ void dense_tile(const DenseJob& p, int m0, int nt, char* lds) {
   typedef typename Vec<E>::v8 v8;
   constexpr int BM = 64 * FM, BN = 64 * FN;
@@ -179,6 +179,16 @@ __device__ __forceinline__ void dense_tile(const DenseJob& p, int m0, int nt, ch
   const int wm = (wave >> 1) * 32 * FM, wn = (wave & 1) * 32 * FN;
   const int width = EPI == kEpiGate ? p.N >> 1 : p.N;
 
+  // this lane's rows' adapters, -1 for none
+  int id[FM];
+  if constexpr (LORA) {
+#pragma unroll
+    for (int fm = 0; fm < FM; ++fm) {
+      const int m = m0 + wm + fm * 32 + l32;
+      id[fm] = m < p.M ? p.ids[m] : -1;
+      if (id[fm] < 0 || id[fm] >= p.num_adapters) id[fm] = -1;
+    }
+  }
   A a;
   B b;
   a.init(p.a, p.lda, p.M, m0, wave, lane);
@@ -258,6 +268,102 @@ __device__ __forceinline__ void dense_tile(const DenseJob& p, int m0, int nt, ch
     block_barrier();
   }
 
+  // each adapter present in the wave's rows in turn: its product goes to sums of
+  // its own, which only that adapter's rows take up.  s enters as two 16-bit
+  // operands (its high and low part), so that it is not rounded to one.  Two
+  // 16-deep steps are loaded together, and all rows where there are registers
+  // for it (256 accumulators leave none: they would have to leave the matrix
+  // cores' registers at once): the time is the loads' latency.
+  if constexpr (LORA) {
+    constexpr int HS = 2, FB = FM * FN > 8 ? 1 : FM;   // steps, fragment rows together
+    auto add_adapters = [&](auto F0) {
+    constexpr int f0 = decltype(F0)::value;
+    for (;;) {
+      int cur = -1;
+#pragma unroll
+      for (int fm = f0; fm < f0 + FB; ++fm) {
+        const uint64_t left = __ballot(id[fm] >= 0);
+        if (cur < 0 && left) cur = __builtin_amdgcn_readlane(id[fm], __ffsll((unsigned long long)left) - 1);
+      }
+      if (cur < 0) break;
+      bool mine[FB];
+#pragma unroll
+      for (int fm = f0; fm < f0 + FB; ++fm) {
+        mine[fm - f0] = id[fm] == cur;
+        if (mine[fm - f0]) id[fm] = -1;
+      }
+      int rank = p.R;
+      if (p.ranks) rank = min(max(p.ranks[cur], 0), p.R);
+      const float* const sp = p.s + (size_t)(m0 + wm + l32) * p.R;
+      const E* const lb = static_cast<const E*>(p.lb) + (size_t)cur * p.N * p.R;
+      for (int r = 0; r < rank; r += 16 * HS) {
+        F8 sv[FB][HS];
+        v8 bv[HS][FN];
+#pragma unroll
+        for (int h = 0; h < HS; ++h) {
+          const int k = r + 16 * h + 8 * g;
+#pragma unroll
+          for (int fn = 0; fn < FN; ++fn) {
+            int first, step, up;
+            b_block(p, nt, BN, (wn >> 5) + fn, &first, &step, &up);
+            const int i = first + l32;
+            const int row = EPI == kEpiGate ? (p.interleaved ? 2 * i + up : up * width + i) : i;
+            bv[h][fn] = v8{};
+            if (i < width && k < rank) bv[h][fn] = *reinterpret_cast<const v8*>(lb + (size_t)row * p.R + k);
+          }
+#pragma unroll
+          for (int fm = f0; fm < f0 + FB; ++fm) {
+            sv[fm - f0][h] = F8{};
+            if (mine[fm - f0] && k < rank) sv[fm - f0][h] = load8<E>(sp + (size_t)fm * 32 * p.R, MOE_FLOAT_FP32, k);
+          }
+        }
+        if (rank & 7) {   // what lies behind the rank does not count
+#pragma unroll
+          for (int h = 0; h < HS; ++h) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (r + 16 * h + 8 * g + e >= rank) {
+#pragma unroll
+                for (int fn = 0; fn < FN; ++fn) bv[h][fn][e] = (E)0.0f;
+#pragma unroll
+                for (int fm = f0; fm < f0 + FB; ++fm) sv[fm - f0][h].v[e] = 0.0f;
+              }
+          }
+        }
+#pragma unroll
+        for (int fm = f0; fm < f0 + FB; ++fm) {
+          if (!__ballot(mine[fm - f0])) continue;
+          v8 hi[HS], lo[HS];
+#pragma unroll
+          for (int h = 0; h < HS; ++h)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              E x, y;
+              split16(sv[fm - f0][h].v[e], &x, &y);
+              hi[h][e] = x, lo[h][e] = y;
+            }
+#pragma unroll
+          for (int fn = 0; fn < FN; ++fn) {
+            v16f t;
+#pragma unroll
+            for (int q = 0; q < 16; ++q) t[q] = 0.0f;
+#pragma unroll
+            for (int h = 0; h < HS; ++h) t = mfma32(bv[h][fn], hi[h], mfma32(bv[h][fn], lo[h], t));
+#pragma unroll
+            for (int q = 0; q < 16; ++q) acc[fm][fn][q] += mine[fm - f0] ? t[q] : 0.0f;
+          }
+        }
+      }
+    }
+    };
+    add_adapters(std::integral_constant<int, 0>());
+    if constexpr (FB < FM) {
+      add_adapters(std::integral_constant<int, 1>());
+      add_adapters(std::integral_constant<int, 2>());
+      add_adapters(std::integral_constant<int, 3>());
+    }
+  }
+
   // ---- epilogue: 32 rows of the wave's tile at a time ----
   char* const st = lds + wave * STAGING;
   constexpr int PITCH = FN * 32 * 4;          // bytes of a staged row
@@ -266,65 +372,6 @@ __device__ __forceinline__ void dense_tile(const DenseJob& p, int m0, int nt, ch
     constexpr int fm = decltype(FMI)::value;
     const int r0 = m0 + wm + fm * 32;
     if (r0 >= p.M) return;
-    // each adapter present in these rows in turn: its product goes to sums of
-    // its own, which only that adapter's rows take up.  s enters as two 16-bit
-    // operands (its high and low part), so that it is not rounded to one.
-    if (EPI != kEpiGateGrad && !TB && p.ids) {
-      const int m = r0 + l32;
-      const int id = m < p.M ? p.ids[m] : -1;
-      bool open = id >= 0 && id < p.num_adapters;
-      uint64_t left = __ballot(open);
-      while (left) {
-        const int cur = __builtin_amdgcn_readlane(id, __ffsll((unsigned long long)left) - 1);
-        const bool mine = open && id == cur;
-        int rank = p.R;
-        if (p.ranks) rank = min(max(p.ranks[cur], 0), p.R);
-        const float* const sp = p.s + (size_t)m * p.R;
-        const E* const lb = static_cast<const E*>(p.lb) + (size_t)cur * p.N * p.R;
-        v16f t[FN];
-#pragma unroll
-        for (int fn = 0; fn < FN; ++fn)
-#pragma unroll
-          for (int q = 0; q < 16; ++q) t[fn][q] = 0.0f;
-        for (int r = 0; r < rank; r += 16) {
-          const int k = r + 8 * g;
-          v8 hi = {}, lo = {}, bv[FN] = {};
-          if (mine && k < rank) {
-            const F8 sv = load8<E>(sp, MOE_FLOAT_FP32, k);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              E h, l;
-              split16(k + e < rank ? sv.v[e] : 0.0f, &h, &l);
-              hi[e] = h, lo[e] = l;
-            }
-          }
-#pragma unroll
-          for (int fn = 0; fn < FN; ++fn) {
-            int first, step, up;
-            b_block(p, nt, BN, (wn >> 5) + fn, &first, &step, &up);
-            const int i = first + l32;
-            const int row = EPI == kEpiGate ? (p.interleaved ? 2 * i + up : up * width + i) : i;
-            if (i < width && k < rank) bv[fn] = *reinterpret_cast<const v8*>(lb + (size_t)row * p.R + k);
-          }
-          if (k < rank && k + 8 > rank) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if (k + e >= rank) {
-#pragma unroll
-                for (int fn = 0; fn < FN; ++fn) bv[fn][e] = (E)0.0f;
-              }
-          }
-#pragma unroll
-          for (int fn = 0; fn < FN; ++fn) t[fn] = mfma32(bv[fn], hi, mfma32(bv[fn], lo, t[fn]));
-        }
-#pragma unroll
-        for (int fn = 0; fn < FN; ++fn)
-#pragma unroll
-          for (int q = 0; q < 16; ++q) acc[fm][fn][q] += mine ? t[fn][q] : 0.0f;
-        open = open && !mine;
-        left = __ballot(open);
-      }
-    }
     // stage: lane = row l32, four columns at a time, chunks permuted by row
 #pragma unroll
     for (int fn = 0; fn < FN; ++fn)
@@ -378,7 +425,7 @@ __device__ __forceinline__ void dense_tile(const DenseJob& p, int m0, int nt, ch
 // 128 x 256 halves or 128 x 128 quarters: a part takes 0.65 or 0.33 of a whole
 // tile's time where a whole one takes 1 on a chip that is partly idle.
 // `full` whole tiles, then `rest` tiles in `parts` blocks each.
-template <typename E, bool TA, bool TB, int EPI>
+template <typename E, bool TA, bool TB, int EPI, bool LORA>
 __global__ __launch_bounds__(256, 1) void tile_kernel(DenseJob p, int full, int rest, int parts) {
   __shared__ __attribute__((aligned(1024))) char lds[kTileLds];
   const int cols = EPI == kEpiGate ? 128 : 256, width = EPI == kEpiGate ? p.N >> 1 : p.N;
@@ -387,17 +434,17 @@ __global__ __launch_bounds__(256, 1) void tile_kernel(DenseJob p, int full, int 
   int mt, nt;
   if (b < full) {
     tile_at(xcd_run(b, full), mts, nts, &mt, &nt);
-    dense_tile<E, TA, TB, EPI, 4, 4, 4>(p, mt * 256, nt, lds);
+    dense_tile<E, TA, TB, EPI, LORA, 4, 4, 4>(p, mt * 256, nt, lds);
     return;
   }
   const int u = xcd_run(b - full, rest * parts), part = u % parts;
   tile_at(full + u / parts, mts, nts, &mt, &nt);
   if (parts == 1) {
-    dense_tile<E, TA, TB, EPI, 4, 4, 4>(p, mt * 256, nt, lds);
+    dense_tile<E, TA, TB, EPI, LORA, 4, 4, 4>(p, mt * 256, nt, lds);
   } else if (parts == 2) {
-    if (mt * 256 + part * 128 < p.M) dense_tile<E, TA, TB, EPI, 2, 4, 5>(p, mt * 256 + part * 128, nt, lds);
+    if (mt * 256 + part * 128 < p.M) dense_tile<E, TA, TB, EPI, LORA, 2, 4, 5>(p, mt * 256 + part * 128, nt, lds);
   } else if (mt * 256 + (part & 1) * 128 < p.M && (2 * nt + (part >> 1)) * (cols / 2) < width) {
-    dense_tile<E, TA, TB, EPI, 2, 2, 8>(p, mt * 256 + (part & 1) * 128, 2 * nt + (part >> 1), lds);
+    dense_tile<E, TA, TB, EPI, LORA, 2, 2, 8>(p, mt * 256 + (part & 1) * 128, 2 * nt + (part >> 1), lds);
   }
 }
 
@@ -407,9 +454,9 @@ template <typename E>
 __global__ __launch_bounds__(256, 3) void adapters_only_kernel(DenseJob p) {
   __shared__ __attribute__((aligned(1024))) char lds[32 << 10];
   int mt, nt;
-  const int mts = (p.M + 127) >> 7, nts = (p.N + 127) >> 7;
+  const int mts = (p.M + 63) >> 6, nts = (p.N + 127) >> 7;
   tile_at(xcd_run(blockIdx.x, gridDim.x), mts, nts, &mt, &nt);
-  dense_tile<E, false, false, kEpiPlain, 2, 2, 2>(p, mt * 128, nt, lds);
+  dense_tile<E, false, false, kEpiPlain, true, 1, 2, 2>(p, mt * 64, nt, lds);
 }
 
 }  // namespace
