@@ -56,13 +56,13 @@ moe_status launch_small(const DenseJob& j, hipStream_t s) {
   return MOE_OK;
 }
 
-template <typename E, int MB, int NB, bool XLDS, int D>
+template <typename E, int MB, int NB, bool DMA, int D>
 moe_status launch_few(const DenseJob& j, hipStream_t s) {
   const dim3 grid((j.N + 16 * NB - 1) / (16 * NB)), block(64 * kFewWaves);
   if (j.epi == kEpiGate)
-    hipLaunchKernelGGL((few_kernel<E, MB, NB, kEpiGate, XLDS, D>), grid, block, 0, s, j);
+    hipLaunchKernelGGL((few_kernel<E, MB, NB, kEpiGate, DMA, D>), grid, block, 0, s, j);
   else
-    hipLaunchKernelGGL((few_kernel<E, MB, NB, kEpiPlain, XLDS, D>), grid, block, 0, s, j);
+    hipLaunchKernelGGL((few_kernel<E, MB, NB, kEpiPlain, DMA, D>), grid, block, 0, s, j);
   MXMOE_HIP(hipGetLastError());
   return MOE_OK;
 }
@@ -90,13 +90,12 @@ moe_status launch_typed(const DenseJob& j, void* ws, hipStream_t s) {
   const int64_t reach = j.epi == kEpiGate ? (int64_t)(j.N / 2 + 16) * j.ldb * 2 : 0;
   if (j.M <= 64 && j.epi != kEpiGateGrad && !j.ta && !j.tb && reach < (1ll << 30)) {
     const bool wide = (j.N + 15) / 16 > num_cus();
+    // D: what the LDS holds (128 KB, for 16 rows 64 or 96)
     if (j.M <= 4) return launch_few<E, 1, 1, false, 4>(j, s);
-    if (j.M <= 16) return wide ? launch_few<E, 1, 2, true, 4>(j, s) : launch_few<E, 1, 1, true, 4>(j, s);
-    if (j.M <= 32) return wide ? launch_few<E, 2, 2, true, 4>(j, s) : launch_few<E, 2, 1, true, 4>(j, s);
-    return wide ? launch_few<E, 4, 2, true, 2>(j, s) : launch_few<E, 4, 1, true, 2>(j, s);
+    if (j.M <= 16) return wide ? launch_few<E, 1, 2, true, 2>(j, s) : launch_few<E, 1, 1, true, 2>(j, s);
+    if (j.M <= 32) return wide ? launch_few<E, 2, 2, true, 2>(j, s) : launch_few<E, 2, 1, true, 2>(j, s);
+    return wide ? launch_few<E, 4, 2, true, 1>(j, s) : launch_few<E, 4, 1, true, 1>(j, s);
   }
-  if (tiles(j, 64, 64) > 0x7fffffff)
-    return fail(MOE_ERR_SHAPE, "dense product: %d x %d is too large for one launch", j.M, j.N);
   // (a decode batch's mixed adapters are the small kernel's)
 #ifdef FORCE_TILE
   return g_force ? launch_tiles<E>(j, s) : launch_small<E>(j, s);

@@ -4,20 +4,19 @@
 // epilogue) and all rows of A, up to 16 MB of them; its waves split K in turns of 64 (one
 // 128-byte line of every weight row) and add their sums up through the LDS.
 //
-// Weights go straight to registers in the 16x16x32 MFMA's operand layout (lane
-// l: row l % 16, k 8 (l / 16) .. + 8): each is used once.  In that layout 16
-// neighbouring lanes touch 16 lines, which costs the vector L1 64 clocks per
-// KB (16 bytes a clock and CU, measured); the weights alone stay under that,
-// but A, which every block reads whole, would not.  So A takes the other way:
-// DMA to the LDS in whole 128-byte lines (50 bytes a clock), each wave its own
-// turns, and fragments from there; chunks are permuted by row (chunk ^ row / 2)
-// so that 16 rows cover all banks.  With up to four rows the lanes' addresses
-// coincide and direct loads are as cheap (XLDS = false).
-// Loads return in order, so both run the same D turns ahead: 2 KB of weights
-// per wave and turn, of which a CU needs some 24 KB in flight.
+// Operand layout of the 16x16x32 MFMA: lane l holds row l % 16, k 8 (l / 16) ..
+// + 8.  Loads straight into it touch 16 lines with 16 neighbouring lanes, which
+// costs the vector L1 64 clocks per KB (16 bytes a clock and CU, measured), as
+// much as the weights alone may take.  So both operands go to the LDS by DMA, in
+// whole 128-byte lines (20 clocks per KB), each wave its own turns D ahead, and
+// from there to the products; chunks are permuted by row (chunk ^ row / 2) so
+// that 16 rows cover all banks.  32 rows of 7168 x 7168: 26.2 us, against 33.4
+// with the weights loaded directly and 41 with both.  With up to four rows
+// A's lanes coincide and everything goes directly (DMA = false; one row of
+// 4096 x 4096: 9.1 against 9.3 us).
 // NB = 2 halves what A costs, and is taken once 16 rows a block would give
-// more blocks than CUs.
-// A turn past the end, or k past the end, reads zeros without a request.
+// more blocks than CUs.  A turn past the end, or k past the end, reads zeros
+// without a request.
 // Rows past the end repeat the last one; their sums are not used.
 #pragma once
 
@@ -29,13 +28,13 @@ namespace {
 
 constexpr int kFewWaves = 8;
 
-template <typename E, int MB, int NB, int EPI, bool XLDS, int D>
+template <typename E, int MB, int NB, int EPI, bool DMA, int D>
 __global__ __launch_bounds__(64 * kFewWaves) void few_kernel(DenseJob p) {
   typedef typename Vec<E>::v8 v8;
   constexpr int WAVES = kFewWaves;
   constexpr int COLS = NB * (EPI == kEpiGate ? 8 : 16), PITCH = 16 * NB + 4;
-  constexpr int TURN_X = XLDS ? MB * 2048 : 0;                     // LDS bytes of a wave's turn of A
-  constexpr int PART = WAVES * MB * NB * 1024, XBUF = WAVES * D * TURN_X;
+  constexpr int TURN = DMA ? (MB + NB) * 2048 : 0;                // LDS bytes of a wave's turn: A, then weights
+  constexpr int PART = WAVES * MB * NB * 1024, XBUF = WAVES * D * TURN;
   constexpr int BUF = XBUF > PART ? XBUF : PART;
   // one array: with several, the compiler gives each alias scopes by which it
   // drains all LDS DMA before an LDS read
@@ -53,47 +52,48 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_kernel(DenseJob p) {
   const int K = p.K;
   const int turns = (((K + 63) >> 6) - wave + WAVES - 1) / WAVES;  // lines wave, wave + WAVES, ...
   const int row0 = __builtin_amdgcn_readfirstlane(b_row(0));       // the lowest of the block's rows
-  uint32_t woff[NB];
-#pragma unroll
-  for (int n = 0; n < NB; ++n) woff[n] = (uint32_t)((b_row(16 * n + l16) - row0) * (p.ldb * 2)) + kl * 2;
   const char* const wbase = static_cast<const char*>(p.b) + (int64_t)row0 * p.ldb * 2;
   const char* const xbase = static_cast<const char*>(p.a);
-  // W of a turn: two operands (k 0..31 and 32..63 of the line)
-  v8 b[D][2][NB];
-  auto load_w = [&](int t, int u) {
+  // this lane's offsets: by DMA row 8 j + lane / 8 of 2 * 8 rows per block of
+  // 16 (row / 2 % 8 is 4 (j % 2) + lane / 16), directly row 16 i + lane % 16
+  const int c8 = (lane & 7) ^ ((lane >> 4) & 3);
+  constexpr int PER = DMA ? 2 : 1;
+  uint32_t xoff[PER * MB], woff[PER * NB];
+#pragma unroll
+  for (int j = 0; j < PER * MB; ++j)
+    xoff[j] = (uint32_t)(min(DMA ? 8 * j + (lane >> 3) : 16 * j + l16, p.M - 1) * (p.lda * 2)) +
+              (DMA ? (c8 ^ ((j & 1) << 2)) * 16 : kl * 2);
+#pragma unroll
+  for (int j = 0; j < PER * NB; ++j)
+    woff[j] = (uint32_t)((b_row(DMA ? 8 * j + (lane >> 3) : 16 * j + l16) - row0) * (p.ldb * 2)) +
+              (DMA ? (c8 ^ ((j & 1) << 2)) * 16 : kl * 2);
+  char* const ring = lds + wave * D * TURN;
+  v8 xr[DMA ? 1 : D][2][MB], wr[DMA ? 1 : D][2][NB];
+  auto load = [&](int t, int u) {
     const int k = (wave + t * WAVES) * 64;
-    const auto rs = rsrc_at(wbase + (int64_t)k * 2);
+    const auto rx = rsrc_at(xbase + (int64_t)k * 2), rw = rsrc_at(wbase + (int64_t)k * 2);
+    if constexpr (DMA) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int n = 0; n < NB; ++n) b[u][h][n] = load16<E>(rs, k + 32 * h + kl < K ? woff[n] + 64 * h : kOut);
-  };
-  // A of a turn: into LDS buffer u, or registers
-  uint32_t xoff[XLDS ? 2 * MB : MB];
-  const int xc = (lane & 7) ^ ((lane >> 4) & 3);                   // row r = 8 j + lane / 8: r / 2 % 8 is
-  if constexpr (XLDS) {                                            // 4 (j % 2) + lane / 16
-#pragma unroll
-    for (int j = 0; j < 2 * MB; ++j)
-      xoff[j] = (uint32_t)(min(8 * j + (lane >> 3), p.M - 1) * (p.lda * 2)) + (xc ^ ((j & 1) << 2)) * 16;
-  } else {
-#pragma unroll
-    for (int i = 0; i < MB; ++i) xoff[i] = (uint32_t)(min(i * 16 + l16, p.M - 1) * (p.lda * 2)) + kl * 2;
-  }
-  char* const xbuf = lds + wave * D * TURN_X;
-  v8 xr[XLDS ? 1 : D][2][MB];
-  auto load_x = [&](int t, int u) {
-    const int k = (wave + t * WAVES) * 64;
-    const auto rs = rsrc_at(xbase + (int64_t)k * 2);
-    if constexpr (XLDS) {
-#pragma unroll
-      for (int j = 0; j < 2 * MB; ++j)
-        dma16(rs, k + (xc ^ ((j & 1) << 2)) * 8 < K ? xoff[j] : kOut, xbuf + u * TURN_X + j * 1024);
+      for (int j = 0; j < 2 * (MB + NB); ++j) {
+        const uint32_t o = j < 2 * MB ? xoff[j < 2 * MB ? j : 0] : woff[j < 2 * MB ? 0 : j - 2 * MB];
+        dma16(j < 2 * MB ? rx : rw, k + (c8 ^ ((j & 1) << 2)) * 8 < K ? o : kOut, ring + u * TURN + j * 1024);
+      }
     } else {
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int h = 0; h < 2; ++h) {
+        const bool in = k + 32 * h + kl < K;
 #pragma unroll
-        for (int i = 0; i < MB; ++i) xr[u][h][i] = load16<E>(rs, k + 32 * h + kl < K ? xoff[i] + 64 * h : kOut);
+        for (int i = 0; i < MB; ++i) xr[u][h][i] = load16<E>(rx, in ? xoff[i] + 64 * h : kOut);
+#pragma unroll
+        for (int n = 0; n < NB; ++n) wr[u][h][n] = load16<E>(rw, in ? woff[n] + 64 * h : kOut);
+      }
     }
+  };
+  // operand h of block i of the turn in buffer u (A's blocks, then the weights')
+  auto operand = [&](int u, int h, int i) {
+    const int row = i * 16 + l16;
+    return read_lds((const __attribute__((address_space(3))) v8*)(
+        ring + u * TURN + row * 128 + (((h * 4 + (lane >> 4)) ^ ((row >> 1) & 7)) << 4)));
   };
 
   v4f acc[NB][MB];
@@ -103,8 +103,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_kernel(DenseJob p) {
     for (int i = 0; i < MB; ++i) acc[n][i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
   for (int u = 0; u < D; ++u) {
-    load_x(u, u);
-    load_w(u, u);
+    load(u, u);
     __builtin_amdgcn_sched_barrier(0);   // the waits below count on this order
   }
   // D turns per step without a way out between them, so that every load has a
@@ -113,37 +112,45 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_kernel(DenseJob p) {
   for (int t0 = 0; t0 < turns; t0 += D) {
 #pragma unroll
     for (int u = 0; u < D; ++u) {
-      const int t = t0 + u;
-      v8 a[2][MB];
-      if constexpr (XLDS) {
+      v8 a[2][MB], b[2][NB];
+      if constexpr (DMA) {
         // this turn's loads have landed; those of the D - 1 younger turns may fly
-        wait_vm<(D - 1) * (2 * MB + 2 * NB)>();
+        wait_vm<(D - 1) * 2 * (MB + NB)>();
+        __builtin_amdgcn_sched_barrier(0);
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int i = 0; i < MB; ++i) {
+          if constexpr (DMA) a[h][i] = operand(u, h, i);
+          else a[h][i] = xr[u][h][i];
+        }
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+          if constexpr (DMA) b[h][n] = operand(u, h, MB + n);
+          else b[h][n] = wr[u][h][n];
+        }
+      }
+      if constexpr (DMA) {
+        wait_lgkm0();                      // the buffer has been read
+        __builtin_amdgcn_sched_barrier(0);
+        load(t0 + u + D, u);
         __builtin_amdgcn_sched_barrier(0);
       }
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int i = 0; i < MB; ++i) {
-          const int row = i * 16 + l16;
-          if constexpr (XLDS)
-            a[h][i] = read_lds((const __attribute__((address_space(3))) v8*)(
-                xbuf + u * TURN_X + row * 128 + (((h * 4 + (lane >> 4)) ^ ((row >> 1) & 7)) << 4)));
-          else a[h][i] = xr[u][h][i];
-        }
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
         for (int n = 0; n < NB; ++n)
 #pragma unroll
-          for (int i = 0; i < MB; ++i) acc[n][i] = mfma16(b[u][h][n], a[h][i], acc[n][i]);
-      if constexpr (XLDS) wait_lgkm0();    // the buffer has been read
+          for (int i = 0; i < MB; ++i) acc[n][i] = mfma16(b[h][n], a[h][i], acc[n][i]);
       __builtin_amdgcn_sched_barrier(0);
-      load_x(t + D, u);
-      load_w(t + D, u);
-      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (!DMA) {
+        load(t0 + u + D, u);
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
   }
-  if constexpr (XLDS) {   // the sums take the place of A's turns
+  if constexpr (DMA) {   // the sums take the place of A's turns
     wait_vm<0>();
     __syncthreads();
   }
