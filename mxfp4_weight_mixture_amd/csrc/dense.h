@@ -43,6 +43,8 @@ constexpr int kFewTokens = 256;
 
 size_t dense_ws_bytes(int M, int N, int K);
 moe_status launch_dense(const DenseJob& j, void* ws, hipStream_t s);
+// Up to three independent plain products of one type with B stored [K][N].
+moe_status launch_dense_group(const DenseJob* jobs, int n, void* ws, hipStream_t s);
 
 // ---- argument checks shared by the entry points -------------------------
 constexpr int kMaxWidth = 1 << 18;

@@ -109,6 +109,22 @@ moe_status launch_typed(const DenseJob& j, void* ws, hipStream_t s) {
   return launch_tiles<E>(j, s);
 }
 
+template <typename E>
+moe_status launch_group_typed(const DenseJob* jobs, int n, hipStream_t s) {
+  SmallGroup g{};
+  int64_t at = 0;
+  for (int i = 0; i < 3; ++i) {
+    g.job[i] = jobs[i < n ? i : 0];
+    g.start[i] = (int)at;
+    g.tiles[i] = i < n ? (int)tiles(jobs[i], 64, 64) : 0;
+    at += (g.tiles[i] + 7) / 8 * 8;
+  }
+  g.start[3] = (int)at;
+  hipLaunchKernelGGL((small_group_kernel<E>), dim3((unsigned)at), dim3(256), 0, s, g);
+  MXMOE_HIP(hipGetLastError());
+  return MOE_OK;
+}
+
 }  // namespace
 
 size_t dense_ws_bytes(int M, int N, int K) { return 0; }
@@ -116,6 +132,21 @@ size_t dense_ws_bytes(int M, int N, int K) { return 0; }
 moe_status launch_dense(const DenseJob& j, void* ws, hipStream_t s) {
   if (j.M == 0) return MOE_OK;
   return j.dtype == MOE_FLOAT_BF16 ? launch_typed<__bf16>(j, ws, s) : launch_typed<_Float16>(j, ws, s);
+}
+
+moe_status launch_dense_group(const DenseJob* jobs, int n, void* ws, hipStream_t s) {
+  // one launch where each would run in 64 x 64 tiles that leave CUs idle
+  int64_t blocks = 0;
+  bool small = n > 1;
+  for (int i = 0; i < n; ++i) {
+    if (jobs[i].M == 0 || !small_is_faster(jobs[i])) small = false;
+    else blocks += tiles(jobs[i], 64, 64);
+  }
+  if (small && blocks <= 8 * (int64_t)num_cus())
+    return jobs[0].dtype == MOE_FLOAT_BF16 ? launch_group_typed<__bf16>(jobs, n, s)
+                                           : launch_group_typed<_Float16>(jobs, n, s);
+  for (int i = 0; i < n; ++i) MXMOE_TRY(launch_dense(jobs[i], ws, s));
+  return MOE_OK;
 }
 
 }  // namespace mxmoe

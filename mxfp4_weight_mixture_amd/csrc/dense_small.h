@@ -127,18 +127,21 @@ __device__ __forceinline__ F8 get_sum8(const char* areas, int area_bytes, int ro
   return r;
 }
 
+constexpr int kSmallLds = 64 << 10;
+
+// The C tile of block `block` of `blocks`.
 template <typename E, bool TA, bool TB, int EPI, bool LORA>
-__global__ __launch_bounds__(256, 2) void small_kernel(DenseJob p) {
+__device__ __forceinline__ void small_tile(const DenseJob& p, int block, int blocks, char* lds) {
   using A = Operand<E, 64, TA, 1>;
   using B = Operand<E, 64, TB, 1>;
   constexpr int NST = 2;
   constexpr int STAGE = A::BYTES + B::BYTES;
   constexpr int TILE = 64 * 64 * 4, RING = NST * STAGE > TILE ? NST * STAGE : TILE;
-  __shared__ __attribute__((aligned(1024))) char lds[4 * RING];
+  static_assert(4 * RING <= kSmallLds, "LDS of a tile");
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int cols = EPI == kEpiGate ? 32 : 64, width = EPI == kEpiGate ? p.N >> 1 : p.N;
   int mt, nt;
-  tile_at(xcd_run(blockIdx.x, gridDim.x), (p.M + 63) >> 6, (width + cols - 1) / cols, &mt, &nt);
+  tile_at(xcd_run(block, blocks), (p.M + 63) >> 6, (width + cols - 1) / cols, &mt, &nt);
   const int m0 = mt * 64, n0 = nt * cols;
 
   A a;
@@ -196,6 +199,29 @@ __global__ __launch_bounds__(256, 2) void small_kernel(DenseJob p) {
       }
     }
   }
+}
+
+template <typename E, bool TA, bool TB, int EPI, bool LORA>
+__global__ __launch_bounds__(256, 2) void small_kernel(DenseJob p) {
+  __shared__ __attribute__((aligned(1024))) char lds[kSmallLds];
+  small_tile<E, TA, TB, EPI, LORA>(p, blockIdx.x, gridDim.x, lds);
+}
+
+// Independent products in one launch: their few blocks share the chip, and
+// only one launch's ends are paid for.  Blocks [start[i], start[i + 1]) are
+// job i's (the starts multiples of 8, which keeps every job's blocks on the
+// XCDs they are dealt to; blocks past a job's tiles do nothing).
+struct SmallGroup {
+  DenseJob job[3];
+  int start[4], tiles[3];
+};
+template <typename E>
+__global__ __launch_bounds__(256, 2) void small_group_kernel(SmallGroup g) {
+  __shared__ __attribute__((aligned(1024))) char lds[kSmallLds];
+  const int b = blockIdx.x, i = b >= g.start[2] ? 2 : b >= g.start[1] ? 1 : 0, block = b - g.start[i];
+  if (block >= g.tiles[i]) return;
+  if (g.job[i].ta) small_tile<E, true, true, kEpiPlain, false>(g.job[i], block, g.tiles[i], lds);
+  else small_tile<E, false, true, kEpiPlain, false>(g.job[i], block, g.tiles[i], lds);
 }
 
 }  // namespace

@@ -169,6 +169,9 @@ moe_status moe_gated_ffn_backward(const moe_ffn_grad_args* a, void* stream) {
   j.h = ws + w.h;
   MXMOE_TRY(launch_dense(j, ws + w.gemm, s));
 
+  // what is asked for of dx, dw1 and dw2, independent of each other
+  DenseJob jobs[3];
+  int n = 0;
   j.epi = kEpiPlain;
   j.gu = j.h = nullptr;
   if (a->dx) {
@@ -176,7 +179,7 @@ moe_status moe_gated_ffn_backward(const moe_ffn_grad_args* a, void* stream) {
     j.b = a->w1, j.ldb = H, j.tb = 1;
     j.M = a->T, j.N = a->H, j.K = 2 * a->I;
     j.c = a->dx, j.ldc = a->dx_stride, j.c_dtype = a->dx_dtype;
-    MXMOE_TRY(launch_dense(j, ws + w.gemm, s));
+    if (a->T > 0) jobs[n++] = j;
   }
   // the weights' gradients sum over the tokens: both operands have the
   // reduction outermost
@@ -189,7 +192,7 @@ moe_status moe_gated_ffn_backward(const moe_ffn_grad_args* a, void* stream) {
     j.M = 2 * a->I, j.N = a->H;
     j.c = a->dw1, j.ldc = H;
     j.add = a->accumulate ? a->dw1 : nullptr, j.ldadd = H;
-    MXMOE_TRY(launch_dense(j, ws + w.gemm, s));
+    jobs[n++] = j;
   }
   if (a->dw2) {
     j.a = a->dout, j.lda = a->dout_stride;
@@ -197,8 +200,9 @@ moe_status moe_gated_ffn_backward(const moe_ffn_grad_args* a, void* stream) {
     j.M = a->H, j.N = a->I;
     j.c = a->dw2, j.ldc = I;
     j.add = a->accumulate ? a->dw2 : nullptr, j.ldadd = I;
-    MXMOE_TRY(launch_dense(j, ws + w.gemm, s));
+    jobs[n++] = j;
   }
+  MXMOE_TRY(launch_dense_group(jobs, n, ws + w.gemm, s));
   return MOE_OK;
 }
 
