@@ -538,11 +538,14 @@ class Layer:
     """A resident layer: weights stay on the device; forward() runs the five steps on one stream."""
 
     def __init__(self, w1_packed, w1_scales, w2_packed, w2_scales, k: int, layout: str = "split",
-                 inter: str = "bf16", w_format: str = "canonical", tile: bool = False):
+                 inter: str = "bf16", w_format: str = "canonical", tile: bool = False,
+                 shared: Optional["GatedFFN"] = None):
         """inter: precision of the SwiGLU output fed to FC2, "bf16" or "mxfp8".
         w_format: the order of the given weights, "canonical" or "tiled" (W1 tiled
         with `layout`, W2 with "none").  tile=True: canonical weights are tiled
-        here once and the layer keeps only the tiled copy."""
+        here once and the layer keeps only the tiled copy.
+        shared: a GatedFFN that every token passes beside its routed experts (a
+        shared expert); forward() adds its result to theirs."""
         if tile:
             if w_format != "canonical":
                 raise ValueError("tile=True takes canonical weights")
@@ -556,6 +559,9 @@ class Layer:
         self.k = k
         self.layout = LAYOUT[layout]
         self.inter = OUT[{"bf16": "MOE_OUT_BF16", "mxfp8": "MOE_OUT_MXFP8_E4M3"}[inter]]
+        if shared is not None and shared.H != self.H:
+            raise ValueError(f"the shared expert's width {shared.H} is not the layer's {self.H}")
+        self.shared = shared
         self._ws = None
 
     def workspace_bytes(self, T: int) -> int:
@@ -571,8 +577,25 @@ class Layer:
                          x_next=x_next.data_ptr() if x_next is not None else None,
                          workspace=ws.data_ptr(), workspace_bytes=ws.numel(), w_format=self.w_format)
 
+    def _shared_input(self, x, x_scales, x_shared, x_next):
+        """The shared expert's activations, [T][H] in its type: x itself where that is what x holds."""
+        if self.shared is None:
+            if x_shared is not None:
+                raise ValueError("x_shared without a shared expert")
+            return None
+        if x_next is not None:
+            raise ValueError("x_next is taken from the routed experts' sum: not with a shared expert")
+        xs = x if x_shared is None and x_scales is None else x_shared
+        if xs is None:
+            raise ValueError("MXFP8 activations: the shared expert needs x_shared, their 16-bit values")
+        _rows("the shared expert's input", xs, x.shape[0], self.H, (self.shared.dtype,), self.shared.device)
+        return xs
+
     def forward(self, logits: torch.Tensor, x: torch.Tensor, x_scales: Optional[torch.Tensor] = None,
-                out: Optional[torch.Tensor] = None, x_next: Optional[torch.Tensor] = None, stream=None):
+                out: Optional[torch.Tensor] = None, x_next: Optional[torch.Tensor] = None, stream=None,
+                x_shared: Optional[torch.Tensor] = None):
+        """x_shared: the shared expert's activations where x does not hold them (MXFP8 x, or another type)."""
+        x_shared = self._shared_input(x, x_scales, x_shared, x_next)
         T = logits.shape[0]
         n = self.workspace_bytes(T)
         if self._ws is None or self._ws.numel() < n:
@@ -583,12 +606,15 @@ class Layer:
         _check(lib.moe_layer_forward(ctypes.byref(args), _stream(stream)))
         # the workspace may be replaced by a larger one on a later call while this one still runs
         _keep_until_done(stream, self._ws, out)
+        if x_shared is not None:
+            self.shared.forward(x_shared, add=out, out=out, stream=stream)
         return out
 
     def capture(self, logits: torch.Tensor, x: torch.Tensor, x_scales: Optional[torch.Tensor] = None,
-                out: Optional[torch.Tensor] = None, x_next: Optional[torch.Tensor] = None) -> "LayerGraph":
+                out: Optional[torch.Tensor] = None, x_next: Optional[torch.Tensor] = None,
+                x_shared: Optional[torch.Tensor] = None) -> "LayerGraph":
         """moe_layer_graph_create: this layer on these buffers, captured once; see LayerGraph."""
-        return LayerGraph(self, logits, x, x_scales, out, x_next)
+        return LayerGraph(self, logits, x, x_scales, out, x_next, x_shared)
 
     def routing(self, T: int):
         """Views of the routing arrays the last forward() wrote into its workspace."""
@@ -606,11 +632,13 @@ class LayerGraph:
 
     The graph owns its workspace and keeps the tensors it was captured on:
     replay() runs the five steps with one launch, reading the current contents
-    of logits / x / x_scales and writing `out` (and x_next).  Replays on one
-    graph must not overlap each other.
+    of logits / x / x_scales and writing `out` (and x_next); a shared expert
+    follows as launches of its own.  Replays on one graph must not overlap each
+    other.
     """
 
-    def __init__(self, layer: Layer, logits, x, x_scales=None, out=None, x_next=None):
+    def __init__(self, layer: Layer, logits, x, x_scales=None, out=None, x_next=None, x_shared=None):
+        self.x_shared = layer._shared_input(x, x_scales, x_shared, x_next)
         T = logits.shape[0]
         dev = logits.device
         self.layer, self.T = layer, T
@@ -628,6 +656,8 @@ class LayerGraph:
         if not self._h:
             raise MoeError(STATUS["MOE_ERR_INVALID_ARG"], "graph already destroyed")
         _check(lib.moe_layer_graph_launch(self._h, _stream(stream)))
+        if self.x_shared is not None:
+            self.layer.shared.forward(self.x_shared, add=self.out, out=self.out, stream=stream)
         return self.out
 
     def routing(self):
