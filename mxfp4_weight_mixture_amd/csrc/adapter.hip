@@ -84,7 +84,7 @@ __global__ __launch_bounds__(256, 1) void shrink_runs_kernel(moe_adapter_args p,
       for (int f = 0; f < FN; ++f)
 #pragma unroll
         for (int q = 0; q < 16; ++q) acc[0][f][q] = 0.0f;
-      split_k_product<E, 1, FN, NST>(a, b, p.K, wave, lane, ring, acc);
+      split_k_product<E, 1, FN, NST, 32>(a, b, p.K, wave, lane, ring, acc);
       put_sums<1, FN>(ring, lane, acc);
       __syncthreads();
       const int row = threadIdx.x / (4 * FN), x = threadIdx.x % (4 * FN), t = t0 + row, r = r0 + 8 * x;

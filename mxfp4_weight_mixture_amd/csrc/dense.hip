@@ -49,9 +49,20 @@ moe_status launch_tiles(const DenseJob& j, hipStream_t s) {
 template <typename E>
 moe_status launch_small(const DenseJob& j, hipStream_t s) {
   const dim3 grid((unsigned)tiles(j, 64, 64)), block(256);
-#define MXMOE_LAUNCH(TA, TB, EPI, LORA) hipLaunchKernelGGL((small_kernel<E, TA, TB, EPI, LORA>), grid, block, 0, s, j)
-  MXMOE_DENSE_FORMS(MXMOE_LAUNCH);
+  if (j.K >= 4096 && !j.tb) {   // long rows: stages of 64 k
+#define MXMOE_LAUNCH(TA, TB, EPI, LORA) \
+  hipLaunchKernelGGL((small_kernel<E, TA, TB, EPI, LORA, 64>), grid, block, 0, s, j)
+    if (j.epi == kEpiGate && j.ids) MXMOE_LAUNCH(false, false, kEpiGate, true);
+    else if (j.epi == kEpiGate) MXMOE_LAUNCH(false, false, kEpiGate, false);
+    else if (j.ids) MXMOE_LAUNCH(false, false, kEpiPlain, true);
+    else MXMOE_LAUNCH(false, false, kEpiPlain, false);
 #undef MXMOE_LAUNCH
+  } else {
+#define MXMOE_LAUNCH(TA, TB, EPI, LORA) \
+  hipLaunchKernelGGL((small_kernel<E, TA, TB, EPI, LORA, 32>), grid, block, 0, s, j)
+    MXMOE_DENSE_FORMS(MXMOE_LAUNCH);
+#undef MXMOE_LAUNCH
+  }
   MXMOE_HIP(hipGetLastError());
   return MOE_OK;
 }
@@ -97,9 +108,6 @@ moe_status launch_typed(const DenseJob& j, void* ws, hipStream_t s) {
     return wide ? launch_few<E, 4, 2, true, 1>(j, s) : launch_few<E, 4, 1, true, 1>(j, s);
   }
   // (a decode batch's mixed adapters are the small kernel's)
-#ifdef FORCE_TILE
-  return g_force ? launch_tiles<E>(j, s) : launch_small<E>(j, s);
-#endif
   if (j.ids && j.K == 0 && j.M > kFewTokens) {
     hipLaunchKernelGGL((adapters_only_kernel<E>), dim3((unsigned)tiles(j, 64, 128)), dim3(256), 0, s, j);
     MXMOE_HIP(hipGetLastError());

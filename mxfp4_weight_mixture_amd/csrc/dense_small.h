@@ -2,13 +2,17 @@
 //
 // Where few tiles exist a block's time is the latency of its K loop, and
 // barriers between short stages are most of it.  Here no wave waits for
-// another before the end: wave w takes the 32-deep stages w, w + 4, ..., with a
+// another before the end: wave w takes the BK-deep stages w, w + 4, ..., with a
 // DMA ring of its own, and holds the whole 64 x 64 tile (2 x 2 fragments of
-// 32x32x16); the four sums meet in the LDS.  Bound by the L2 -> LDS rate, 8 KB
-// per stage at about 50 bytes a clock and CU: 164 clocks, against 64 of matrix
-// work.  A ring of two stages a wave leaves room for two blocks per CU, which
-// measured faster than one block with rings of four (64 KB of LDS each way in
-// flight: 512 x 4096 x 4096 32 against 34 us, 1552 x 1096 x 517 9.0 against 11.9).
+// 32x32x16); the four sums meet in the LDS.  Bound by the L2 -> LDS path: 8 KB
+// per 32 k against 64 clocks of matrix work, at 25 to 30 bytes a clock and CU
+// (50 where every line hits and nothing else runs).
+// A ring of two 32-deep stages a wave leaves room for two blocks per CU, which
+// measured faster than rings of four and one block (512 x 4096 x 4096 32
+// against 34 us, 1552 x 1096 x 517 9.0 against 11.9).  Long rows do better in
+// stages of 64 k, a whole line per row and load (192 x 4096 x 4096 15.0 against
+// 17.4 us, 100 x 7168 x 7168 22.4 against 27.0), short ones do not (517 x 1096
+// x 1552 8.7 against 8.2).
 //
 // Adapters: each thread adds its row's low-rank product to its eight columns,
 // so mixed adapters cost no more than equal ones.
@@ -37,54 +41,67 @@ __device__ __forceinline__ void add_low_rank(F8& v, const float* s, const E* lb,
 
 // This wave's share of a K loop: stages wave, wave + 4, ... of 32 k, through a
 // ring of NST stages of its own.  acc[fm][fn] += A fragments x B fragments.
-template <typename E, int FM, int FN, int NST, typename A, typename B>
+template <typename E, int FM, int FN, int NST, int BK, typename A, typename B>
 __device__ __forceinline__ void split_k_product(const A& a, const B& b, int K, int wave, int lane, char* ring,
                                                 v16f (&acc)[FM][FN]) {
   typedef typename Vec<E>::v8 v8;
   constexpr int STAGE = A::BYTES + B::BYTES, LOADS = A::LOADS + B::LOADS;
   static_assert(NST % 2 == 0, "fragment registers alternate by turn");
-  const int turns = ((K + kBK - 1) / kBK - wave + 3) >> 2;
-  auto issue = [&](int t, int buf) {
-    const int s = wave + 4 * t;
-#pragma unroll
-    for (int j = 0; j < A::LOADS; ++j) a.issue(j, s, K, 0, ring + buf * STAGE);
-#pragma unroll
-    for (int j = 0; j < B::LOADS; ++j) b.issue(j, s, K, 0, ring + buf * STAGE + A::BYTES);
+  constexpr int KS = BK / 16;
+  const int turns = ((K + BK - 1) / BK - wave + 3) >> 2;
+  auto issue = [&](int j, int t, int buf) {
+    if (j < A::LOADS) a.issue(j, wave + 4 * t, K, 0, ring + buf * STAGE);
+    else b.issue(j - A::LOADS, wave + 4 * t, K, 0, ring + buf * STAGE + A::BYTES);
   };
-  v8 fa[2][2][FM], fb[2][2][FN];   // [turn parity][k step][fragment]
-  auto read = [&](int buf, int d) {
-#pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
-#pragma unroll
-      for (int f = 0; f < FM; ++f) fa[d][ks][f] = A::frag(ring + buf * STAGE, f * 32, ks, lane);
-#pragma unroll
-      for (int f = 0; f < FN; ++f) fb[d][ks][f] = B::frag(ring + buf * STAGE + A::BYTES, f * 32, ks, lane);
-    }
+  v8 fa[2][KS][FM], fb[2][KS][FN];   // [turn parity][k step][fragment]
+  constexpr int NR = KS * (FM + FN), MF = KS / 2 * FM * FN, EARLY = LOADS / 2;
+  auto read = [&](int r, int buf, int d) {
+    const int ks = r / (FM + FN), f = r % (FM + FN);
+    if (f < FN) fb[d][ks][f] = B::frag(ring + buf * STAGE + A::BYTES, f * 32, ks, lane);
+    else fa[d][ks][f - FN] = A::frag(ring + buf * STAGE, (f - FN) * 32, ks, lane);
   };
 #pragma unroll
-  for (int t = 0; t < NST; ++t) issue(t, t);
+  for (int t = 0; t < NST; ++t)
+#pragma unroll
+    for (int j = 0; j < LOADS; ++j) issue(j, t, t);
   wait_vm<(NST - 1) * LOADS>();
   __builtin_amdgcn_sched_barrier(0);
-  read(0, 0);
+#pragma unroll
+  for (int r = 0; r < NR; ++r) read(r, 0, 0);
+  auto product = [&](int d, int i) {
+    const int ks = i / (FM * FN), fm = i % FM, fn = i % (FM * FN) / FM;
+    acc[fm][fn] = mfma32(fb[d][ks][fn], fa[d][ks][fm], acc[fm][fn]);
+  };
   // NST turns per step without a way out: turns past the end read zeros
   for (int t0 = 0; t0 < turns; t0 += NST) {
 #pragma unroll
     for (int u = 0; u < NST; ++u) {
-      // this turn is in registers: its buffer takes turn t + NST, and the next
-      // turn, which has landed, is read beside the products
+      // This turn is in registers, so its buffer takes turn t + NST: half the
+      // DMA beside the first half's products, half beside the second's, and
+      // there the next turn, which has landed by then, is read as well.
       wait_lgkm0();
       __builtin_amdgcn_sched_barrier(0);
-      issue(t0 + u + NST, u);
-      wait_vm<(NST - 1) * LOADS>();
-      __builtin_amdgcn_sched_barrier(0);
-      read((u + 1) % NST, (u + 1) & 1);
+#pragma unroll
+      for (int i = 0; i < MF; ++i) {
+        product(u & 1, i);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int j = EARLY * i / MF; j < EARLY * (i + 1) / MF; ++j) issue(j, t0 + u + NST, u);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      wait_vm<(NST - 2) * LOADS + EARLY>();
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int ks = 0; ks < 2; ++ks)
+      for (int i = 0; i < MF; ++i) {
+        product(u & 1, MF + i);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int f = 0; f < FM * FN; ++f)
-          acc[f % FM][f / FM] = mfma32(fb[u & 1][ks][f / FM], fa[u & 1][ks][f % FM], acc[f % FM][f / FM]);
-      __builtin_amdgcn_sched_barrier(0);
+        for (int r = NR * i / MF; r < NR * (i + 1) / MF; ++r) read(r, (u + 1) % NST, (u + 1) & 1);
+#pragma unroll
+        for (int j = EARLY + (LOADS - EARLY) * i / MF; j < EARLY + (LOADS - EARLY) * (i + 1) / MF; ++j)
+          issue(j, t0 + u + NST, u);
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
   }
   wait_vm<0>();
@@ -127,22 +144,20 @@ __device__ __forceinline__ F8 get_sum8(const char* areas, int area_bytes, int ro
   return r;
 }
 
-constexpr int kSmallLds = 64 << 10;
+constexpr int split_k_lds(int BK) { return BK == 32 ? 64 << 10 : 128 << 10; }
 
-// The C tile of block `block` of `blocks`.
-template <typename E, bool TA, bool TB, int EPI, bool LORA>
-__device__ __forceinline__ void small_tile(const DenseJob& p, int block, int blocks, char* lds) {
-  using A = Operand<E, 64, TA, 1>;
-  using B = Operand<E, 64, TB, 1>;
+// The C tile of 64 rows from m0 and the nt-th 64 columns of B.
+template <typename E, bool TA, bool TB, int EPI, bool LORA, int BK>
+__device__ __forceinline__ void split_k_tile(const DenseJob& p, int m0, int nt, char* lds) {
   constexpr int NST = 2;
+  using A = Operand<E, 64, TA, 1, BK>;
+  using B = Operand<E, 64, TB, 1, BK>;
   constexpr int STAGE = A::BYTES + B::BYTES;
-  constexpr int TILE = 64 * 64 * 4, RING = NST * STAGE > TILE ? NST * STAGE : TILE;
-  static_assert(4 * RING <= kSmallLds, "LDS of a tile");
+  constexpr int AREA = 64 * 64 * 4, RING = NST * STAGE > AREA ? NST * STAGE : AREA;
+  static_assert(4 * RING <= split_k_lds(BK), "LDS of a tile");
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int cols = EPI == kEpiGate ? 32 : 64, width = EPI == kEpiGate ? p.N >> 1 : p.N;
-  int mt, nt;
-  tile_at(xcd_run(block, blocks), (p.M + 63) >> 6, (width + cols - 1) / cols, &mt, &nt);
-  const int m0 = mt * 64, n0 = nt * cols;
+  const int n0 = nt * cols;
 
   A a;
   B b;
@@ -155,19 +170,23 @@ __device__ __forceinline__ void small_tile(const DenseJob& p, int block, int blo
 #pragma unroll
     for (int q = 0; q < 16; ++q) acc[i >> 1][i & 1][q] = 0.0f;
   char* const ring = lds + wave * RING;
-  split_k_product<E, 2, 2, NST>(a, b, p.K, wave, lane, ring, acc);
-  put_sums<2, 2>(ring, lane, acc);
-  __syncthreads();
-  auto sum8 = [&](int row, int c) { return get_sum8<2>(lds, RING, row, c); };
+  split_k_product<E, 2, 2, NST, BK>(a, b, p.K, wave, lane, ring, acc);
   // an adapter's rank, 0 for none
   auto rank_of = [&](int id) {
     if (id < 0 || id >= p.num_adapters) return 0;
     return p.ranks ? min(max(p.ranks[id], 0), p.R) : p.R;
   };
-  if constexpr (EPI == kEpiGate) {
-    const int row = threadIdx.x >> 2, x = threadIdx.x & 3, m = m0 + row, i = n0 + x * 8;
-    if (m < p.M && i < width) {
-      F8 gt = sum8(row, 2 * x), up = sum8(row, 8 + 2 * x);
+  put_sums<2, 2>(ring, lane, acc);
+  __syncthreads();
+  // units of eight columns (eight gate and eight up columns) of a row
+  constexpr int PER = EPI == kEpiGate ? 4 : 8;
+#pragma unroll
+  for (int it = 0; it < 64 * PER / 256; ++it) {
+    const int unit = it * 256 + threadIdx.x, row = unit / PER, x = unit % PER, m = m0 + row;
+    if constexpr (EPI == kEpiGate) {
+      const int blk = x >> 2, c = blk * 16 + (x & 3) * 2, i = n0 + x * 8;
+      if (m >= p.M || i >= width) continue;
+      F8 gt = get_sum8<2>(lds, RING, row, c), up = get_sum8<2>(lds, RING, row, c + 8);
       if constexpr (LORA) {
         const int id = p.ids[m], rank = rank_of(id);
         if (rank > 0) {
@@ -179,21 +198,18 @@ __device__ __forceinline__ void small_tile(const DenseJob& p, int block, int blo
         }
       }
       finish_gate<E>(p, m, i, gt, up);
-    }
-  } else {
-#pragma unroll
-    for (int it = 0; it < 2; ++it) {
-      const int row = it * 32 + (threadIdx.x >> 3), x = threadIdx.x & 7, m = m0 + row, n = n0 + x * 8;
+    } else {
+      const int n = n0 + x * 8;
       if (m >= p.M || n >= width) continue;
-      F8 v = sum8(row, 2 * x);
+      F8 v = get_sum8<2>(lds, RING, row, 2 * x);
       if constexpr (EPI == kEpiGateGrad) {
         finish_gate_grad<E>(p, m, n, v);
       } else {
         if constexpr (LORA) {
           const int id = p.ids[m], rank = rank_of(id);
           if (rank > 0)
-            add_low_rank<E>(v, p.s + (size_t)m * p.R, static_cast<const E*>(p.lb) + ((size_t)id * p.N + n) * p.R, p.R,
-                            rank);
+            add_low_rank<E>(v, p.s + (size_t)m * p.R, static_cast<const E*>(p.lb) + ((size_t)id * p.N + n) * p.R,
+                            p.R, rank);
         }
         finish_plain<E>(p, m, n, v);
       }
@@ -201,10 +217,19 @@ __device__ __forceinline__ void small_tile(const DenseJob& p, int block, int blo
   }
 }
 
-template <typename E, bool TA, bool TB, int EPI, bool LORA>
-__global__ __launch_bounds__(256, 2) void small_kernel(DenseJob p) {
-  __shared__ __attribute__((aligned(1024))) char lds[kSmallLds];
-  small_tile<E, TA, TB, EPI, LORA>(p, blockIdx.x, gridDim.x, lds);
+// The C tile of block `block` of `blocks`.
+template <typename E, bool TA, bool TB, int EPI, bool LORA, int BK>
+__device__ __forceinline__ void split_k_block(const DenseJob& p, int block, int blocks, char* lds) {
+  const int cols = EPI == kEpiGate ? 32 : 64, width = EPI == kEpiGate ? p.N >> 1 : p.N;
+  int mt, nt;
+  tile_at(xcd_run(block, blocks), (p.M + 63) >> 6, (width + cols - 1) / cols, &mt, &nt);
+  split_k_tile<E, TA, TB, EPI, LORA, BK>(p, mt * 64, nt, lds);
+}
+
+template <typename E, bool TA, bool TB, int EPI, bool LORA, int BK>
+__global__ __launch_bounds__(256, BK == 32 ? 2 : 1) void small_kernel(DenseJob p) {
+  __shared__ __attribute__((aligned(1024))) char lds[split_k_lds(BK)];
+  split_k_block<E, TA, TB, EPI, LORA, BK>(p, blockIdx.x, gridDim.x, lds);
 }
 
 // Independent products in one launch: their few blocks share the chip, and
@@ -217,11 +242,11 @@ struct SmallGroup {
 };
 template <typename E>
 __global__ __launch_bounds__(256, 2) void small_group_kernel(SmallGroup g) {
-  __shared__ __attribute__((aligned(1024))) char lds[kSmallLds];
+  __shared__ __attribute__((aligned(1024))) char lds[split_k_lds(32)];
   const int b = blockIdx.x, i = b >= g.start[2] ? 2 : b >= g.start[1] ? 1 : 0, block = b - g.start[i];
   if (block >= g.tiles[i]) return;
-  if (g.job[i].ta) small_tile<E, true, true, kEpiPlain, false>(g.job[i], block, g.tiles[i], lds);
-  else small_tile<E, false, true, kEpiPlain, false>(g.job[i], block, g.tiles[i], lds);
+  if (g.job[i].ta) split_k_block<E, true, true, kEpiPlain, false, 32>(g.job[i], block, g.tiles[i], lds);
+  else split_k_block<E, false, true, kEpiPlain, false, 32>(g.job[i], block, g.tiles[i], lds);
 }
 
 }  // namespace

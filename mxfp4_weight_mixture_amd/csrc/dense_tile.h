@@ -60,9 +60,11 @@ __device__ __forceinline__ void b_block(const DenseJob& p, int nt, int bn, int j
 
 // One operand's way from memory to the products: DMA of a stage, fragment reads.
 // ROWS: rows of the tile; T: stored [K][rows]; PARTS: waves that share a stage's loads.
-template <typename E, int ROWS, bool T, int PARTS>
+// BK: k per stage, 32 or 64.
+template <typename E, int ROWS, bool T, int PARTS, int BK = kBK>
 struct Operand {
-  static constexpr int BYTES = ROWS * kBK * 2;            // of a stage
+  static constexpr int BYTES = ROWS * BK * 2;             // of a stage
+  static constexpr int CPR = T ? ROWS / 8 : BK / 8;       // 16-byte chunks per stored row
   static constexpr int LOADS = BYTES / 1024 / PARTS;      // DMA instructions per wave
   static_assert(LOADS >= 1, "at least 16 rows per wave");
   const char* base;      // of the tile's first row (or column), k = 0
@@ -72,6 +74,7 @@ struct Operand {
   uint32_t up_mask;      // loads that take up rows
   int kk;                // this lane's k within a stage (of its chunk, or its k-row of load 0)
 
+  static __device__ __forceinline__ int swz(int row) { return BK == 32 ? (row >> 2) & 3 : (row >> 1) & 7; }
   static __device__ __forceinline__ int swz_t(int k) { return ((k & 3) * 2) & (ROWS / 16 - 1); }
 
   // rows [r0, r0 + ROWS) of an operand with `rows` rows
@@ -80,19 +83,18 @@ struct Operand {
     up_off = 0;
     if constexpr (!T) {
       base = static_cast<const char*>(p) + (int64_t)r0 * ld * 2;
-      stage_step = kBK * 2;
-      const int c = (lane & 3) ^ ((lane >> 4) & 3);       // row = 16 j + lane / 4: (row / 4) % 4
-      kk = c * 8;
+      stage_step = BK * 2;
 #pragma unroll
       for (int j = 0; j < LOADS; ++j) {
-        const int r = (wave * LOADS + j) * 16 + (lane >> 2);
+        const int r = (wave * LOADS + j) * (64 / CPR) + lane / CPR;
+        const int c = (lane % CPR) ^ swz(r);
+        if (j == 0) kk = c * 8;
         off[j] = r0 + r < rows ? (uint32_t)(r * ld * 2 + c * 16) : kOut;
       }
     } else {
       // ROWS * 2 bytes per k-row; a load covers 1024 bytes of them
       base = static_cast<const char*>(p) + (int64_t)r0 * 2;
-      stage_step = (int64_t)kBK * ld * 2;
-      constexpr int CPR = ROWS / 8;                       // 16-byte chunks per k-row
+      stage_step = (int64_t)BK * ld * 2;
       const int slot = lane % CPR;
       kk = (wave * LOADS) * (64 / CPR) + lane / CPR;
 #pragma unroll
@@ -107,16 +109,16 @@ struct Operand {
   __device__ __forceinline__ void init_gate(const DenseJob& p, int nt, int wave, int lane) {
     const int I = p.N >> 1, i0 = nt * (ROWS / 2);
     base = static_cast<const char*>(p.b) + (int64_t)i0 * p.ldb * 2 * (p.interleaved ? 2 : 1);
-    stage_step = kBK * 2;
+    stage_step = BK * 2;
     up_off = p.interleaved ? p.ldb * 2 : (int64_t)I * p.ldb * 2;
     up_mask = 0;
-    const int c = (lane & 3) ^ ((lane >> 4) & 3);
-    kk = c * 8;
 #pragma unroll
     for (int j = 0; j < LOADS; ++j) {
-      const int r16 = wave * LOADS + j;                   // 16-row group: four per gate/up block pair
-      const int i = (r16 >> 2) * 32 + (r16 & 1) * 16 + (lane >> 2);
-      if (r16 & 2) up_mask |= 1u << j;
+      const int first = (wave * LOADS + j) * (64 / CPR), r = first + lane / CPR;
+      const int c = (lane % CPR) ^ swz(r);
+      if (j == 0) kk = c * 8;
+      const int i = (first >> 6) * 32 + (r & 31);         // 64-row groups: 32 gate rows, 32 up rows
+      if (first & 32) up_mask |= 1u << j;
       off[j] = i0 + i < I ? (uint32_t)(i * p.ldb * 2 * (p.interleaved ? 2 : 1) + c * 16) : kOut;
     }
   }
@@ -124,8 +126,9 @@ struct Operand {
   __device__ __forceinline__ void issue(int j, int s, int K, int wave, char* buf) const {
     const char* b = base + s * stage_step + ((up_mask >> j) & 1 ? up_off : 0);
     int k = kk;
-    if constexpr (T) k += j * (64 / (ROWS / 8));
-    const uint32_t o = k < K - s * kBK ? off[j] : kOut;
+    if constexpr (T) k += j * (64 / CPR);
+    else if (BK == 64 && (j & 1)) k ^= 32;                // swz(r) alternates by 8 rows
+    const uint32_t o = k < K - s * BK ? off[j] : kOut;
     dma16(rsrc_at(b), o, buf + (wave * LOADS + j) * 1024);
   }
   // fragment of rows [r, r + 32), k [16 ks, 16 ks + 16)
@@ -133,7 +136,7 @@ struct Operand {
     typedef typename Vec<E>::v8 v8;
     if constexpr (!T) {
       const int row = r + (lane & 31), c = 2 * ks + (lane >> 5);
-      return *reinterpret_cast<const v8*>(buf + row * 64 + ((c ^ ((row >> 2) & 3)) << 4));
+      return *reinterpret_cast<const v8*>(buf + row * (BK * 2) + ((c ^ swz(row)) << 4));
     } else {
       // 16-lane group q: columns 16 (q % 2), k half q / 2; lane i: k-row i / 4, columns 4 (i % 4)
       const int i = lane & 15, q = (lane >> 4) & 1, g = lane >> 5;
