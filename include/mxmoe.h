@@ -426,8 +426,8 @@ moe_status moe_layer_prefill_streamed(const moe_streamed_args* args, void* compu
  * Products accumulate in fp32, the gate is applied to the fp32 sums; h is
  * rounded once to `dtype` (the matrix cores' operand), out once to out_dtype.
  *
- * Sizes: T >= 0 (T == 0 enqueues nothing), H and I multiples of 8, both in
- * [8, 262144].  Row strides are in elements, multiples of 8, at least the row
+ * Sizes: 0 <= T <= 2^28 (T == 0 enqueues nothing), H and I multiples of 8, both
+ * in [8, 262144], T rows of max(H, 2I) fewer than 2^24 tiles of 64 x 64.  Row strides are in elements, multiples of 8, at least the row
  * and at most 2^21; every pointer is 16-byte aligned.  w1, w2 and gate_up are
  * contiguous.  `out` may be `add` itself (same pointer and stride); apart
  * from that no output may overlap an input or another output. */
@@ -498,9 +498,14 @@ moe_status moe_gated_ffn_backward(const moe_ffn_grad_args* args, void* stream);
  * A token's result depends on its own row and adapter only: infinities or NaN
  * in one adapter or token do not reach the others.
  * The low-rank row scales[a] * x A^T is held in fp32 and enters the second
- * product as the sum of two numbers of type `dtype`.
+ * product as it is, or (batches of more than 256 tokens) as the sum of two
+ * numbers of type `dtype`: with fp16 its magnitude must stay below 65504 there.
  *
- * Sizes: T >= 0 (T == 0 enqueues nothing), K, N multiples of 8 in [8, 262144],
+ * Any order of tokens gives the same results; batches of more than 256 tokens
+ * are fastest where the tokens of a request stand together, as prompts do.
+ *
+ * Sizes: 0 <= T <= 2^28 (T == 0 enqueues nothing), K, N multiples of 8 in
+ * [8, 262144], T rows of N fewer than 2^24 tiles of 64 x 64,
  * N % 16 == 0 for SWIGLU; 0 <= num_adapters <= 65536; R a multiple of 8 in
  * [8, 256].  Strides, alignment and overlap as for moe_gated_ffn_forward
  * (ids, scales and ranks: 4-byte aligned).  With a SWIGLU epilogue add has N

@@ -111,16 +111,8 @@ moe_status launch_shrink(const moe_adapter_args& a, float* s, hipStream_t st) {
   return MOE_OK;
 }
 
-struct AdapterWs {
-  size_t s, gemm, total;
-};
-AdapterWs adapter_ws(int T, int K, int N, int R) {
-  AdapterWs w;
-  w.s = 0;
-  w.gemm = align_up((size_t)T * R * 4, 256);
-  w.total = w.gemm + dense_ws_bytes(T, N, K) + 256;
-  return w;
-}
+// Workspace: s.
+size_t adapter_ws_bytes(int T, int R) { return (size_t)T * R * 4 + 256; }
 
 }  // namespace
 }  // namespace mxmoe
@@ -131,16 +123,16 @@ extern "C" {
 
 size_t moe_adapter_workspace_size(int32_t T, int32_t K, int32_t N, int32_t num_adapters, int32_t R) {
   if (T < 0 || K < 1 || N < 1 || num_adapters < 0 || R < 1) return 0;
-  return adapter_ws(T, K, N, R).total;
+  return adapter_ws_bytes(T, R);
 }
 
 moe_status moe_adapter_linear(const moe_adapter_args* a, void* stream) {
   const char* what = "adapter projection";
   clear_error();
   if (!a) return fail(MOE_ERR_INVALID_ARG, "%s: null args", what);
-  if (a->T < 0) return fail(MOE_ERR_SHAPE, "%s: T = %d < 0", what, a->T);
   MXMOE_TRY(check_width(what, "K", a->K));
   MXMOE_TRY(check_width(what, "N", a->N));
+  MXMOE_TRY(check_tokens(what, a->T, a->N));
   if (a->num_adapters < 0 || a->num_adapters > 65536)
     return fail(MOE_ERR_SHAPE, "%s: num_adapters = %d outside [0, 65536]", what, a->num_adapters);
   if (a->R < 8 || a->R > 256 || a->R % 8)
@@ -158,19 +150,19 @@ moe_status moe_adapter_linear(const moe_adapter_args* a, void* stream) {
   MXMOE_TRY(check_stride(what, "x_stride", a->x_stride, K));
   MXMOE_TRY(check_stride(what, "out_stride", a->out_stride, n_out));
   if (a->add) MXMOE_TRY(check_stride(what, "add_stride", a->add_stride, N));
-  const AdapterWs w = adapter_ws(a->T, a->K, a->N, a->R);
+  const size_t need = adapter_ws_bytes(a->T, a->R);
   if (T > 0) {
     if (!a->x || !a->out || (n > 0 && (!a->ids || !a->a || !a->b)))
       return fail(MOE_ERR_INVALID_ARG, "%s: null pointer", what);
-    if (!a->workspace || a->workspace_bytes < w.total)
-      return fail(MOE_ERR_WORKSPACE, "%s: workspace %zu bytes, need %zu", what, a->workspace_bytes, w.total);
+    if (!a->workspace || a->workspace_bytes < need)
+      return fail(MOE_ERR_WORKSPACE, "%s: workspace %zu bytes, need %zu", what, a->workspace_bytes, need);
     const void* words[] = {a->ids, a->scales, a->ranks};
     for (const void* p : words)
       if (reinterpret_cast<uintptr_t>(p) & 3)
         return fail(MOE_ERR_INVALID_ARG, "%s: ids, scales and ranks must be 4-byte aligned", what);
     const bool in_place = !gate && a->add == a->out && a->add_stride == a->out_stride;
     const Span out[] = {span("out", a->out, T, n_out, a->out_stride, a->out_dtype),
-                        {"workspace", a->workspace, w.total}};
+                        {"workspace", a->workspace, need}};
     const Span in[] = {span("x", a->x, T, K, a->x_stride, a->dtype), span("w", a->w, N, K, K, a->dtype),
                        span("a", a->a, n * R, K, K, a->dtype), span("b", a->b, n * N, R, R, a->dtype),
                        span("add", in_place ? nullptr : a->add, T, N, a->add_stride, a->out_dtype)};
@@ -183,7 +175,6 @@ moe_status moe_adapter_linear(const moe_adapter_args* a, void* stream) {
   }
   MXMOE_TRY(check_device());
   if (T == 0) return MOE_OK;
-  uint8_t* ws = static_cast<uint8_t*>(a->workspace);
   const hipStream_t s = (hipStream_t)stream;
 
   DenseJob j{};
@@ -197,13 +188,13 @@ moe_status moe_adapter_linear(const moe_adapter_args* a, void* stream) {
   j.add = a->add, j.ldadd = a->add_stride;
   j.c = a->out, j.ldc = a->out_stride, j.c_dtype = a->out_dtype;
   if (n > 0) {
-    float* const low = reinterpret_cast<float*>(ws + w.s);
+    float* const low = static_cast<float*>(a->workspace);
     MXMOE_TRY(a->dtype == MOE_FLOAT_BF16 ? launch_shrink<__bf16>(*a, low, s) : launch_shrink<_Float16>(*a, low, s));
     j.ids = a->ids, j.ranks = a->ranks;
     j.s = low, j.lb = a->b;
     j.num_adapters = a->num_adapters, j.R = a->R;
   }
-  return launch_dense(j, ws + w.gemm, s);
+  return launch_dense(j, s);
 }
 
 }  // extern "C"

@@ -41,14 +41,14 @@ struct DenseJob {
 // on its neighbours'.)
 constexpr int kFewTokens = 256;
 
-size_t dense_ws_bytes(int M, int N, int K);
-moe_status launch_dense(const DenseJob& j, void* ws, hipStream_t s);
+moe_status launch_dense(const DenseJob& j, hipStream_t s);
 // Up to three independent plain products of one type with B stored [K][N].
-moe_status launch_dense_group(const DenseJob* jobs, int n, void* ws, hipStream_t s);
+moe_status launch_dense_group(const DenseJob* jobs, int n, hipStream_t s);
 
 // ---- argument checks shared by the entry points -------------------------
 constexpr int kMaxWidth = 1 << 18;
-constexpr int64_t kMaxStride = 1 << 21;
+constexpr int64_t kMaxStride = 1 << 21;   // 256 rows of it stay below 2^31 bytes
+constexpr int kMaxTokens = 1 << 28;
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 inline size_t float_bytes(int dtype) { return dtype == MOE_FLOAT_FP32 ? 4 : 2; }
@@ -85,6 +85,14 @@ inline moe_status check_spans(const char* what, const Span* out, int n_out, cons
 inline moe_status check_width(const char* what, const char* name, int v) {
   if (v < 8 || v > kMaxWidth || v % 8)
     return fail(MOE_ERR_SHAPE, "%s: %s = %d must be a multiple of 8 in [8, %d]", what, name, v, kMaxWidth);
+  return MOE_OK;
+}
+// T rows of at most `cols` columns: a grid of 64 x 64 tiles stays below 2^24
+// blocks (2^32 threads).
+inline moe_status check_tokens(const char* what, int T, int64_t cols) {
+  if (T < 0) return fail(MOE_ERR_SHAPE, "%s: T = %d < 0", what, T);
+  if (T > kMaxTokens || ((int64_t)T + 63) / 64 * ((cols + 63) / 64) >= 1 << 24)
+    return fail(MOE_ERR_SHAPE, "%s: T = %d rows of %lld are too many for one launch", what, T, (long long)cols);
   return MOE_OK;
 }
 inline moe_status check_stride(const char* what, const char* name, int64_t stride, int64_t cols) {

@@ -95,7 +95,7 @@ bool small_is_faster(const DenseJob& j) {
 }
 
 template <typename E>
-moe_status launch_typed(const DenseJob& j, void* ws, hipStream_t s) {
+moe_status launch_typed(const DenseJob& j, hipStream_t s) {
   // (the few-row kernel addresses a block's rows with 31 bits from the first;
   // a split gate's up rows lie I rows behind)
   const int64_t reach = j.epi == kEpiGate ? (int64_t)(j.N / 2 + 16) * j.ldb * 2 : 0;
@@ -135,14 +135,12 @@ moe_status launch_group_typed(const DenseJob* jobs, int n, hipStream_t s) {
 
 }  // namespace
 
-size_t dense_ws_bytes(int M, int N, int K) { return 0; }
-
-moe_status launch_dense(const DenseJob& j, void* ws, hipStream_t s) {
+moe_status launch_dense(const DenseJob& j, hipStream_t s) {
   if (j.M == 0) return MOE_OK;
-  return j.dtype == MOE_FLOAT_BF16 ? launch_typed<__bf16>(j, ws, s) : launch_typed<_Float16>(j, ws, s);
+  return j.dtype == MOE_FLOAT_BF16 ? launch_typed<__bf16>(j, s) : launch_typed<_Float16>(j, s);
 }
 
-moe_status launch_dense_group(const DenseJob* jobs, int n, void* ws, hipStream_t s) {
+moe_status launch_dense_group(const DenseJob* jobs, int n, hipStream_t s) {
   // one launch where each would run in 64 x 64 tiles that leave CUs idle
   int64_t blocks = 0;
   bool small = n > 1;
@@ -153,7 +151,7 @@ moe_status launch_dense_group(const DenseJob* jobs, int n, void* ws, hipStream_t
   if (small && blocks <= 8 * (int64_t)num_cus())
     return jobs[0].dtype == MOE_FLOAT_BF16 ? launch_group_typed<__bf16>(jobs, n, s)
                                            : launch_group_typed<_Float16>(jobs, n, s);
-  for (int i = 0; i < n; ++i) MXMOE_TRY(launch_dense(jobs[i], ws, s));
+  for (int i = 0; i < n; ++i) MXMOE_TRY(launch_dense(jobs[i], s));
   return MOE_OK;
 }
 

@@ -13,9 +13,9 @@ namespace mxmoe {
 namespace {
 
 moe_status check_block(const char* what, int T, int H, int I, int layout, int act, int dtype) {
-  if (T < 0) return fail(MOE_ERR_SHAPE, "%s: T = %d < 0", what, T);
   MXMOE_TRY(check_width(what, "H", H));
   MXMOE_TRY(check_width(what, "I", I));
+  MXMOE_TRY(check_tokens(what, T, std::max(H, 2 * I)));
   if (layout != MOE_EPI_SWIGLU_SPLIT && layout != MOE_EPI_SWIGLU_INTERLEAVED)
     return fail(MOE_ERR_INVALID_ARG, "%s: layout %d must be a SWIGLU epilogue", what, layout);
   if (act != MOE_GATE_SILU && act != MOE_GATE_GELU)
@@ -23,31 +23,10 @@ moe_status check_block(const char* what, int T, int H, int I, int layout, int ac
   return check_dtype16(what, dtype);
 }
 
-// Workspace: h, then the products' own scratch (they run one after the other).
-struct FfnWs {
-  size_t h, gemm, total;
-};
-FfnWs ffn_ws(int T, int H, int I) {
-  FfnWs w;
-  w.h = 0;
-  w.gemm = align_up((size_t)T * I * 2, 256);
-  w.total = w.gemm + std::max(dense_ws_bytes(T, 2 * I, H), dense_ws_bytes(T, H, I)) + 256;
-  return w;
-}
-
-struct GradWs {
-  size_t dgu, h, gemm, total;
-};
-GradWs grad_ws(int T, int H, int I) {
-  GradWs w;
-  w.dgu = 0;
-  w.h = align_up((size_t)T * 2 * I * 2, 256);
-  w.gemm = w.h + align_up((size_t)T * I * 2, 256);
-  w.total = w.gemm + 256 +
-            std::max(std::max(dense_ws_bytes(T, I, H), dense_ws_bytes(T, H, 2 * I)),
-                     std::max(dense_ws_bytes(2 * I, H, T), dense_ws_bytes(H, I, T)));
-  return w;
-}
+// Workspaces: h; for the gradients d_gate_up, then h.
+size_t ffn_ws_bytes(int T, int I) { return (size_t)T * I * 2 + 256; }
+size_t grad_h_offset(int T, int I) { return align_up((size_t)T * 2 * I * 2, 256); }
+size_t grad_ws_bytes(int T, int I) { return grad_h_offset(T, I) + (size_t)T * I * 2 + 256; }
 
 }  // namespace
 }  // namespace mxmoe
@@ -58,7 +37,7 @@ extern "C" {
 
 size_t moe_gated_ffn_workspace_size(int32_t T, int32_t H, int32_t I) {
   if (T < 0 || H < 1 || I < 1) return 0;
-  return ffn_ws(T, H, I).total;
+  return ffn_ws_bytes(T, I);
 }
 
 moe_status moe_gated_ffn_forward(const moe_ffn_args* a, void* stream) {
@@ -71,16 +50,16 @@ moe_status moe_gated_ffn_forward(const moe_ffn_args* a, void* stream) {
   MXMOE_TRY(check_stride(what, "x_stride", a->x_stride, a->H));
   MXMOE_TRY(check_stride(what, "out_stride", a->out_stride, a->H));
   if (a->add) MXMOE_TRY(check_stride(what, "add_stride", a->add_stride, a->H));
-  const FfnWs w = ffn_ws(a->T, a->H, a->I);
+  const size_t need = ffn_ws_bytes(a->T, a->I);
   if (a->T > 0) {
     if (!a->x || !a->w1 || !a->w2 || !a->out) return fail(MOE_ERR_INVALID_ARG, "%s: null pointer", what);
-    if (!a->workspace || a->workspace_bytes < w.total)
-      return fail(MOE_ERR_WORKSPACE, "%s: workspace %zu bytes, need %zu", what, a->workspace_bytes, w.total);
+    if (!a->workspace || a->workspace_bytes < need)
+      return fail(MOE_ERR_WORKSPACE, "%s: workspace %zu bytes, need %zu", what, a->workspace_bytes, need);
     const int64_t T = a->T, H = a->H, I = a->I;
     const bool in_place = a->add == a->out && a->add_stride == a->out_stride;
     const Span out[] = {span("out", a->out, T, H, a->out_stride, a->out_dtype),
                         span("gate_up", a->gate_up, T, 2 * I, 2 * I, a->save_dtype),
-                        {"workspace", a->workspace, w.total}};
+                        {"workspace", a->workspace, need}};
     const Span in[] = {span("x", a->x, T, H, a->x_stride, a->dtype), span("w1", a->w1, 2 * I, H, H, a->dtype),
                        span("w2", a->w2, H, I, I, a->dtype),
                        span("add", in_place ? nullptr : a->add, T, H, a->add_stride, a->out_dtype)};
@@ -100,23 +79,23 @@ moe_status moe_gated_ffn_forward(const moe_ffn_args* a, void* stream) {
   j.b = a->w1, j.ldb = a->H;
   j.N = 2 * a->I, j.K = a->H;
   j.epi = kEpiGate;
-  j.c = ws + w.h, j.ldc = a->I, j.c_dtype = a->dtype;
+  j.c = ws, j.ldc = a->I, j.c_dtype = a->dtype;
   j.gu = a->gate_up, j.gu_dtype = a->save_dtype;
-  MXMOE_TRY(launch_dense(j, ws + w.gemm, s));
+  MXMOE_TRY(launch_dense(j, s));
 
-  j.a = ws + w.h, j.lda = a->I;
+  j.a = ws, j.lda = a->I;
   j.b = a->w2, j.ldb = a->I;
   j.N = a->H, j.K = a->I;
   j.epi = kEpiPlain;
   j.gu = nullptr;
   j.add = a->add, j.ldadd = a->add_stride;
   j.c = a->out, j.ldc = a->out_stride, j.c_dtype = a->out_dtype;
-  return launch_dense(j, ws + w.gemm, s);
+  return launch_dense(j, s);
 }
 
 size_t moe_gated_ffn_grad_workspace_size(int32_t T, int32_t H, int32_t I) {
   if (T < 0 || H < 1 || I < 1) return 0;
-  return grad_ws(T, H, I).total;
+  return grad_ws_bytes(T, I);
 }
 
 moe_status moe_gated_ffn_backward(const moe_ffn_grad_args* a, void* stream) {
@@ -132,17 +111,17 @@ moe_status moe_gated_ffn_backward(const moe_ffn_grad_args* a, void* stream) {
   MXMOE_TRY(check_stride(what, "dout_stride", a->dout_stride, a->H));
   if (a->dw1) MXMOE_TRY(check_stride(what, "x_stride", a->x_stride, a->H));
   if (a->dx) MXMOE_TRY(check_stride(what, "dx_stride", a->dx_stride, a->H));
-  const GradWs w = grad_ws(a->T, a->H, a->I);
+  const size_t need = grad_ws_bytes(a->T, a->I);
   const int64_t T = a->T, H = a->H, I = a->I;
   if (T > 0) {
     if (!a->dout || !a->w2 || !a->gate_up || (a->dw1 && !a->x) || (a->dx && !a->w1))
       return fail(MOE_ERR_INVALID_ARG, "%s: null pointer", what);
-    if (!a->workspace || a->workspace_bytes < w.total)
-      return fail(MOE_ERR_WORKSPACE, "%s: workspace %zu bytes, need %zu", what, a->workspace_bytes, w.total);
+    if (!a->workspace || a->workspace_bytes < need)
+      return fail(MOE_ERR_WORKSPACE, "%s: workspace %zu bytes, need %zu", what, a->workspace_bytes, need);
   }
   const Span out[] = {span("dx", a->dx, T, H, a->dx_stride, a->dx_dtype),
                       span("dw1", a->dw1, 2 * I, H, H, a->dw_dtype), span("dw2", a->dw2, H, I, I, a->dw_dtype),
-                      {"workspace", a->workspace, T > 0 ? w.total : 0}};
+                      {"workspace", a->workspace, T > 0 ? need : 0}};
   const Span in[] = {span("dout", a->dout, T, H, a->dout_stride, a->dtype),
                      span("x", a->dw1 ? a->x : nullptr, T, H, a->x_stride, a->dtype),
                      span("w1", a->dx ? a->w1 : nullptr, 2 * I, H, H, a->dtype),
@@ -155,6 +134,7 @@ moe_status moe_gated_ffn_backward(const moe_ffn_grad_args* a, void* stream) {
   uint8_t* ws = static_cast<uint8_t*>(a->workspace);
   const hipStream_t s = (hipStream_t)stream;
 
+  uint8_t* const h = ws + grad_h_offset(a->T, a->I);
   DenseJob j{};
   j.dtype = a->dtype;
   j.act = a->gate_act;
@@ -165,9 +145,9 @@ moe_status moe_gated_ffn_backward(const moe_ffn_grad_args* a, void* stream) {
   j.M = a->T, j.N = a->I, j.K = a->H;
   j.epi = kEpiGateGrad;
   j.gu = const_cast<void*>(a->gate_up), j.gu_dtype = a->save_dtype;
-  j.c = ws + w.dgu, j.ldc = 2 * I, j.c_dtype = a->dtype;
-  j.h = ws + w.h;
-  MXMOE_TRY(launch_dense(j, ws + w.gemm, s));
+  j.c = ws, j.ldc = 2 * I, j.c_dtype = a->dtype;
+  j.h = h;
+  MXMOE_TRY(launch_dense(j, s));
 
   // what is asked for of dx, dw1 and dw2, independent of each other
   DenseJob jobs[3];
@@ -175,7 +155,7 @@ moe_status moe_gated_ffn_backward(const moe_ffn_grad_args* a, void* stream) {
   j.epi = kEpiPlain;
   j.gu = j.h = nullptr;
   if (a->dx) {
-    j.a = ws + w.dgu, j.lda = 2 * I;
+    j.a = ws, j.lda = 2 * I;
     j.b = a->w1, j.ldb = H, j.tb = 1;
     j.M = a->T, j.N = a->H, j.K = 2 * a->I;
     j.c = a->dx, j.ldc = a->dx_stride, j.c_dtype = a->dx_dtype;
@@ -187,7 +167,7 @@ moe_status moe_gated_ffn_backward(const moe_ffn_grad_args* a, void* stream) {
   j.K = a->T;
   j.c_dtype = a->dw_dtype;
   if (a->dw1) {
-    j.a = ws + w.dgu, j.lda = 2 * I;
+    j.a = ws, j.lda = 2 * I;
     j.b = a->x, j.ldb = a->x_stride;
     j.M = 2 * a->I, j.N = a->H;
     j.c = a->dw1, j.ldc = H;
@@ -196,13 +176,13 @@ moe_status moe_gated_ffn_backward(const moe_ffn_grad_args* a, void* stream) {
   }
   if (a->dw2) {
     j.a = a->dout, j.lda = a->dout_stride;
-    j.b = ws + w.h, j.ldb = I;
+    j.b = h, j.ldb = I;
     j.M = a->H, j.N = a->I;
     j.c = a->dw2, j.ldc = I;
     j.add = a->accumulate ? a->dw2 : nullptr, j.ldadd = I;
     jobs[n++] = j;
   }
-  MXMOE_TRY(launch_dense_group(jobs, n, ws + w.gemm, s));
+  MXMOE_TRY(launch_dense_group(jobs, n, s));
   return MOE_OK;
 }
 

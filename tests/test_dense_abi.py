@@ -40,6 +40,8 @@ def _refused(fn, args, status, needle):
 
 @pytest.mark.parametrize("kw,status,needle", [
     (dict(T=-1), "MOE_ERR_SHAPE", "T = -1"),
+    (dict(T=(1 << 28) + 1), "MOE_ERR_SHAPE", "too many"),
+    (dict(T=1 << 20, I=1 << 16, H=64), "MOE_ERR_SHAPE", "too many"),
     (dict(H=60), "MOE_ERR_SHAPE", "H = 60"),
     (dict(I=0), "MOE_ERR_SHAPE", "I = 0"),
     (dict(I=(1 << 18) + 8), "MOE_ERR_SHAPE", "I ="),
@@ -95,6 +97,7 @@ def test_ffn_gradient_refusals(kw, status, needle):
 
 @pytest.mark.parametrize("kw,status,needle", [
     (dict(T=-3), "MOE_ERR_SHAPE", "T = -3"),
+    (dict(T=1 << 22, N=1 << 16, out_stride=1 << 16), "MOE_ERR_SHAPE", "too many"),
     (dict(K=4), "MOE_ERR_SHAPE", "K = 4"),
     (dict(N=33), "MOE_ERR_SHAPE", "N = 33"),
     (dict(N=24, epilogue=1), "MOE_ERR_SHAPE", "multiple of 16"),
