@@ -394,6 +394,8 @@ class GatedFFN:
             a.add_stride = _rows("add", add, T, self.H, (out.dtype,), self.device)
             a.add = add.data_ptr()
         gate_up = None
+        if save not in (False, True, "half"):
+            raise ValueError(f"save is {save!r}, not False, True or 'half'")
         if save:
             gate_up = torch.empty((T, 2 * self.I), device=self.device,
                                   dtype=self.dtype if save == "half" else torch.float32)

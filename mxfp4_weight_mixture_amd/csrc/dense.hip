@@ -98,7 +98,7 @@ template <typename E>
 moe_status launch_typed(const DenseJob& j, hipStream_t s) {
   // (the few-row kernel addresses a block's rows with 31 bits from the first;
   // a split gate's up rows lie I rows behind)
-  const int64_t reach = j.epi == kEpiGate ? (int64_t)(j.N / 2 + 16) * j.ldb * 2 : 0;
+  const int64_t reach = j.epi == kEpiGate && !j.interleaved ? (int64_t)(j.N / 2 + 16) * j.ldb * 2 : 0;
   if (j.M <= 64 && j.epi != kEpiGateGrad && !j.ta && !j.tb && reach < (1ll << 30)) {
     const bool wide = (j.N + 15) / 16 > num_cus();
     // D: what the LDS holds (128 KB, for 16 rows 64 or 96)

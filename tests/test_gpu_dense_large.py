@@ -187,3 +187,48 @@ def test_offsets_past_32_bits():
     # against the smaller call, which may take other kernels: both are within a rounding of h and of out
     assert (out[:1000].double() - ref.double()).abs().max() <= 16 * du.u(BF) * ref.double().abs().max()
     assert (gu[:1000] - gref).abs().max() <= 2 * H * du.F32 * 64
+
+
+@pytest.mark.parametrize("T", [3, 20, 300])
+def test_up_rows_far_behind_the_gate_rows(T):
+    """w1 of 2 GiB: in the split order a gate row's up row lies 1 GiB behind it; the interleaved order of the
+    same weights keeps them together.  Both against float64 on some columns."""
+    H, I = 8192, 65536
+    w1 = torch.empty((2 * I, H), dtype=BF, device="cuda").normal_(0, H ** -0.5, generator=torch.Generator("cuda")
+                                                                  .manual_seed(1))
+    x = du.normal((T, H), 1.0, BF, 2)
+    cols = torch.tensor([0, 1, 31, 32, 33000, 65527, 65535], device="cuda")
+    pick = torch.zeros((H, I), dtype=BF, device="cuda")   # out[:, j] = h[:, cols[j]]
+    pick[torch.arange(len(cols)), cols] = 1.0
+    inter = torch.stack([w1[:I], w1[I:]], 1).reshape(2 * I, H)
+    g, up = mm(x.double(), w1[cols].double().t()), mm(x.double(), w1[I + cols].double().t())
+    h = g * torch.sigmoid(g) * up
+    e = H * du.F32 * (H ** 0.5) * 4   # sum |x w| of these spreads is below 0.64 sqrt(H) + 7 sigma < sqrt(H)
+    err = e * (1.1 * up.abs() + g.abs() + 4 * e) + du.u(BF) * h.abs()
+    for w, layout in ((w1, "split"), (inter, "interleaved")):
+        out = mx.GatedFFN(w, pick, layout=layout).forward(x)
+        _within(out[:, : len(cols)], h, err, layout)
+        assert not out[:, len(cols):].any()
+
+
+def test_16_bit_subnormals_count():
+    """Operands below the smallest normal number are not flushed to zero."""
+    K, N = 64, 16
+    for dtype, tiny in ((HF, 2.0 ** -20), (BF, 2.0 ** -130)):
+        for T in (1, 20, 300):
+            x = torch.full((T, K), tiny, dtype=dtype, device="cuda")
+            w = torch.full((N, K), 2.0, dtype=dtype, device="cuda")
+            none = mx.AdapterLinear(w, w.new_zeros((0, 8, K)), w.new_zeros((0, N, 8)))
+            assert (none.forward(x, torch.zeros(T, dtype=torch.int32, device="cuda"), out_dtype=F)
+                    == 2 * K * tiny).all(), (dtype, T)
+
+
+@pytest.mark.parametrize("T", [1, 40, 100, 700])
+def test_no_projection_and_no_adapter(T):
+    N, K = 136, 64
+    x, add = du.normal((T, K), 1.0, BF, 1), du.normal((T, N), 1.0, BF, 2)
+    ids = torch.full((T,), -1, dtype=torch.int32, device="cuda")
+    for n in (0, 2):
+        f = mx.AdapterLinear(None, x.new_full((n, 8, K), float("nan")), x.new_full((n, N, 8), float("nan")))
+        assert torch.equal(f.forward(x, ids, add=add), add)
+        assert not f.forward(x, ids).any()

@@ -193,6 +193,8 @@ def test_binding_refusals():
                         (dict(x=x, add=z(4, 64, device="cuda"), out_dtype=BF), "add is")):
         with pytest.raises(ValueError, match=needle):
             f.forward(**bad)
+    with pytest.raises(ValueError, match="save"):
+        f.forward(x, save="fp8")
     out, gu = f.forward(x, save=True)
     with pytest.raises(ValueError, match="gate_up"):
         f.backward(out, x, gu[:, :32])
