@@ -6,6 +6,8 @@
 // will), more for prompts (adapters in runs); either way any order is right.
 // Two launches: the first gives s [T][R] in fp32, the second the shared
 // projection with s B^T added to its fp32 sums and the epilogue.
+#include <algorithm>
+
 #include "dense_small.h"
 
 namespace mxmoe {
@@ -111,8 +113,20 @@ moe_status launch_shrink(const moe_adapter_args& a, float* s, hipStream_t st) {
   return MOE_OK;
 }
 
-// Workspace: s.
-size_t adapter_ws_bytes(int T, int R) { return (size_t)T * R * 4 + 256; }
+// Workspace: s, then the second product's scratch (the most that any form of
+// it takes).
+size_t adapter_gemm_offset(int T, int R) { return align_up((size_t)T * R * 4, 256); }
+size_t adapter_ws_bytes(int T, int K, int N, int R) {
+  size_t most = 0;
+  for (int epi : {(int)kEpiPlain, (int)kEpiGate})
+    for (bool ids : {false, true}) {
+      static const int32_t some = 0;
+      DenseJob j = dense_sizes(T, N, K, epi, 0, 0);
+      j.ids = ids ? &some : nullptr;
+      most = std::max(most, dense_ws_bytes(j));
+    }
+  return adapter_gemm_offset(T, R) + most + 256;
+}
 
 }  // namespace
 }  // namespace mxmoe
@@ -123,7 +137,7 @@ extern "C" {
 
 size_t moe_adapter_workspace_size(int32_t T, int32_t K, int32_t N, int32_t num_adapters, int32_t R) {
   if (T < 0 || K < 1 || N < 1 || num_adapters < 0 || R < 1) return 0;
-  return adapter_ws_bytes(T, R);
+  return adapter_ws_bytes(T, K, N, R);
 }
 
 moe_status moe_adapter_linear(const moe_adapter_args* a, void* stream) {
@@ -150,7 +164,7 @@ moe_status moe_adapter_linear(const moe_adapter_args* a, void* stream) {
   MXMOE_TRY(check_stride(what, "x_stride", a->x_stride, K));
   MXMOE_TRY(check_stride(what, "out_stride", a->out_stride, n_out));
   if (a->add) MXMOE_TRY(check_stride(what, "add_stride", a->add_stride, N));
-  const size_t need = adapter_ws_bytes(a->T, a->R);
+  const size_t need = adapter_ws_bytes(a->T, a->K, a->N, a->R);
   if (T > 0) {
     if (!a->x || !a->out || (n > 0 && (!a->ids || !a->a || !a->b)))
       return fail(MOE_ERR_INVALID_ARG, "%s: null pointer", what);
@@ -194,7 +208,7 @@ moe_status moe_adapter_linear(const moe_adapter_args* a, void* stream) {
     j.s = low, j.lb = a->b;
     j.num_adapters = a->num_adapters, j.R = a->R;
   }
-  return launch_dense(j, s);
+  return launch_dense(j, static_cast<uint8_t*>(a->workspace) + adapter_gemm_offset(a->T, a->R), s);
 }
 
 }  // extern "C"

@@ -34,6 +34,9 @@ struct DenseJob {
   const float* s;           // [M][R]
   const void* lb;           // [num_adapters][N][R]
   int num_adapters, R;
+  // K split over blocks: where the block's part of the sums goes, fp32 [M][N]
+  // (set by the kernels; null: the sums are whole)
+  float* partial;
 };
 
 // Token counts up to this are decode batches: their adapters differ from token
@@ -41,9 +44,17 @@ struct DenseJob {
 // on its neighbours'.)
 constexpr int kFewTokens = 256;
 
-moe_status launch_dense(const DenseJob& j, hipStream_t s);
+// Scratch of a product: M, N, K, epi, ta, tb and whether there are ids decide.
+size_t dense_ws_bytes(const DenseJob& j);
+moe_status launch_dense(const DenseJob& j, void* ws, hipStream_t s);
 // Up to three independent plain products of one type with B stored [K][N].
-moe_status launch_dense_group(const DenseJob* jobs, int n, hipStream_t s);
+moe_status launch_dense_group(const DenseJob* jobs, int n, void* ws, hipStream_t s);
+// The sizes of a product, for dense_ws_bytes.
+inline DenseJob dense_sizes(int M, int N, int K, int epi, int ta, int tb) {
+  DenseJob j{};
+  j.M = M, j.N = N, j.K = K, j.epi = epi, j.ta = ta, j.tb = tb;
+  return j;
+}
 
 // ---- argument checks shared by the entry points -------------------------
 constexpr int kMaxWidth = 1 << 18;

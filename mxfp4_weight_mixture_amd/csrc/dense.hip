@@ -21,25 +21,62 @@ int64_t tiles(const DenseJob& j, int bm, int bn) {
   else if (j.ids) LAUNCH(false, false, kEpiPlain, true);                      \
   else LAUNCH(false, false, kEpiPlain, false)
 
-// Whole 256 x 256 tiles in full rounds of the CUs, the rest whole or in parts.
-struct TilePlan {
-  int64_t full, rest, parts;
+// The plan (and with it the scratch) is made for all CUs of an MI355X; a device
+// that shows fewer takes more rounds.
+constexpr int kCus = 256;
+
+// How a product is cut: 64 x 64 tiles, or 256 x 256 tiles in full rounds of the
+// CUs and the rest whole or in parts; K in one or several parts.
+struct Plan {
+  bool small;
+  int splits;
+  int64_t full, rest, parts;   // of 256 x 256 tiles
+  int64_t blocks() const { return full + rest * parts; }
 };
-TilePlan plan_tiles(const DenseJob& j, int cus) {
-  TilePlan t;
-  const int64_t n = tiles(j, 256, 256);
-  t.full = n / cus * cus;
-  t.rest = n - t.full;
-  t.parts = 4 * t.rest <= cus ? 4 : 2 * t.rest <= cus ? 2 : 1;
-  return t;
+
+// Expected times in microseconds per 32-deep stage, measured on a filled chip:
+// 0.84 a round of whole 256 x 256 tiles, 0.55 of halves, 0.28 of quarters; 0.22
+// a round of 64 x 64 tiles, two per CU, 0.11 of up to one per CU.  About 4 a
+// round for its ends.  A split of K costs a launch and the sums' way to memory
+// and back, at 4 MB a microsecond.
+Plan make_plan(const DenseJob& j) {
+  const int cus = kCus;
+  Plan best{};
+  const int64_t n = tiles(j, 256, 256), n64 = tiles(j, 64, 64);
+  best.full = n / cus * cus;
+  best.rest = n - best.full;
+  best.parts = 4 * best.rest <= cus ? 4 : 2 * best.rest <= cus ? 2 : 1;
+  best.splits = 1;
+  const Plan whole = best;
+  double least = 1e30;
+  // (a decode batch's mixed adapters are the small kernel's)
+  const bool only_small = j.ids && j.M <= kFewTokens;
+  for (int splits = 1; splits <= 8; splits *= 2) {
+    const double stages = ((j.K + 63) / 64 + splits - 1) / splits * 2;
+    if (splits > 1 && stages < 16) break;
+    const double join = splits > 1 ? 4 + 2e-6 * splits * j.M * j.N : 0.0;
+    if (!only_small && (splits == 1 || whole.full == 0)) {
+      const double c = whole.parts == 4 ? 0.28 : whole.parts == 2 ? 0.55 : 0.84;
+      const int64_t rest = whole.rest * whole.parts * splits;
+      const double t = (double)(whole.full / cus) * (stages * 0.84 + 4) +
+                       (double)((rest + cus - 1) / cus) * (stages * c + 4) + join;
+      if (t < least) least = t, best = whole, best.splits = splits;
+    }
+    if (splits == 1 || n64 <= cus) {
+      const int64_t b = n64 * splits;
+      const double t = (b <= cus ? stages * 0.11 + 4 : (double)((b + 2 * cus - 1) / (2 * cus)) * (stages * 0.22 + 4)) + join;
+      if (t < least) least = t, best = whole, best.small = true, best.splits = splits;
+    }
+  }
+  return best;
 }
 
 template <typename E>
-moe_status launch_tiles(const DenseJob& j, hipStream_t s) {
-  const TilePlan t = plan_tiles(j, num_cus() / 8 * 8);
-  const dim3 grid((unsigned)(t.full + t.rest * t.parts)), block(256);
-#define MXMOE_LAUNCH(TA, TB, EPI, LORA) \
-  hipLaunchKernelGGL((tile_kernel<E, TA, TB, EPI, LORA>), grid, block, 0, s, j, (int)t.full, (int)t.rest, (int)t.parts)
+moe_status launch_tiles(const DenseJob& j, const Plan& t, float* partial, hipStream_t s) {
+  const dim3 grid((unsigned)(t.blocks() * t.splits)), block(256);
+#define MXMOE_LAUNCH(TA, TB, EPI, LORA)                                                                     \
+  hipLaunchKernelGGL((tile_kernel<E, TA, TB, EPI, LORA>), grid, block, 0, s, j, (int)t.full, (int)t.rest,   \
+                     (int)t.parts, partial, t.splits)
   MXMOE_DENSE_FORMS(MXMOE_LAUNCH);
 #undef MXMOE_LAUNCH
   MXMOE_HIP(hipGetLastError());
@@ -47,11 +84,12 @@ moe_status launch_tiles(const DenseJob& j, hipStream_t s) {
 }
 
 template <typename E>
-moe_status launch_small(const DenseJob& j, hipStream_t s) {
-  const dim3 grid((unsigned)tiles(j, 64, 64)), block(256);
+moe_status launch_small(const DenseJob& j, int splits, float* partial, hipStream_t s) {
+  const int64_t n = tiles(j, 64, 64);
+  const dim3 grid((unsigned)(splits > 1 ? (n + 7) / 8 * 8 * splits : n)), block(256);
   if (j.K >= 4096 && !j.tb) {   // long rows: stages of 64 k
 #define MXMOE_LAUNCH(TA, TB, EPI, LORA) \
-  hipLaunchKernelGGL((small_kernel<E, TA, TB, EPI, LORA, 64>), grid, block, 0, s, j)
+  hipLaunchKernelGGL((small_kernel<E, TA, TB, EPI, LORA, 64>), grid, block, 0, s, j, partial, splits)
     if (j.epi == kEpiGate && j.ids) MXMOE_LAUNCH(false, false, kEpiGate, true);
     else if (j.epi == kEpiGate) MXMOE_LAUNCH(false, false, kEpiGate, false);
     else if (j.ids) MXMOE_LAUNCH(false, false, kEpiPlain, true);
@@ -59,12 +97,31 @@ moe_status launch_small(const DenseJob& j, hipStream_t s) {
 #undef MXMOE_LAUNCH
   } else {
 #define MXMOE_LAUNCH(TA, TB, EPI, LORA) \
-  hipLaunchKernelGGL((small_kernel<E, TA, TB, EPI, LORA, 32>), grid, block, 0, s, j)
+  hipLaunchKernelGGL((small_kernel<E, TA, TB, EPI, LORA, 32>), grid, block, 0, s, j, partial, splits)
     MXMOE_DENSE_FORMS(MXMOE_LAUNCH);
 #undef MXMOE_LAUNCH
   }
   MXMOE_HIP(hipGetLastError());
   return MOE_OK;
+}
+
+template <typename E>
+moe_status launch_join(const DenseJob& j, int splits, const float* partial, hipStream_t s) {
+  const int64_t units = (int64_t)j.M * (j.epi == kEpiGate ? j.N / 16 : j.N / 8);
+  const dim3 grid((unsigned)((units + 255) / 256)), block(256);
+  if (j.epi == kEpiGate) hipLaunchKernelGGL((join_kernel<E, kEpiGate>), grid, block, 0, s, j, partial, splits);
+  else if (j.epi == kEpiGateGrad)
+    hipLaunchKernelGGL((join_kernel<E, kEpiGateGrad>), grid, block, 0, s, j, partial, splits);
+  else hipLaunchKernelGGL((join_kernel<E, kEpiPlain>), grid, block, 0, s, j, partial, splits);
+  MXMOE_HIP(hipGetLastError());
+  return MOE_OK;
+}
+
+// Few rows, B's rows contiguous and a block's rows (16 or 32; of a split gate
+// also their up rows, I rows behind) within 31 bits of the first.
+bool takes_few(const DenseJob& j) {
+  const int64_t reach = j.epi == kEpiGate && !j.interleaved ? (int64_t)(j.N / 2 + 16) * j.ldb * 2 : 0;
+  return j.M <= 64 && j.epi != kEpiGateGrad && !j.ta && !j.tb && reach < (1ll << 30);
 }
 
 template <typename E, int MB, int NB, bool DMA, int D>
@@ -78,43 +135,26 @@ moe_status launch_few(const DenseJob& j, hipStream_t s) {
   return MOE_OK;
 }
 
-// Whether 64 x 64 tiles are expected to take less time.  In microseconds per
-// 32-deep stage, measured on a filled chip: 0.84 a round of whole 256 x 256
-// tiles, 0.55 of halves, 0.28 of quarters; 0.22 a round of 64 x 64 tiles, two
-// per CU, 0.11 of up to one per CU.  About 4 a round for its ends.
-bool small_is_faster(const DenseJob& j) {
-  const int cus = num_cus() / 8 * 8;
-  const double stages = (j.K + 31) / 32;
-  const TilePlan t = plan_tiles(j, cus);
-  const double tail = t.rest == 0 ? 0.0 : t.parts == 4 ? stages * 0.28 + 4 : t.parts == 2 ? stages * 0.55 + 4
-                                                                                         : stages * 0.84 + 4;
-  const double big = (double)(t.full / cus) * (stages * 0.84 + 4) + tail;
-  const int64_t n = tiles(j, 64, 64);
-  const double small = n <= cus ? stages * 0.11 + 4 : (double)((n + 2 * cus - 1) / (2 * cus)) * (stages * 0.22 + 4);
-  return small < big;
-}
-
 template <typename E>
-moe_status launch_typed(const DenseJob& j, hipStream_t s) {
-  // (the few-row kernel addresses a block's rows with 31 bits from the first;
-  // a split gate's up rows lie I rows behind)
-  const int64_t reach = j.epi == kEpiGate && !j.interleaved ? (int64_t)(j.N / 2 + 16) * j.ldb * 2 : 0;
-  if (j.M <= 64 && j.epi != kEpiGateGrad && !j.ta && !j.tb && reach < (1ll << 30)) {
-    const bool wide = (j.N + 15) / 16 > num_cus();
+moe_status launch_typed(const DenseJob& j, void* ws, hipStream_t s) {
+  if (takes_few(j)) {
+    const bool wide = (j.N + 15) / 16 > kCus;
     // D: what the LDS holds (128 KB, for 16 rows 64 or 96)
     if (j.M <= 4) return launch_few<E, 1, 1, false, 4>(j, s);
     if (j.M <= 16) return wide ? launch_few<E, 1, 2, true, 2>(j, s) : launch_few<E, 1, 1, true, 2>(j, s);
     if (j.M <= 32) return wide ? launch_few<E, 2, 2, true, 2>(j, s) : launch_few<E, 2, 1, true, 2>(j, s);
     return wide ? launch_few<E, 4, 2, true, 1>(j, s) : launch_few<E, 4, 1, true, 1>(j, s);
   }
-  // (a decode batch's mixed adapters are the small kernel's)
   if (j.ids && j.K == 0 && j.M > kFewTokens) {
     hipLaunchKernelGGL((adapters_only_kernel<E>), dim3((unsigned)tiles(j, 64, 128)), dim3(256), 0, s, j);
     MXMOE_HIP(hipGetLastError());
     return MOE_OK;
   }
-  if ((j.ids && j.M <= kFewTokens) || small_is_faster(j)) return launch_small<E>(j, s);
-  return launch_tiles<E>(j, s);
+  const Plan t = make_plan(j);
+  float* const partial = static_cast<float*>(ws);
+  if (t.small) MXMOE_TRY(launch_small<E>(j, t.splits, partial, s));
+  else MXMOE_TRY(launch_tiles<E>(j, t, partial, s));
+  return t.splits > 1 ? launch_join<E>(j, t.splits, partial, s) : MOE_OK;
 }
 
 template <typename E>
@@ -135,23 +175,30 @@ moe_status launch_group_typed(const DenseJob* jobs, int n, hipStream_t s) {
 
 }  // namespace
 
-moe_status launch_dense(const DenseJob& j, hipStream_t s) {
-  if (j.M == 0) return MOE_OK;
-  return j.dtype == MOE_FLOAT_BF16 ? launch_typed<__bf16>(j, s) : launch_typed<_Float16>(j, s);
+size_t dense_ws_bytes(const DenseJob& j) {
+  if (j.M == 0 || j.K == 0) return 0;
+  const int splits = make_plan(j).splits;
+  return splits > 1 ? (size_t)splits * j.M * j.N * 4 : 0;
 }
 
-moe_status launch_dense_group(const DenseJob* jobs, int n, hipStream_t s) {
-  // one launch where each would run in 64 x 64 tiles that leave CUs idle
+moe_status launch_dense(const DenseJob& j, void* ws, hipStream_t s) {
+  if (j.M == 0) return MOE_OK;
+  return j.dtype == MOE_FLOAT_BF16 ? launch_typed<__bf16>(j, ws, s) : launch_typed<_Float16>(j, ws, s);
+}
+
+moe_status launch_dense_group(const DenseJob* jobs, int n, void* ws, hipStream_t s) {
+  // one launch where each would run in whole 64 x 64 tiles that leave CUs idle
   int64_t blocks = 0;
   bool small = n > 1;
   for (int i = 0; i < n; ++i) {
-    if (jobs[i].M == 0 || !small_is_faster(jobs[i])) small = false;
+    const Plan t = make_plan(jobs[i]);
+    if (jobs[i].M == 0 || !t.small || t.splits > 1) small = false;
     else blocks += tiles(jobs[i], 64, 64);
   }
-  if (small && blocks <= 8 * (int64_t)num_cus())
+  if (small && blocks <= 8 * kCus)
     return jobs[0].dtype == MOE_FLOAT_BF16 ? launch_group_typed<__bf16>(jobs, n, s)
                                            : launch_group_typed<_Float16>(jobs, n, s);
-  for (int i = 0; i < n; ++i) MXMOE_TRY(launch_dense(jobs[i], s));
+  for (int i = 0; i < n; ++i) MXMOE_TRY(launch_dense(jobs[i], ws, s));
   return MOE_OK;
 }
 

@@ -77,6 +77,7 @@ __device__ __forceinline__ void store_pair(void* base, int dtype, size_t row, in
 // Plain: v are columns [n, n + 8) of C.
 template <typename E>
 __device__ __forceinline__ void finish_plain(const DenseJob& p, int m, int n, F8 v) {
+  if (p.partial) return store8<E>(p.partial, MOE_FLOAT_FP32, (size_t)m * p.N + n, v);
   if (p.add) {
     const F8 a = load8<E>(p.add, p.c_dtype, (size_t)m * p.ldadd + n);
 #pragma unroll
@@ -88,6 +89,7 @@ __device__ __forceinline__ void finish_plain(const DenseJob& p, int m, int n, F8
 template <typename E>
 __device__ __forceinline__ void finish_gate(const DenseJob& p, int m, int i, F8 g, F8 u) {
   const int I = p.N >> 1;
+  if (p.partial) return store_pair<E>(p.partial, MOE_FLOAT_FP32, (size_t)m * p.N, I, i, p.interleaved, g, u);
   if (p.add) {
     F8 a, b;
     load_pair<E>(p.add, p.c_dtype, (size_t)m * p.ldadd, I, i, p.interleaved, &a, &b);
@@ -103,6 +105,7 @@ __device__ __forceinline__ void finish_gate(const DenseJob& p, int m, int i, F8 
 // Gate gradient: d are dh's columns [i, i + 8).
 template <typename E>
 __device__ __forceinline__ void finish_gate_grad(const DenseJob& p, int m, int i, F8 d) {
+  if (p.partial) return store8<E>(p.partial, MOE_FLOAT_FP32, (size_t)m * p.N + i, d);
   F8 g, u, h;
   load_pair<E>(p.gu, p.gu_dtype, (size_t)m * 2 * p.N, p.N, i, p.interleaved, &g, &u);
 #pragma unroll
@@ -115,6 +118,44 @@ __device__ __forceinline__ void finish_gate_grad(const DenseJob& p, int m, int i
   }
   store8<E>(p.h, p.dtype, (size_t)m * p.N + i, h);
   store_pair<E>(p.c, p.c_dtype, (size_t)m * p.ldc, p.N, i, p.interleaved, g, u);
+}
+
+// Part z of `splits` of K, in whole 64-deep stages: the job's operands from
+// there on.  The adapters go with part 0.
+__device__ __forceinline__ void take_part(DenseJob& p, float* partial, int z, int splits) {
+  const int stages = (p.K + 63) >> 6, per = (stages + splits - 1) / splits;
+  const int k0 = min(z * per * 64, p.K), k1 = min(k0 + per * 64, p.K);
+  p.a = static_cast<const char*>(p.a) + (p.ta ? (int64_t)k0 * p.lda : k0) * 2;
+  p.b = static_cast<const char*>(p.b) + (p.tb ? (int64_t)k0 * p.ldb : k0) * 2;
+  p.K = k1 - k0;
+  p.partial = partial + (size_t)z * p.M * p.N;
+  if (z > 0) p.num_adapters = 0;
+}
+
+// The parts' sums in order, and what follows them: eight columns a thread.
+template <typename E, int EPI>
+__global__ __launch_bounds__(256) void join_kernel(DenseJob p, const float* partial, int splits) {
+  const int width = EPI == kEpiGate ? p.N >> 1 : p.N, per = width >> 3;
+  const int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int m = (int)(u / per), i = (int)(u % per) * 8;
+  if (m >= p.M) return;
+  F8 v{}, w{};
+  for (int z = 0; z < splits; ++z) {
+    const float* const q = partial + (size_t)z * p.M * p.N;
+    if constexpr (EPI == kEpiGate) {
+      F8 a, b;
+      load_pair<E>(q, MOE_FLOAT_FP32, (size_t)m * p.N, width, i, p.interleaved, &a, &b);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v.v[e] += a.v[e], w.v[e] += b.v[e];
+    } else {
+      const F8 a = load8<E>(q, MOE_FLOAT_FP32, (size_t)m * p.N + i);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v.v[e] += a.v[e];
+    }
+  }
+  if constexpr (EPI == kEpiGate) finish_gate<E>(p, m, i, v, w);
+  else if constexpr (EPI == kEpiGateGrad) finish_gate_grad<E>(p, m, i, v);
+  else finish_plain<E>(p, m, i, v);
 }
 
 }  // namespace

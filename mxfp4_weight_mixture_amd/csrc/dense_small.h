@@ -221,15 +221,23 @@ __device__ __forceinline__ void split_k_tile(const DenseJob& p, int m0, int nt, 
 template <typename E, bool TA, bool TB, int EPI, bool LORA, int BK>
 __device__ __forceinline__ void split_k_block(const DenseJob& p, int block, int blocks, char* lds) {
   const int cols = EPI == kEpiGate ? 32 : 64, width = EPI == kEpiGate ? p.N >> 1 : p.N;
+  const int mts = (p.M + 63) >> 6, nts = (width + cols - 1) / cols, t = xcd_run(block, blocks);
+  if (t >= mts * nts) return;
   int mt, nt;
-  tile_at(xcd_run(block, blocks), (p.M + 63) >> 6, (width + cols - 1) / cols, &mt, &nt);
+  tile_at(t, mts, nts, &mt, &nt);
   split_k_tile<E, TA, TB, EPI, LORA, BK>(p, mt * 64, nt, lds);
 }
 
 template <typename E, bool TA, bool TB, int EPI, bool LORA, int BK>
-__global__ __launch_bounds__(256, BK == 32 ? 2 : 1) void small_kernel(DenseJob p) {
+__global__ __launch_bounds__(256, BK == 32 ? 2 : 1) void small_kernel(DenseJob p, float* partial, int splits) {
   __shared__ __attribute__((aligned(1024))) char lds[split_k_lds(BK)];
-  split_k_block<E, TA, TB, EPI, LORA, BK>(p, blockIdx.x, gridDim.x, lds);
+  int block = blockIdx.x, blocks = gridDim.x;
+  if (splits > 1) {   // (a multiple of 8 blocks per part: each keeps its XCD)
+    blocks /= splits;
+    take_part(p, partial, block / blocks, splits);
+    block %= blocks;
+  }
+  split_k_block<E, TA, TB, EPI, LORA, BK>(p, block, blocks, lds);
 }
 
 // Independent products in one launch: their few blocks share the chip, and

@@ -427,9 +427,11 @@ __device__ __forceinline__ void dense_tile(const DenseJob& p, int m0, int nt, ch
 // 256 x 256 tiles, of which the last (fewer than one per CU) may be split into
 // 128 x 256 halves or 128 x 128 quarters: a part takes 0.65 or 0.33 of a whole
 // tile's time where a whole one takes 1 on a chip that is partly idle.
-// `full` whole tiles, then `rest` tiles in `parts` blocks each.
+// `full` whole tiles, then `rest` tiles in `parts` blocks each; with few tiles
+// (full == 0) K may be split as well.
 template <typename E, bool TA, bool TB, int EPI, bool LORA>
-__global__ __launch_bounds__(256, 1) void tile_kernel(DenseJob p, int full, int rest, int parts) {
+__global__ __launch_bounds__(256, 1) void tile_kernel(DenseJob p, int full, int rest, int parts, float* partial,
+                                                      int splits) {
   __shared__ __attribute__((aligned(1024))) char lds[kTileLds];
   const int cols = EPI == kEpiGate ? 128 : 256, width = EPI == kEpiGate ? p.N >> 1 : p.N;
   const int mts = (p.M + 255) >> 8, nts = (width + cols - 1) / cols;
@@ -440,7 +442,13 @@ __global__ __launch_bounds__(256, 1) void tile_kernel(DenseJob p, int full, int 
     dense_tile<E, TA, TB, EPI, LORA, 4, 4, 4>(p, mt * 256, nt, lds);
     return;
   }
-  const int u = xcd_run(b - full, rest * parts), part = u % parts;
+  int block = b - full;
+  if (splits > 1) {
+    const int blocks = rest * parts;
+    take_part(p, partial, block / blocks, splits);
+    block %= blocks;
+  }
+  const int u = xcd_run(block, rest * parts), part = u % parts;
   tile_at(full + u / parts, mts, nts, &mt, &nt);
   if (parts == 1) {
     dense_tile<E, TA, TB, EPI, LORA, 4, 4, 4>(p, mt * 256, nt, lds);

@@ -23,10 +23,30 @@ moe_status check_block(const char* what, int T, int H, int I, int layout, int ac
   return check_dtype16(what, dtype);
 }
 
-// Workspaces: h; for the gradients d_gate_up, then h.
-size_t ffn_ws_bytes(int T, int I) { return (size_t)T * I * 2 + 256; }
-size_t grad_h_offset(int T, int I) { return align_up((size_t)T * 2 * I * 2, 256); }
-size_t grad_ws_bytes(int T, int I) { return grad_h_offset(T, I) + (size_t)T * I * 2 + 256; }
+// Workspaces: h, for the gradients d_gate_up and h; then the products' scratch
+// (they run one after the other).
+struct Ws {
+  size_t h, gemm, total;
+};
+Ws ffn_ws(int T, int H, int I) {
+  Ws w{};
+  w.gemm = align_up((size_t)T * I * 2, 256);
+  w.total = w.gemm + 256 +
+            std::max(dense_ws_bytes(dense_sizes(T, 2 * I, H, kEpiGate, 0, 0)),
+                     dense_ws_bytes(dense_sizes(T, H, I, kEpiPlain, 0, 0)));
+  return w;
+}
+Ws grad_ws(int T, int H, int I) {
+  Ws w{};
+  w.h = align_up((size_t)T * 2 * I * 2, 256);
+  w.gemm = w.h + align_up((size_t)T * I * 2, 256);
+  w.total = w.gemm + 256 +
+            std::max({dense_ws_bytes(dense_sizes(T, I, H, kEpiGateGrad, 0, 1)),
+                      dense_ws_bytes(dense_sizes(T, H, 2 * I, kEpiPlain, 0, 1)),
+                      dense_ws_bytes(dense_sizes(2 * I, H, T, kEpiPlain, 1, 1)),
+                      dense_ws_bytes(dense_sizes(H, I, T, kEpiPlain, 1, 1))});
+  return w;
+}
 
 }  // namespace
 }  // namespace mxmoe
@@ -37,7 +57,7 @@ extern "C" {
 
 size_t moe_gated_ffn_workspace_size(int32_t T, int32_t H, int32_t I) {
   if (T < 0 || H < 1 || I < 1) return 0;
-  return ffn_ws_bytes(T, I);
+  return ffn_ws(T, H, I).total;
 }
 
 moe_status moe_gated_ffn_forward(const moe_ffn_args* a, void* stream) {
@@ -50,7 +70,8 @@ moe_status moe_gated_ffn_forward(const moe_ffn_args* a, void* stream) {
   MXMOE_TRY(check_stride(what, "x_stride", a->x_stride, a->H));
   MXMOE_TRY(check_stride(what, "out_stride", a->out_stride, a->H));
   if (a->add) MXMOE_TRY(check_stride(what, "add_stride", a->add_stride, a->H));
-  const size_t need = ffn_ws_bytes(a->T, a->I);
+  const Ws w = ffn_ws(a->T, a->H, a->I);
+  const size_t need = w.total;
   if (a->T > 0) {
     if (!a->x || !a->w1 || !a->w2 || !a->out) return fail(MOE_ERR_INVALID_ARG, "%s: null pointer", what);
     if (!a->workspace || a->workspace_bytes < need)
@@ -81,7 +102,7 @@ moe_status moe_gated_ffn_forward(const moe_ffn_args* a, void* stream) {
   j.epi = kEpiGate;
   j.c = ws, j.ldc = a->I, j.c_dtype = a->dtype;
   j.gu = a->gate_up, j.gu_dtype = a->save_dtype;
-  MXMOE_TRY(launch_dense(j, s));
+  MXMOE_TRY(launch_dense(j, ws + w.gemm, s));
 
   j.a = ws, j.lda = a->I;
   j.b = a->w2, j.ldb = a->I;
@@ -90,12 +111,12 @@ moe_status moe_gated_ffn_forward(const moe_ffn_args* a, void* stream) {
   j.gu = nullptr;
   j.add = a->add, j.ldadd = a->add_stride;
   j.c = a->out, j.ldc = a->out_stride, j.c_dtype = a->out_dtype;
-  return launch_dense(j, s);
+  return launch_dense(j, ws + w.gemm, s);
 }
 
 size_t moe_gated_ffn_grad_workspace_size(int32_t T, int32_t H, int32_t I) {
   if (T < 0 || H < 1 || I < 1) return 0;
-  return grad_ws_bytes(T, I);
+  return grad_ws(T, H, I).total;
 }
 
 moe_status moe_gated_ffn_backward(const moe_ffn_grad_args* a, void* stream) {
@@ -111,7 +132,8 @@ moe_status moe_gated_ffn_backward(const moe_ffn_grad_args* a, void* stream) {
   MXMOE_TRY(check_stride(what, "dout_stride", a->dout_stride, a->H));
   if (a->dw1) MXMOE_TRY(check_stride(what, "x_stride", a->x_stride, a->H));
   if (a->dx) MXMOE_TRY(check_stride(what, "dx_stride", a->dx_stride, a->H));
-  const size_t need = grad_ws_bytes(a->T, a->I);
+  const Ws w = grad_ws(a->T, a->H, a->I);
+  const size_t need = w.total;
   const int64_t T = a->T, H = a->H, I = a->I;
   if (T > 0) {
     if (!a->dout || !a->w2 || !a->gate_up || (a->dw1 && !a->x) || (a->dx && !a->w1))
@@ -134,7 +156,7 @@ moe_status moe_gated_ffn_backward(const moe_ffn_grad_args* a, void* stream) {
   uint8_t* ws = static_cast<uint8_t*>(a->workspace);
   const hipStream_t s = (hipStream_t)stream;
 
-  uint8_t* const h = ws + grad_h_offset(a->T, a->I);
+  uint8_t* const h = ws + w.h;
   DenseJob j{};
   j.dtype = a->dtype;
   j.act = a->gate_act;
@@ -147,7 +169,7 @@ moe_status moe_gated_ffn_backward(const moe_ffn_grad_args* a, void* stream) {
   j.gu = const_cast<void*>(a->gate_up), j.gu_dtype = a->save_dtype;
   j.c = ws, j.ldc = 2 * I, j.c_dtype = a->dtype;
   j.h = h;
-  MXMOE_TRY(launch_dense(j, s));
+  MXMOE_TRY(launch_dense(j, ws + w.gemm, s));
 
   // what is asked for of dx, dw1 and dw2, independent of each other
   DenseJob jobs[3];
@@ -182,7 +204,7 @@ moe_status moe_gated_ffn_backward(const moe_ffn_grad_args* a, void* stream) {
     j.add = a->accumulate ? a->dw2 : nullptr, j.ldadd = I;
     jobs[n++] = j;
   }
-  MXMOE_TRY(launch_dense_group(jobs, n, s));
+  MXMOE_TRY(launch_dense_group(jobs, n, ws + w.gemm, s));
   return MOE_OK;
 }
 

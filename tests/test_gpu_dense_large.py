@@ -50,7 +50,19 @@ def _hoeff(q2, dtype):
     (700, BF, "split", "silu", True), (1288, HF, "interleaved", "gelu", "half"), (2601, BF, "interleaved", "silu", True),
     (5001, HF, "split", "gelu", True)])
 def test_ffn(T, dtype, layout, act, save):
-    H = I = 1544
+    _check_ffn(T, 1544, 1544, dtype, layout, act, save)
+
+
+# few tiles and a long reduction: K is split over blocks (forward, dh, dx or the weights' gradients)
+@pytest.mark.parametrize("T,H,I,dtype,layout,act,save", [
+    (87, 1312, 3480, BF, "split", "silu", True), (70, 8200, 136, HF, "interleaved", "gelu", True),
+    (300, 136, 9000, BF, "interleaved", "gelu", "half"), (20000, 72, 200, HF, "split", "silu", True),
+    (1281, 4560, 264, BF, "split", "gelu", True)])
+def test_ffn_with_long_reductions(T, H, I, dtype, layout, act, save):
+    _check_ffn(T, H, I, dtype, layout, act, save)
+
+
+def _check_ffn(T, H, I, dtype, layout, act, save):
     x, dout = du.normal((T, H), 1.0, dtype, T), du.normal((T, H), 1.0, dtype, T + 1)
     w1, w2 = du.normal((2 * I, H), H ** -0.5, dtype, T + 2), du.normal((H, I), I ** -0.5, dtype, T + 3)
     f = mx.GatedFFN(w1, w2, layout=layout, act=act)
@@ -95,7 +107,19 @@ def test_ffn(T, dtype, layout, act, save):
 def test_adapters(T, n, R, kind, dtype, epilogue, act, base):
     if not base and epilogue != "none":
         epilogue = "none"
-    K, N = 1000, 3088
+    _check_adapters(T, 1000, 3088, n, R, kind, dtype, epilogue, act, base)
+
+
+# few tiles and long rows: K is split over blocks, the adapters' part goes with one of them
+@pytest.mark.parametrize("T,K,N,n,R,kind,dtype,epilogue", [
+    (100, 9000, 136, 6, 16, "each", BF, "none"), (256, 7168, 528, 40, 24, "each", HF, "split"),
+    (400, 8008, 272, 3, 64, "runs", BF, "interleaved"), (2407, 4888, 960, 2, 16, "runs", HF, "none"),
+    (1100, 12000, 528, 5, 40, "runs", BF, "split")])
+def test_adapters_with_long_rows(T, K, N, n, R, kind, dtype, epilogue):
+    _check_adapters(T, K, N, n, R, kind, dtype, epilogue, "gelu", True)
+
+
+def _check_adapters(T, K, N, n, R, kind, dtype, epilogue, act, base):
     x = du.normal((T, K), 1.0, dtype, T)
     w = du.normal((N, K), K ** -0.5, dtype, T + 1) if base else None
     a, b = du.normal((n, R, K), K ** -0.5, dtype, T + 2), du.normal((n, N, R), R ** -0.5, dtype, T + 3)
