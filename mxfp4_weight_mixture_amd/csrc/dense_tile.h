@@ -167,12 +167,12 @@ __device__ __forceinline__ void tile_at(int t, int mt, int nt, int* m, int* n) {
 }
 
 // The C tile of 64 FM rows from m0 and the nt-th 64 FN columns of B.
-template <typename E, bool TA, bool TB, int EPI, bool LORA, int FM, int FN, int NST>
+template <typename E, bool TA, bool TB, int EPI, bool LORA, int FM, int FN, int NST, int BK>
 __device__ __forceinline__ void dense_tile(const DenseJob& p, int m0, int nt, char* lds) {
   typedef typename Vec<E>::v8 v8;
   constexpr int BM = 64 * FM, BN = 64 * FN;
-  using A = Operand<E, BM, TA, 4>;
-  using B = Operand<E, BN, TB, 4>;
+  using A = Operand<E, BM, TA, 4, BK>;
+  using B = Operand<E, BN, TB, 4, BK>;
   constexpr int STAGE = A::BYTES + B::BYTES;
   constexpr int STAGING = 32 * FN * 32 * 4;               // a wave's 32 rows of fp32 sums
   static_assert(NST * STAGE <= kTileLds && 4 * STAGING <= kTileLds, "LDS of a tile");
@@ -197,9 +197,9 @@ __device__ __forceinline__ void dense_tile(const DenseJob& p, int m0, int nt, ch
   a.init(p.a, p.lda, p.M, m0, wave, lane);
   if constexpr (EPI == kEpiGate) b.init_gate(p, nt, wave, lane);
   else b.init(p.b, p.ldb, p.N, nt * BN, wave, lane);
-  const int K = p.K, nst = (K + kBK - 1) / kBK;
+  const int K = p.K, nst = (K + BK - 1) / BK;
   constexpr int LOADS = A::LOADS + B::LOADS;
-  constexpr int EARLY = LOADS / 2;   // of them, issued half a stage before the rest
+  constexpr int EARLY = LOADS * 16 / BK;   // of them, issued half a stage before the rest
   auto issue = [&](int j, int s) {
     char* buf = lds + __builtin_amdgcn_readfirstlane((uint32_t)s % NST * STAGE);
     if (j < A::LOADS) a.issue(j, s, K, wave, buf);
@@ -231,24 +231,26 @@ __device__ __forceinline__ void dense_tile(const DenseJob& p, int m0, int nt, ch
     constexpr int RP = (NR + MF - 1) / MF;      // reads after each product
     // the DMA of a stage is spread over a whole stage's products: issued in a
     // lump, it takes longer to accept (20 clocks per KB) than the products last
-    auto spread = [&](int i, int j0, int j1, int s) {
+    auto spread = [&](int i, int n, int j0, int j1, int s) {
 #pragma unroll
       for (int j = j0; j < j1; ++j)
-        if ((j - j0) * MF / (j1 - j0) == i) issue(j, s);
+        if ((j - j0) * n / (j1 - j0) == i) issue(j, s);
     };
     wait_vm<(NST - 2) * LOADS + EARLY>();
     block_barrier();
 #pragma unroll
     for (int r = 0; r < NR; ++r) read(0, 0, r, fa[0], fb[0]);
+    constexpr int KS = BK / 16;
     for (int s = 0; s < nst; ++s) {
 #pragma unroll
-      for (int i = 0; i < MF; ++i) {
-        acc[i % FM][i / FM] = mfma32(fb[0][i / FM], fa[0][i % FM], acc[i % FM][i / FM]);
+      for (int i = 0; i < (KS - 1) * MF; ++i) {
+        const int ks = i / MF, f = i % MF;
+        acc[f % FM][f / FM] = mfma32(fb[ks & 1][f / FM], fa[ks & 1][f % FM], acc[f % FM][f / FM]);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int r = RP * i; r < RP * i + RP; ++r)
-          if (r < NR) read(s, 1, r, fa[1], fb[1]);
-        spread(i, EARLY, LOADS, s + NST - 1);
+        for (int r = RP * f; r < RP * f + RP; ++r)
+          if (r < NR) read(s, ks + 1, r, fa[(ks + 1) & 1], fb[(ks + 1) & 1]);
+        spread(i, (KS - 1) * MF, EARLY, LOADS, s + NST - 1);
         __builtin_amdgcn_sched_barrier(0);
       }
       // all of stage s is in this wave's registers; its part of stage s + 1 has landed
@@ -262,7 +264,7 @@ __device__ __forceinline__ void dense_tile(const DenseJob& p, int m0, int nt, ch
 #pragma unroll
         for (int r = RP * i; r < RP * i + RP; ++r)
           if (r < NR) read(s + 1, 0, r, fa[0], fb[0]);
-        spread(i, 0, EARLY, s + NST);
+        spread(i, MF, 0, EARLY, s + NST);
         __builtin_amdgcn_sched_barrier(0);
       }
     }
@@ -439,7 +441,7 @@ __global__ __launch_bounds__(256, 1) void tile_kernel(DenseJob p, int full, int 
   int mt, nt;
   if (b < full) {
     tile_at(xcd_run(b, full), mts, nts, &mt, &nt);
-    dense_tile<E, TA, TB, EPI, LORA, 4, 4, 4>(p, mt * 256, nt, lds);
+    dense_tile<E, TA, TB, EPI, LORA, 4, 4, 4, 32>(p, mt * 256, nt, lds);
     return;
   }
   int block = b - full;
@@ -451,11 +453,11 @@ __global__ __launch_bounds__(256, 1) void tile_kernel(DenseJob p, int full, int 
   const int u = xcd_run(block, rest * parts), part = u % parts;
   tile_at(full + u / parts, mts, nts, &mt, &nt);
   if (parts == 1) {
-    dense_tile<E, TA, TB, EPI, LORA, 4, 4, 4>(p, mt * 256, nt, lds);
+    dense_tile<E, TA, TB, EPI, LORA, 4, 4, 4, 32>(p, mt * 256, nt, lds);
   } else if (parts == 2) {
-    if (mt * 256 + part * 128 < p.M) dense_tile<E, TA, TB, EPI, LORA, 2, 4, 5>(p, mt * 256 + part * 128, nt, lds);
+    if (mt * 256 + part * 128 < p.M) dense_tile<E, TA, TB, EPI, LORA, 2, 4, 5, 32>(p, mt * 256 + part * 128, nt, lds);
   } else if (mt * 256 + (part & 1) * 128 < p.M && (2 * nt + (part >> 1)) * (cols / 2) < width) {
-    dense_tile<E, TA, TB, EPI, LORA, 2, 2, 8>(p, mt * 256 + (part & 1) * 128, 2 * nt + (part >> 1), lds);
+    dense_tile<E, TA, TB, EPI, LORA, 2, 2, 4, 64>(p, mt * 256 + (part & 1) * 128, 2 * nt + (part >> 1), lds);
   }
 }
 
@@ -467,7 +469,7 @@ __global__ __launch_bounds__(256, 3) void adapters_only_kernel(DenseJob p) {
   int mt, nt;
   const int mts = (p.M + 63) >> 6, nts = (p.N + 127) >> 7;
   tile_at(xcd_run(blockIdx.x, gridDim.x), mts, nts, &mt, &nt);
-  dense_tile<E, false, false, kEpiPlain, true, 1, 2, 2>(p, mt * 64, nt, lds);
+  dense_tile<E, false, false, kEpiPlain, true, 1, 2, 2, 32>(p, mt * 64, nt, lds);
 }
 
 }  // namespace
