@@ -35,8 +35,8 @@ struct Plan {
 };
 
 // Expected times in microseconds per 32-deep stage, measured on a filled chip:
-// 0.84 a round of whole 256 x 256 tiles, 0.55 of halves, 0.28 of quarters; 0.22
-// a round of 64 x 64 tiles, two per CU, 0.11 of up to one per CU.  About 4 a
+// 0.84 a round of whole 256 x 256 tiles, 0.46 of halves, 0.25 of quarters; 0.20
+// a round of 64 x 64 tiles, two per CU, 0.10 of up to one per CU.  About 4 a
 // round for its ends.  A split of K costs a launch and the sums' way to memory
 // and back, at 4 MB a microsecond.
 Plan make_plan(const DenseJob& j) {
@@ -56,7 +56,7 @@ Plan make_plan(const DenseJob& j) {
     if (splits > 1 && stages < 16) break;
     const double join = splits > 1 ? 4 + 2e-6 * splits * j.M * j.N : 0.0;
     if (!only_small && (splits == 1 || whole.full == 0)) {
-      const double c = whole.parts == 4 ? 0.28 : whole.parts == 2 ? 0.55 : 0.84;
+      const double c = whole.parts == 4 ? 0.25 : whole.parts == 2 ? 0.46 : 0.84;
       const int64_t rest = whole.rest * whole.parts * splits;
       const double t = (double)(whole.full / cus) * (stages * 0.84 + 4) +
                        (double)((rest + cus - 1) / cus) * (stages * c + 4) + join;
@@ -64,7 +64,7 @@ Plan make_plan(const DenseJob& j) {
     }
     if (splits == 1 || n64 <= cus) {
       const int64_t b = n64 * splits;
-      const double t = (b <= cus ? stages * 0.11 + 4 : (double)((b + 2 * cus - 1) / (2 * cus)) * (stages * 0.22 + 4)) + join;
+      const double t = (b <= cus ? stages * 0.10 + 4 : (double)((b + 2 * cus - 1) / (2 * cus)) * (stages * 0.20 + 4)) + join;
       if (t < least) least = t, best = whole, best.small = true, best.splits = splits;
     }
   }

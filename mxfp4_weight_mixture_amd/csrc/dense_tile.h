@@ -36,7 +36,7 @@ namespace mxmoe {
 namespace {
 
 constexpr int kBK = 32;          // k per stage
-constexpr int kTileLds = 128 << 10;
+constexpr int kTileLds = 144 << 10;
 // Transposing LDS read: lane i of 16 gets column i of the 4 x 16 patch whose row
 // r the lanes 4 r .. 4 r + 3 address, 8 bytes each.  `restrict` gives the read
 // alias information; without any, the compiler takes it to depend on every
@@ -427,8 +427,8 @@ __device__ __forceinline__ void dense_tile(const DenseJob& p, int m0, int nt, ch
 }
 
 // 256 x 256 tiles, of which the last (fewer than one per CU) may be split into
-// 128 x 256 halves or 128 x 128 quarters: a part takes 0.65 or 0.33 of a whole
-// tile's time where a whole one takes 1 on a chip that is partly idle.
+// 128 x 256 halves or 128 x 128 quarters: a part takes 0.55 or 0.3 of a whole
+// tile's time.  Their stages are 64 deep: half the barriers, whole lines.
 // `full` whole tiles, then `rest` tiles in `parts` blocks each; with few tiles
 // (full == 0) K may be split as well.
 template <typename E, bool TA, bool TB, int EPI, bool LORA>
@@ -455,7 +455,7 @@ __global__ __launch_bounds__(256, 1) void tile_kernel(DenseJob p, int full, int 
   if (parts == 1) {
     dense_tile<E, TA, TB, EPI, LORA, 4, 4, 4, 32>(p, mt * 256, nt, lds);
   } else if (parts == 2) {
-    if (mt * 256 + part * 128 < p.M) dense_tile<E, TA, TB, EPI, LORA, 2, 4, 5, 32>(p, mt * 256 + part * 128, nt, lds);
+    if (mt * 256 + part * 128 < p.M) dense_tile<E, TA, TB, EPI, LORA, 2, 4, 3, 64>(p, mt * 256 + part * 128, nt, lds);
   } else if (mt * 256 + (part & 1) * 128 < p.M && (2 * nt + (part >> 1)) * (cols / 2) < width) {
     dense_tile<E, TA, TB, EPI, LORA, 2, 2, 4, 64>(p, mt * 256 + (part & 1) * 128, 2 * nt + (part >> 1), lds);
   }
