@@ -154,7 +154,6 @@ moe_status moe_adapter_linear(const moe_adapter_args* a, void* stream) {
   const bool gate = a->epilogue != MOE_EPI_NONE;
   if (gate && a->epilogue != MOE_EPI_SWIGLU_SPLIT && a->epilogue != MOE_EPI_SWIGLU_INTERLEAVED)
     return fail(MOE_ERR_INVALID_ARG, "%s: bad epilogue %d", what, a->epilogue);
-  if (gate && a->N % 16) return fail(MOE_ERR_SHAPE, "%s: N = %d (gate + up) must be a multiple of 16", what, a->N);
   if (gate && a->gate_act != MOE_GATE_SILU && a->gate_act != MOE_GATE_GELU)
     return fail(MOE_ERR_INVALID_ARG, "%s: bad gate_act %d", what, a->gate_act);
   if (gate && !a->w && a->T > 0) return fail(MOE_ERR_INVALID_ARG, "%s: a SWIGLU epilogue needs w", what);
@@ -162,7 +161,7 @@ moe_status moe_adapter_linear(const moe_adapter_args* a, void* stream) {
   MXMOE_TRY(check_dtype_or_fp32(what, "out_dtype", a->out_dtype, a->dtype));
   const int64_t T = a->T, K = a->K, N = a->N, n = a->num_adapters, R = a->R, n_out = gate ? N / 2 : N;
   MXMOE_TRY(check_stride(what, "x_stride", a->x_stride, K));
-  MXMOE_TRY(check_stride(what, "out_stride", a->out_stride, n_out));
+  MXMOE_TRY(check_stride(what, "out_stride", a->out_stride, n_out, gate ? 4 : 8));
   if (a->add) MXMOE_TRY(check_stride(what, "add_stride", a->add_stride, N));
   const size_t need = adapter_ws_bytes(a->T, a->K, a->N, a->R);
   if (T > 0) {

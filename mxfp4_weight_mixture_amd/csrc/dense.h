@@ -106,10 +106,10 @@ inline moe_status check_tokens(const char* what, int T, int64_t cols) {
     return fail(MOE_ERR_SHAPE, "%s: T = %d rows of %lld are too many for one launch", what, T, (long long)cols);
   return MOE_OK;
 }
-inline moe_status check_stride(const char* what, const char* name, int64_t stride, int64_t cols) {
-  if (stride < cols || stride > kMaxStride || stride % 8)
-    return fail(MOE_ERR_SHAPE, "%s: %s = %lld must be a multiple of 8 in [%lld, %lld]", what, name, (long long)stride,
-                (long long)cols, (long long)kMaxStride);
+inline moe_status check_stride(const char* what, const char* name, int64_t stride, int64_t cols, int of = 8) {
+  if (stride < cols || stride > kMaxStride || stride % of)
+    return fail(MOE_ERR_SHAPE, "%s: %s = %lld must be a multiple of %d in [%lld, %lld]", what, name,
+                (long long)stride, of, (long long)cols, (long long)kMaxStride);
   return MOE_OK;
 }
 inline moe_status check_dtype16(const char* what, int dtype) {
@@ -133,11 +133,13 @@ struct Vec;
 template <>
 struct Vec<__bf16> {
   typedef __bf16 v8 __attribute__((ext_vector_type(8)));
+  typedef __bf16 v8half __attribute__((ext_vector_type(8), aligned(8)));
   typedef __bf16 v4 __attribute__((ext_vector_type(4)));
 };
 template <>
 struct Vec<_Float16> {
   typedef _Float16 v8 __attribute__((ext_vector_type(8)));
+  typedef _Float16 v8half __attribute__((ext_vector_type(8), aligned(8)));
   typedef _Float16 v4 __attribute__((ext_vector_type(4)));
 };
 

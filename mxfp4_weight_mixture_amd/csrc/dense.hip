@@ -107,7 +107,7 @@ moe_status launch_small(const DenseJob& j, int splits, float* partial, hipStream
 
 template <typename E>
 moe_status launch_join(const DenseJob& j, int splits, const float* partial, hipStream_t s) {
-  const int64_t units = (int64_t)j.M * (j.epi == kEpiGate ? j.N / 16 : j.N / 8);
+  const int64_t units = (int64_t)j.M * (j.epi == kEpiGate ? (j.N / 2 + 7) / 8 : j.N / 8);
   const dim3 grid((unsigned)((units + 255) / 256)), block(256);
   if (j.epi == kEpiGate) hipLaunchKernelGGL((join_kernel<E, kEpiGate>), grid, block, 0, s, j, partial, splits);
   else if (j.epi == kEpiGateGrad)

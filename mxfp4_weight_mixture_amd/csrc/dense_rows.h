@@ -1,5 +1,6 @@
 // What the dense kernels do with their sums, eight consecutive columns of one
-// row at a time: 16-byte accesses of the 16-bit tensors.
+// row at a time: 16-byte accesses of the 16-bit tensors (8-byte aligned ones:
+// a gated width may be an odd multiple of four, which then ends in half a group).
 #pragma once
 
 #include "dense.h"
@@ -20,7 +21,7 @@ __device__ __forceinline__ F8 load8(const void* base, int dtype, size_t i) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) r.v[e] = a[e], r.v[4 + e] = b[e];
   } else {
-    const typename Vec<E>::v8 a = *reinterpret_cast<const typename Vec<E>::v8*>(static_cast<const E*>(base) + i);
+    const typename Vec<E>::v8 a = *reinterpret_cast<const typename Vec<E>::v8half*>(static_cast<const E*>(base) + i);
 #pragma unroll
     for (int e = 0; e < 8; ++e) r.v[e] = (float)a[e];
   }
@@ -36,7 +37,7 @@ __device__ __forceinline__ void store8(void* base, int dtype, size_t i, const F8
     typename Vec<E>::v8 o;
 #pragma unroll
     for (int e = 0; e < 8; ++e) o[e] = (E)r.v[e];
-    *reinterpret_cast<typename Vec<E>::v8*>(static_cast<E*>(base) + i) = o;
+    *reinterpret_cast<typename Vec<E>::v8half*>(static_cast<E*>(base) + i) = o;
   }
 }
 // Eight gate and eight up values of row m, gate index i, from gate_up-shaped memory.
@@ -73,6 +74,26 @@ __device__ __forceinline__ void store_pair(void* base, int dtype, size_t row, in
   }
 }
 
+// The same for the half group that ends a width of 8 n + 4: four gate and four
+// up values, one by one.
+template <typename E>
+__device__ __forceinline__ void load_half_pair(const void* base, int dtype, size_t row, int I, int i, int interleaved,
+                                               F8* g, F8* u) {
+  for (int e = 0; e < 4; ++e) {
+    const size_t a = row + (interleaved ? 2 * (i + e) : i + e), b = interleaved ? a + 1 : a + I;
+    g->v[e] = dtype == MOE_FLOAT_FP32 ? static_cast<const float*>(base)[a] : (float)static_cast<const E*>(base)[a];
+    u->v[e] = dtype == MOE_FLOAT_FP32 ? static_cast<const float*>(base)[b] : (float)static_cast<const E*>(base)[b];
+    g->v[4 + e] = u->v[4 + e] = 0.0f;
+  }
+}
+template <typename E>
+__device__ __forceinline__ void store_half(void* base, int dtype, size_t i, const F8& v, int step = 1) {
+  for (int e = 0; e < 4; ++e) {
+    if (dtype == MOE_FLOAT_FP32) static_cast<float*>(base)[i + e * step] = v.v[e];
+    else static_cast<E*>(base)[i + e * step] = (E)v.v[e];
+  }
+}
+
 // What follows the sums, on eight consecutive columns of one row.
 // Plain: v are columns [n, n + 8) of C.
 template <typename E>
@@ -89,6 +110,18 @@ __device__ __forceinline__ void finish_plain(const DenseJob& p, int m, int n, F8
 template <typename E>
 __device__ __forceinline__ void finish_gate(const DenseJob& p, int m, int i, F8 g, F8 u) {
   const int I = p.N >> 1;
+  if (i + 8 > I) {
+    if (p.partial) {
+      const size_t row = (size_t)m * p.N;
+      store_half<E>(p.partial, MOE_FLOAT_FP32, row + (p.interleaved ? 2 * i : i), g, p.interleaved ? 2 : 1);
+      store_half<E>(p.partial, MOE_FLOAT_FP32, row + (p.interleaved ? 2 * i + 1 : I + i), u, p.interleaved ? 2 : 1);
+      return;
+    }
+    F8 a{}, b{}, h;
+    if (p.add) load_half_pair<E>(p.add, p.c_dtype, (size_t)m * p.ldadd, I, i, p.interleaved, &a, &b);
+    for (int e = 0; e < 4; ++e) h.v[e] = gate_act(p.act, g.v[e] + a.v[e]) * (u.v[e] + b.v[e]);
+    return store_half<E>(p.c, p.c_dtype, (size_t)m * p.ldc + i, h);   // (gate_up is kept for multiples of 8 only)
+  }
   if (p.partial) return store_pair<E>(p.partial, MOE_FLOAT_FP32, (size_t)m * p.N, I, i, p.interleaved, g, u);
   if (p.add) {
     F8 a, b;
@@ -135,7 +168,7 @@ __device__ __forceinline__ void take_part(DenseJob& p, float* partial, int z, in
 // The parts' sums in order, and what follows them: eight columns a thread.
 template <typename E, int EPI>
 __global__ __launch_bounds__(256) void join_kernel(DenseJob p, const float* partial, int splits) {
-  const int width = EPI == kEpiGate ? p.N >> 1 : p.N, per = width >> 3;
+  const int width = EPI == kEpiGate ? p.N >> 1 : p.N, per = (width + 7) >> 3;
   const int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int m = (int)(u / per), i = (int)(u % per) * 8;
   if (m >= p.M) return;
@@ -144,7 +177,8 @@ __global__ __launch_bounds__(256) void join_kernel(DenseJob p, const float* part
     const float* const q = partial + (size_t)z * p.M * p.N;
     if constexpr (EPI == kEpiGate) {
       F8 a, b;
-      load_pair<E>(q, MOE_FLOAT_FP32, (size_t)m * p.N, width, i, p.interleaved, &a, &b);
+      if (i + 8 > width) load_half_pair<E>(q, MOE_FLOAT_FP32, (size_t)m * p.N, width, i, p.interleaved, &a, &b);
+      else load_pair<E>(q, MOE_FLOAT_FP32, (size_t)m * p.N, width, i, p.interleaved, &a, &b);
 #pragma unroll
       for (int e = 0; e < 8; ++e) v.v[e] += a.v[e], w.v[e] += b.v[e];
     } else {

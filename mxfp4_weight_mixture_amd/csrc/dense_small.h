@@ -23,14 +23,15 @@
 namespace mxmoe {
 namespace {
 
-// sum over r of s[r] B[row][r] for eight rows of B, `step` rows apart
+// sum over r of s[r] B[row][r] for `cols` rows of B, `step` elements apart
 template <typename E>
-__device__ __forceinline__ void add_low_rank(F8& v, const float* s, const E* lb, int64_t step, int rank) {
+__device__ __forceinline__ void add_low_rank(F8& v, const float* s, const E* lb, int64_t step, int rank, int cols = 8) {
   typedef typename Vec<E>::v8 v8;
   for (int r = 0; r < rank; r += 8) {
     F8 sv = load8<E>(s, MOE_FLOAT_FP32, r);
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
+      if (c >= cols) break;
       const v8 b = *reinterpret_cast<const v8*>(lb + c * step + r);
 #pragma unroll
       for (int e = 0; e < 8; ++e)
@@ -193,8 +194,8 @@ __device__ __forceinline__ void split_k_tile(const DenseJob& p, int m0, int nt, 
           const float* s = p.s + (size_t)m * p.R;
           const E* lb = static_cast<const E*>(p.lb) + ((size_t)id * p.N + (p.interleaved ? 2 * i : i)) * p.R;
           const int64_t step = p.interleaved ? 2 * p.R : p.R;
-          add_low_rank<E>(gt, s, lb, step, rank);
-          add_low_rank<E>(up, s, lb + (p.interleaved ? p.R : (int64_t)width * p.R), step, rank);
+          add_low_rank<E>(gt, s, lb, step, rank, width - i);
+          add_low_rank<E>(up, s, lb + (p.interleaved ? p.R : (int64_t)width * p.R), step, rank, width - i);
         }
       }
       finish_gate<E>(p, m, i, gt, up);

@@ -276,11 +276,11 @@ __device__ __forceinline__ void dense_tile(const DenseJob& p, int m0, int nt, ch
   // each adapter present in the wave's rows in turn: its product goes to sums of
   // its own, which only that adapter's rows take up.  s enters as two 16-bit
   // operands (its high and low part), so that it is not rounded to one.  Two
-  // 16-deep steps are loaded together, and all rows where there are registers
-  // for it (256 accumulators leave none: they would have to leave the matrix
-  // cores' registers at once): the time is the loads' latency.
+  // or four 16-deep steps are loaded together, and all rows where there are
+  // registers for it (256 accumulators leave none: they would have to leave the
+  // matrix cores' registers at once): the time is the loads' latency.
   if constexpr (LORA) {
-    constexpr int HS = 2, FB = FM * FN > 8 ? 1 : FM;   // steps, fragment rows together
+    constexpr int HS = FM * FN == 4 ? 4 : 2, FB = FM * FN > 8 ? 1 : FM;   // steps, fragment rows together
     auto add_adapters = [&](auto F0) {
     constexpr int f0 = decltype(F0)::value;
     for (;;) {

@@ -100,7 +100,7 @@ def test_ffn_gradient_refusals(kw, status, needle):
     (dict(T=1 << 22, N=1 << 16, out_stride=1 << 16), "MOE_ERR_SHAPE", "too many"),
     (dict(K=4), "MOE_ERR_SHAPE", "K = 4"),
     (dict(N=33), "MOE_ERR_SHAPE", "N = 33"),
-    (dict(N=24, epilogue=1), "MOE_ERR_SHAPE", "multiple of 16"),
+    (dict(N=24, epilogue=1, out_stride=14), "MOE_ERR_SHAPE", "multiple of 4"),
     (dict(num_adapters=-1), "MOE_ERR_SHAPE", "num_adapters"),
     (dict(num_adapters=65537), "MOE_ERR_SHAPE", "num_adapters"),
     (dict(R=0), "MOE_ERR_SHAPE", "R = 0"),

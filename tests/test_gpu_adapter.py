@@ -63,6 +63,24 @@ def test_against_oracle(T, K, N, n, R, kind, dtype, epilogue, act):
     _check(f, x, ids, f.forward(x, ids), dtype, epilogue=epilogue, act=act)
 
 
+@pytest.mark.parametrize("T", [1, 3, 17, 40, 64, 100, 257, 300])
+@pytest.mark.parametrize("N", [8, 24, 72, 264, 1032, 4504])
+@pytest.mark.parametrize("epilogue", ["split", "interleaved"])
+def test_gated_widths_of_odd_fours(T, N, epilogue):
+    """N / 2 is an odd multiple of four: rows of out are 8-byte aligned, the last group of columns is half one.
+    Nothing is read or written past an adapter's rows or the output's."""
+    x, ids, f = _problem(T, 136, N, 5, 24, HF, "each", 12, epilogue=epilogue, ranks=[24, 7, 0, 16, 24])
+    wide = torch.full((T + 2, N // 2 + 4), 3.0, dtype=HF, device="cuda")
+    out = wide[:, : N // 2][1: T + 1] if (N // 2 + 4) * 2 % 16 == 0 else torch.empty((T, N // 2), dtype=HF, device="cuda")
+    add = du.normal((T, N), 1.0, HF, 13)
+    _check(f, x, ids, f.forward(x, ids, add=add, out=out), HF, add=add, epilogue=epilogue)
+    if out.stride(0) != N // 2 or T == 1:
+        wide[1: T + 1, : N // 2] = 3.0
+        assert (wide == 3.0).all()
+    _check(f, x, ids, f.forward(x, ids), HF, epilogue=epilogue)
+    _check(f, x, ids, f.forward(x, ids, out_dtype=F), F, epilogue=epilogue)
+
+
 @pytest.mark.parametrize("T", [1, 13, 40, 150])
 @pytest.mark.parametrize("out_dtype", [F, HF])
 @pytest.mark.parametrize("base", [True, False])

@@ -114,7 +114,9 @@ def test_adapters(T, n, R, kind, dtype, epilogue, act, base):
 @pytest.mark.parametrize("T,K,N,n,R,kind,dtype,epilogue", [
     (100, 9000, 136, 6, 16, "each", BF, "none"), (256, 7168, 528, 40, 24, "each", HF, "split"),
     (400, 8008, 272, 3, 64, "runs", BF, "interleaved"), (2407, 4888, 960, 2, 16, "runs", HF, "none"),
-    (1100, 12000, 528, 5, 40, "runs", BF, "split")])
+    (1100, 12000, 528, 5, 40, "runs", BF, "split"), (90, 6000, 136, 4, 8, "each", HF, "split"),
+    (300, 8000, 520, 3, 16, "runs", HF, "interleaved"), (2050, 512, 4504, 5, 16, "runs", BF, "interleaved"),
+    (2050, 512, 4504, 5, 16, "runs", BF, "split")])
 def test_adapters_with_long_rows(T, K, N, n, R, kind, dtype, epilogue):
     _check_adapters(T, K, N, n, R, kind, dtype, epilogue, "gelu", True)
 
