@@ -21,5 +21,8 @@ Parity status of each function (what pins it, in tests/test_oracle_*.py):
                      pure-Python brute force of the whole layer on tiny inputs
   moe.moe_tokens     equals moe_layer rows
   moe.rms_rescale / to_bf16_bits   unit RMS; torch bf16 rounding
+  dense.gate_act     torch's silu and tanh gelu, act(z) - act(-z) = z; derivative by differences
+  dense.gated_ffn / gated_ffn_grad   torch autograd in float64, central differences
+  dense.adapter_linear   weights merged per token
 """
-from . import mx, moe  # noqa: F401
+from . import mx, moe, dense  # noqa: F401
