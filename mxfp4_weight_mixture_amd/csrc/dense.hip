@@ -139,7 +139,7 @@ template <typename E>
 moe_status launch_typed(const DenseJob& j, void* ws, hipStream_t s) {
   if (takes_few(j)) {
     const bool wide = (j.N + 15) / 16 > kCus;
-    // D: what the LDS holds (128 KB, for 16 rows 64 or 96)
+    // turns ahead: what 128 KB of LDS hold
     if (j.M <= 4) return launch_few<E, 1, 1, false, 4>(j, s);
     if (j.M <= 16) return wide ? launch_few<E, 1, 2, true, 2>(j, s) : launch_few<E, 1, 1, true, 2>(j, s);
     if (j.M <= 32) return wide ? launch_few<E, 2, 2, true, 2>(j, s) : launch_few<E, 2, 1, true, 2>(j, s);

@@ -40,8 +40,9 @@
 namespace mxmoe {
 namespace {
 
-constexpr int kBK = 32;          // k per stage
+constexpr int kBK = 32;          // k per stage, unless a kernel says otherwise
 constexpr int kTileLds = 144 << 10;
+
 // Transposing LDS read: lane i of 16 gets column i of the 4 x 16 patch whose row
 // r the lanes 4 r .. 4 r + 3 address, 8 bytes each.  `restrict` gives the read
 // alias information; without any, the compiler takes it to depend on every
@@ -51,16 +52,12 @@ typedef short v8s __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) v4s lds_v4s;
 __device__ __forceinline__ v4s read_tr(lds_v4s* __restrict__ a) { return __builtin_amdgcn_ds_read_tr16_b64_v4i16(a); }
 
-// First row of B behind tile columns [32 j, 32 j + 32) of n-tile nt, and the
-// distance of consecutive columns' rows; base is advanced for up rows.
-__device__ __forceinline__ void b_block(const DenseJob& p, int nt, int bn, int j, int* first, int* step, int* up) {
-  if (p.epi != kEpiGate) {
-    *first = nt * bn + 32 * j, *step = 1, *up = 0;
-    return;
-  }
-  *first = nt * (bn >> 1) + (j >> 1) * 32;   // index within gate or up
-  *step = p.interleaved ? 2 : 1;
-  *up = j & 1;
+// Row of B behind tile columns [32 j, 32 j + 32) of n-tile nt: the first one's
+// index among the plain (or the gate's, or the up) rows, and whether it is up.
+__device__ __forceinline__ void b_block(const DenseJob& p, int nt, int bn, int j, int* first, int* up) {
+  const bool gate = p.epi == kEpiGate;
+  *first = gate ? nt * (bn >> 1) + (j >> 1) * 32 : nt * bn + 32 * j;
+  *up = gate ? j & 1 : 0;
 }
 
 // One operand's way from memory to the products: DMA of a stage, fragment reads.
@@ -314,8 +311,8 @@ __device__ __forceinline__ void dense_tile(const DenseJob& p, int m0, int nt, ch
           const int k = r + 16 * h + 8 * g;
 #pragma unroll
           for (int fn = 0; fn < FN; ++fn) {
-            int first, step, up;
-            b_block(p, nt, BN, (wn >> 5) + fn, &first, &step, &up);
+            int first, up;
+            b_block(p, nt, BN, (wn >> 5) + fn, &first, &up);
             const int i = first + l32;
             const int row = EPI == kEpiGate ? (p.interleaved ? 2 * i + up : up * width + i) : i;
             bv[h][fn] = v8{};

@@ -145,6 +145,27 @@ def test_infinities_stay_in_their_row():
     assert out[40].isnan().all() and not out[33].isfinite().any()
 
 
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("big", [100.0, 3e4, 1e12, 1e18])
+def test_saturated_gates(act, big):
+    """Far from zero the activation is g or 0 and its derivative 1 or 0, with nothing overflowing on the way."""
+    T, H, I = 9, 16, 8
+    x = torch.zeros(T, H, dtype=BF, device="cuda")
+    x[:, 0], x[:, 1] = 1.0, 1.0
+    w1, w2 = torch.zeros(2 * I, H, dtype=BF, device="cuda"), torch.zeros(H, I, dtype=BF, device="cuda")
+    w1[:4, 0], w1[4:I, 0], w1[I:, 1] = big, -big, 2.0
+    w2[:I] = torch.eye(I)
+    f = mx.GatedFFN(w1, w2, act=act)
+    out, gu = f.forward(x, save=True)
+    g = float(w1[0, 0])
+    assert (out[:, :4].float() == 2 * g).all() and not out[:, 4:].any()
+    dx, dw1, dw2 = f.backward(torch.ones_like(x), x, gu)
+    assert dx.isfinite().all() and dw1.isfinite().all() and dw2.isfinite().all()
+    # d_gate = 2 act'(gate), d_up = act(gate): over T equal tokens
+    assert (dw1[:4, 0].float() == 2 * T).all() and not dw1[4:I].any() and not dw1[I + 4:].any()
+    assert torch.allclose(dw1[I: I + 4, 1].float(), torch.full((4,), T * g, device="cuda"), rtol=2 * du.u(BF))
+
+
 @pytest.mark.parametrize("T", [1, 20, 150])
 def test_side_stream_and_repeat(T):
     x, f = _block(T, 520, 264, BF, 71)
