@@ -505,8 +505,8 @@ moe_status moe_gated_ffn_backward(const moe_ffn_grad_args* args, void* stream);
  * are fastest where the tokens of a request stand together, as prompts do.
  *
  * Sizes: 0 <= T <= 2^28 (T == 0 enqueues nothing), K, N multiples of 8 in
- * [8, 262144], T rows of N fewer than 2^24 tiles of 64 x 64; 0 <= num_adapters <= 65536; R a multiple of 8 in
- * [8, 256].  Strides, alignment and overlap as for moe_gated_ffn_forward
+ * [8, 262144], T rows of N fewer than 2^24 tiles of 64 x 64;
+ * 0 <= num_adapters <= 65536; R a multiple of 8 in [8, 256].  Strides, alignment and overlap as for moe_gated_ffn_forward
  * (ids, scales and ranks: 4-byte aligned; out_stride a multiple of 4 for
  * SWIGLU, whose N/2 columns need not be 8 n).  With a SWIGLU epilogue add has N
  * columns (it is added before the gate) and cannot be `out`. */

@@ -110,3 +110,29 @@ def test_adapters_on_a_quantised_projection():
     ref, bound = du.adapter_bounds(du.f64(x), None, ids.cpu().numpy(), du.f64(f.lora_a), du.f64(f.lora_b), BF, BF,
                                    add=du.f64(y))
     du.assert_within(out, ref, bound)
+
+
+def test_two_streams_at_once():
+    """Calls in flight on two streams share nothing: forward, backward and adapters of several sizes."""
+    H, I, n = 520, 264, 4
+    work = []
+    for k, T in enumerate((3, 50, 130, 700)):
+        f = mx.GatedFFN(du.normal((2 * I, H), H ** -0.5, BF, k), du.normal((H, I), I ** -0.5, BF, k + 9))
+        lin = mx.AdapterLinear(f.w1, du.normal((n, 16, H), H ** -0.5, BF, k), du.normal((n, 2 * I, 16), 0.25, BF, k))
+        x, dout = du.normal((T, H), 1.0, BF, k), du.normal((T, H), 1.0, BF, k + 5)
+        ids = (torch.arange(T, device="cuda") * n // T).int()
+        work.append((f, lin, x, dout, ids))
+
+    def step(item, stream=None):
+        f, lin, x, dout, ids = item
+        out, gu = f.forward(x, save=True, stream=stream)
+        return (out,) + tuple(f.backward(dout, x, gu, stream=stream)) + (lin.forward(x, ids, stream=stream),)
+
+    want = [step(w) for w in work]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        got = [step(w, streams[(i + j) % 2]) for j in range(2) for i, w in enumerate(work)]
+        torch.cuda.synchronize()
+        for i, g in enumerate(got):
+            assert all(torch.equal(a, b) for a, b in zip(g, want[i % len(work)])), i
