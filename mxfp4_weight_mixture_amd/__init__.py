@@ -9,6 +9,7 @@ back to.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional, Sequence
@@ -170,15 +171,29 @@ def _u8(n: int, device) -> torch.Tensor:
     return torch.empty(max(int(n), 1), dtype=torch.uint8, device=device)
 
 
+def _allocate_on(stream):
+    """Context in which a call allocates its buffers: on the stream that uses them.
+
+    The caching allocator gives a freed block out again at once, to allocations of the
+    stream that the block belongs to: that stream's order protects what still runs.  A
+    block of the current stream would reach `stream`, which does not wait for it, while
+    earlier work of the current stream still uses it."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
 def _keep_until_done(stream, *tensors):
-    """Tensors allocated here on the current stream but used by work enqueued on
-    `stream`: tell the caching allocator so, so that it does not hand their memory
-    to a later allocation before that work has finished."""
-    if stream is None or stream == torch.cuda.current_stream(stream.device):
+    """A call's results, allocated on `stream` or given by the caller: both that stream and
+    the current one, where the caller goes on with them, use them.  Tell the caching allocator
+    so, so that it does not hand their memory out again before either has finished."""
+    if stream is None:
+        return
+    current = torch.cuda.current_stream(stream.device)
+    if stream == current:
         return
     for t in tensors:
         if t is not None:
             t.record_stream(stream)
+            t.record_stream(current)
 
 
 _COPY_STREAMS = {}
@@ -203,8 +218,9 @@ def device_supported() -> bool:
 def route(logits: torch.Tensor, k: int, stream=None):
     """moe_route: logits fp32 [T][E] -> (topk_ids int32 [T][k], topk_w fp32 [T][k])."""
     T, E = logits.shape
-    ids = torch.empty((T, k), dtype=torch.int32, device=logits.device)
-    w = torch.empty((T, k), dtype=torch.float32, device=logits.device)
+    with _allocate_on(stream):
+        ids = torch.empty((T, k), dtype=torch.int32, device=logits.device)
+        w = torch.empty((T, k), dtype=torch.float32, device=logits.device)
     _check(lib.moe_route(_ptr(logits), T, E, k, _ptr(ids), _ptr(w), _stream(stream)))
     _keep_until_done(stream, ids, w)
     return ids, w
@@ -214,14 +230,15 @@ def permute(topk_ids: torch.Tensor, E: int, stream=None):
     """moe_permute: topk_ids [T][k] -> (expert_offsets [E+1], perm_src [T*k], dest_row [T*k])."""
     T, k = topk_ids.shape
     dev = topk_ids.device
-    off = torch.empty(E + 1, dtype=torch.int32, device=dev)
-    ps = torch.empty(T * k, dtype=torch.int32, device=dev)
-    dr = torch.empty(T * k, dtype=torch.int32, device=dev)
     n = lib.moe_permute_workspace_size(T, E, k)
-    ws = _u8(n, dev)
+    with _allocate_on(stream):
+        off = torch.empty(E + 1, dtype=torch.int32, device=dev)
+        ps = torch.empty(T * k, dtype=torch.int32, device=dev)
+        dr = torch.empty(T * k, dtype=torch.int32, device=dev)
+        ws = _u8(n, dev)
     _check(lib.moe_permute(_ptr(topk_ids), T, E, k, _ptr(off), _ptr(ps), _ptr(dr), _ptr(ws), n,
                            _stream(stream)))
-    _keep_until_done(stream, off, ps, dr, ws)
+    _keep_until_done(stream, off, ps, dr)
     return off, ps, dr
 
 
@@ -244,11 +261,12 @@ def grouped_gemm(a: torch.Tensor, w_packed: torch.Tensor, w_scales: torch.Tensor
     n_out = N if epi == 0 else N // 2
     c_dt = {"fp32": 0, "bf16": 1, "mxfp8": 2}[out_dtype]
     c_scales = None
-    if c_dt == 2:
-        c = torch.empty((rows, n_out), dtype=torch.uint8, device=a.device)
-        c_scales = torch.empty((rows, n_out // 32), dtype=torch.uint8, device=a.device)
-    else:
-        c = torch.empty((rows, n_out), dtype=torch.float32 if c_dt == 0 else torch.bfloat16, device=a.device)
+    with _allocate_on(stream):
+        if c_dt == 2:
+            c = torch.empty((rows, n_out), dtype=torch.uint8, device=a.device)
+            c_scales = torch.empty((rows, n_out // 32), dtype=torch.uint8, device=a.device)
+        else:
+            c = torch.empty((rows, n_out), dtype=torch.float32 if c_dt == 0 else torch.bfloat16, device=a.device)
     args = GemmArgs(a=a.data_ptr(), a_scales=a_scales.data_ptr() if a_scales is not None else None,
                     a_gather=a_gather.data_ptr() if a_gather is not None else None,
                     w_packed=w_packed.data_ptr(), w_scales=w_scales.data_ptr(),
@@ -258,9 +276,10 @@ def grouped_gemm(a: torch.Tensor, w_packed: torch.Tensor, w_scales: torch.Tensor
                     a_rows=a.shape[0], rows=rows, E=E, N=N, K=K, epilogue=epi, c_dtype=c_dt,
                     w_format=W_FORMAT[w_format])
     n = lib.moe_grouped_gemm_workspace_size(ctypes.byref(args))
-    ws = _u8(n, a.device)
+    with _allocate_on(stream):
+        ws = _u8(n, a.device)
     _check(lib.moe_mxfp4_grouped_gemm(ctypes.byref(args), _ptr(ws), n, _stream(stream)))
-    _keep_until_done(stream, c, c_scales, ws)
+    _keep_until_done(stream, c, c_scales)
     return (c, c_scales) if c_dt == 2 else c
 
 
@@ -270,7 +289,8 @@ def tile_weights(w_packed: torch.Tensor, w_scales: torch.Tensor, epilogue: str =
     Returns uint8 tensors of the same shapes (the bytes are reordered; the
     shapes only carry E, N, K).  epilogue: the one the matrix is used with."""
     E, N, K2 = w_packed.shape
-    tp, ts = torch.empty_like(w_packed), torch.empty_like(w_scales)
+    with _allocate_on(stream):
+        tp, ts = torch.empty_like(w_packed), torch.empty_like(w_scales)
     _check(lib.moe_mxfp4_tile_weights(_ptr(w_packed), _ptr(w_scales), E, N, 2 * K2,
                                       {"none": 0, "split": 1, "interleaved": 2}[epilogue], _ptr(tp), _ptr(ts),
                                       _stream(stream)))
@@ -281,7 +301,8 @@ def tile_weights(w_packed: torch.Tensor, w_scales: torch.Tensor, epilogue: str =
 def untile_weights(t_packed: torch.Tensor, t_scales: torch.Tensor, epilogue: str = "none", stream=None):
     """moe_mxfp4_untile_weights: the inverse of tile_weights."""
     E, N, K2 = t_packed.shape
-    wp, ws = torch.empty_like(t_packed), torch.empty_like(t_scales)
+    with _allocate_on(stream):
+        wp, ws = torch.empty_like(t_packed), torch.empty_like(t_scales)
     _check(lib.moe_mxfp4_untile_weights(_ptr(t_packed), _ptr(t_scales), E, N, 2 * K2,
                                         {"none": 0, "split": 1, "interleaved": 2}[epilogue], _ptr(wp), _ptr(ws),
                                         _stream(stream)))
@@ -294,8 +315,9 @@ def combine(y: torch.Tensor, dest_row: torch.Tensor, topk_w: torch.Tensor, *, rm
     """moe_combine: y [T*k][H] (fp32 or bf16) -> out fp32 [T][H] (and bf16 x_next if rms_next)."""
     T, k = topk_w.shape
     H = y.shape[1]
-    out = torch.empty((T, H), dtype=torch.float32, device=y.device)
-    xn = torch.empty((T, H), dtype=torch.bfloat16, device=y.device) if rms_next else None
+    with _allocate_on(stream):
+        out = torch.empty((T, H), dtype=torch.float32, device=y.device)
+        xn = torch.empty((T, H), dtype=torch.bfloat16, device=y.device) if rms_next else None
     dt = 1 if y.dtype == torch.bfloat16 else 0
     _check(lib.moe_combine(_ptr(y), dt, _ptr(dest_row), _ptr(topk_w), T, k, H, _ptr(out), _ptr(xn),
                            _stream(stream)))
@@ -384,8 +406,9 @@ class GatedFFN:
         a.x_stride = _rows("x", x, None, self.H, (self.dtype,), self.device)
         T = a.T = x.shape[0]
         if out is None:
-            out = torch.empty((T, self.H), device=self.device,
-                              dtype=out_dtype or (add.dtype if add is not None else self.dtype))
+            with _allocate_on(stream):
+                out = torch.empty((T, self.H), device=self.device,
+                                  dtype=out_dtype or (add.dtype if add is not None else self.dtype))
         a.out_stride = _rows("out", out, T, self.H, self._dtypes, self.device)
         if out_dtype is not None and out.dtype != out_dtype:
             raise ValueError(f"out is {out.dtype}, out_dtype {out_dtype}")
@@ -397,17 +420,19 @@ class GatedFFN:
         if save not in (False, True, "half"):
             raise ValueError(f"save is {save!r}, not False, True or 'half'")
         if save:
-            gate_up = torch.empty((T, 2 * self.I), device=self.device,
-                                  dtype=self.dtype if save == "half" else torch.float32)
+            with _allocate_on(stream):
+                gate_up = torch.empty((T, 2 * self.I), device=self.device,
+                                      dtype=self.dtype if save == "half" else torch.float32)
             a.save_dtype, a.gate_up = FLOAT_DTYPE[gate_up.dtype], gate_up.data_ptr()
         else:
             a.save_dtype = a.dtype
         n = lib.moe_gated_ffn_workspace_size(T, self.H, self.I)
-        ws = _u8(n, self.device)
+        with _allocate_on(stream):
+            ws = _u8(n, self.device)
         a.x, a.w1, a.w2, a.out = x.data_ptr(), self.w1.data_ptr(), self.w2.data_ptr(), out.data_ptr()
         a.workspace, a.workspace_bytes = ws.data_ptr(), n
         _check(lib.moe_gated_ffn_forward(ctypes.byref(a), _stream(stream)))
-        _keep_until_done(stream, out, gate_up, ws)
+        _keep_until_done(stream, out, gate_up)
         return (out, gate_up) if save else out
 
     def backward(self, dout: torch.Tensor, x: torch.Tensor, gate_up: torch.Tensor, *, dx=True, dw1=True, dw2=True,
@@ -427,7 +452,8 @@ class GatedFFN:
 
         def grad(g, shape, dtype):
             if g is True:
-                return torch.empty(shape, dtype=dtype, device=self.device)
+                with _allocate_on(stream):
+                    return torch.empty(shape, dtype=dtype, device=self.device)
             return None if g is None or g is False else g
 
         if accumulate and (dw1 is True or dw2 is True):
@@ -448,11 +474,12 @@ class GatedFFN:
         a.accumulate = int(accumulate)
         a.save_dtype = FLOAT_DTYPE[gate_up.dtype]
         n = lib.moe_gated_ffn_grad_workspace_size(T, self.H, self.I)
-        ws = _u8(n, self.device)
+        with _allocate_on(stream):
+            ws = _u8(n, self.device)
         a.dout, a.x, a.w1, a.w2 = dout.data_ptr(), x.data_ptr(), self.w1.data_ptr(), self.w2.data_ptr()
         a.gate_up, a.workspace, a.workspace_bytes = gate_up.data_ptr(), ws.data_ptr(), n
         _check(lib.moe_gated_ffn_backward(ctypes.byref(a), _stream(stream)))
-        _keep_until_done(stream, dx, dw1, dw2, ws)
+        _keep_until_done(stream, dx, dw1, dw2)
         return dx, dw1, dw2
 
 
@@ -511,8 +538,9 @@ class AdapterLinear:
         T = a.T = x.shape[0]
         _flat("ids", ids, (T,), (torch.int32,), self.device)
         if out is None:
-            out = torch.empty((T, self.n_out), device=self.device,
-                              dtype=out_dtype or (add.dtype if add is not None else self.dtype))
+            with _allocate_on(stream):
+                out = torch.empty((T, self.n_out), device=self.device,
+                                  dtype=out_dtype or (add.dtype if add is not None else self.dtype))
         a.out_stride = _rows("out", out, T, self.n_out, self._dtypes, self.device)
         if out_dtype is not None and out.dtype != out_dtype:
             raise ValueError(f"out is {out.dtype}, out_dtype {out_dtype}")
@@ -521,7 +549,8 @@ class AdapterLinear:
             a.add_stride = _rows("add", add, T, self.N, (out.dtype,), self.device)
             a.add = add.data_ptr()
         n = lib.moe_adapter_workspace_size(T, self.K, self.N, self.n, self.R)
-        ws = _u8(n, self.device)
+        with _allocate_on(stream):
+            ws = _u8(n, self.device)
         a.x, a.ids, a.out, a.a, a.b = (x.data_ptr(), ids.data_ptr(), out.data_ptr(), self.lora_a.data_ptr(),
                                        self.lora_b.data_ptr())
         if self.w is not None:
@@ -532,7 +561,7 @@ class AdapterLinear:
             a.ranks = self.ranks.data_ptr()
         a.workspace, a.workspace_bytes = ws.data_ptr(), n
         _check(lib.moe_adapter_linear(ctypes.byref(a), _stream(stream)))
-        _keep_until_done(stream, out, ws)
+        _keep_until_done(stream, out)
         return out
 
 
@@ -564,7 +593,7 @@ class Layer:
         if shared is not None and shared.H != self.H:
             raise ValueError(f"the shared expert's width {shared.H} is not the layer's {self.H}")
         self.shared = shared
-        self._ws = None
+        self._ws = self._ws_stream = None
 
     def workspace_bytes(self, T: int) -> int:
         return lib.moe_layer_workspace_size(T, self.H, self.I, self.E, self.k, self.inter)
@@ -600,14 +629,18 @@ class Layer:
         x_shared = self._shared_input(x, x_scales, x_shared, x_next)
         T = logits.shape[0]
         n = self.workspace_bytes(T)
-        if self._ws is None or self._ws.numel() < n:
-            self._ws = _u8(n, logits.device)
+        ws, on = self._ws, torch.cuda.current_stream(logits.device) if stream is None else stream
+        # a call on another stream gets a workspace of its own: the kept one may still be in use
+        if ws is None or ws.numel() < n or self._ws_stream != on:
+            with _allocate_on(stream):
+                ws = _u8(n, logits.device)
+            self._ws, self._ws_stream = ws, on
         if out is None:
-            out = torch.empty((T, self.H), dtype=torch.float32, device=logits.device)
-        args = self._args(T, logits, x, x_scales, out, x_next, self._ws)
+            with _allocate_on(stream):
+                out = torch.empty((T, self.H), dtype=torch.float32, device=logits.device)
+        args = self._args(T, logits, x, x_scales, out, x_next, ws)
         _check(lib.moe_layer_forward(ctypes.byref(args), _stream(stream)))
-        # the workspace may be replaced by a larger one on a later call while this one still runs
-        _keep_until_done(stream, self._ws, out)
+        _keep_until_done(stream, ws, out)   # (routing() shows the workspace to the caller)
         if x_shared is not None:
             self.shared.forward(x_shared, add=out, out=out, stream=stream)
         return out
@@ -648,6 +681,9 @@ class LayerGraph:
         self.out = out if out is not None else torch.empty((T, layer.H), dtype=torch.float32, device=dev)
         self.ws = _u8(layer.workspace_bytes(T), dev)
         args = layer._args(T, logits, x, x_scales, self.out, x_next, self.ws)
+        # replays may run on any stream: what the current one still does with these buffers' memory ends here
+        if not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream(dev).synchronize()
         # capture needs a created stream; nothing runs during the capture
         side = torch.cuda.Stream(device=dev)
         self._h = ctypes.c_void_p()
@@ -713,7 +749,9 @@ def prefill_streamed(host_blobs: Sequence[torch.Tensor], slots: Sequence[torch.T
     arr = (_vp * nb)(*[b.data_ptr() for b in host_blobs])
     need = lib.moe_streamed_workspace_size(T, H, I, E, k)
     if workspace is None or workspace.numel() < need:
-        workspace = _u8(need, x.device)
+        # the copy stream waits for the compute stream's earlier work before it begins
+        with _allocate_on(compute_stream):
+            workspace = _u8(need, x.device)
     ev_arr = None
     if events is not None:
         ev_arr = (_vp * len(events))(*[e.cuda_event for e in events])

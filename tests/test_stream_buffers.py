@@ -1,0 +1,148 @@
+"""Where the binding's calls allocate, on the CPU: a call that enqueues on a given stream takes its scratch and
+results from that stream's memory (a block of the current stream may still be in use there), and its results are
+kept for both streams.  Streams, allocations and the library are stand-ins: nothing runs."""
+import contextlib
+import ctypes
+
+import pytest
+import torch
+
+mx = pytest.importorskip("mxfp4_weight_mixture_amd", reason="libmxmoe.so is not built")
+
+BF = torch.bfloat16
+
+
+class Stream:
+    def __init__(self, name, device=None):
+        self.name, self.cuda_stream, self.device, self.synced = name, id(self) % 2 ** 31, torch.device("cpu"), 0
+
+    def synchronize(self):
+        self.synced += 1
+
+
+class Library:
+    """Size queries answer 64 bytes, everything else succeeds; which stream each call got is kept."""
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        def call(*args):
+            if name.endswith(("_workspace_size", "_bytes")):
+                return 64
+            if name.endswith("_offset"):
+                return 0
+            self.calls.append((name, [a.value for a in args if isinstance(a, ctypes.c_void_p)]))
+            return 0
+        return call
+
+
+class World:
+    def __init__(self, patch):
+        self.main, self.side = Stream("main"), Stream("side")
+        self.current, self.made, self.kept = self.main, [], {}
+        empty, empty_like = torch.empty, torch.empty_like
+
+        def made(t):
+            self.made.append((t, self.current))
+            return t
+
+        @contextlib.contextmanager
+        def on(stream):
+            before, self.current = self.current, stream
+            yield
+            self.current = before
+
+        patch.setattr(torch, "empty", lambda *a, **k: made(empty(*a, **k)))
+        patch.setattr(torch, "empty_like", lambda *a, **k: made(empty_like(*a, **k)))
+        patch.setattr(torch.cuda, "current_stream", lambda device=None: self.current)
+        patch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+        patch.setattr(torch.cuda, "synchronize", lambda device=None: None)
+        patch.setattr(torch.cuda, "stream", on)
+        patch.setattr(torch.cuda, "Stream", lambda device=None: Stream("new"))
+        patch.setattr(torch.Tensor, "record_stream", lambda t, s: self.kept.setdefault(id(t), set()).add(s.name),
+                      raising=False)
+        patch.setattr(mx, "_weight", lambda name, w: None)
+        patch.setattr(mx, "_on_current_device", lambda device, stream: None)
+        self.lib = Library()
+        patch.setattr(mx, "lib", self.lib)
+
+
+@pytest.fixture
+def world(monkeypatch):
+    with monkeypatch.context() as m:
+        yield World(m)
+
+
+def z(*shape, dtype=BF):
+    return torch.zeros(shape, dtype=dtype)
+
+
+def _ffn():
+    return mx.GatedFFN(z(64, 32), z(32, 32))
+
+
+def _layer(**kw):
+    u = torch.uint8
+    return mx.Layer(z(4, 64, 16, dtype=u), z(4, 64, 1, dtype=u), z(4, 32, 16, dtype=u), z(4, 32, 1, dtype=u), k=2, **kw)
+
+
+CALLS = {
+    "route": lambda s: mx.route(z(5, 4, dtype=torch.float32), 2, stream=s),
+    "permute": lambda s: mx.permute(z(5, 2, dtype=torch.int32), 4, stream=s),
+    "grouped_gemm": lambda s: mx.grouped_gemm(z(5, 32), z(4, 64, 16, dtype=torch.uint8),
+                                              z(4, 64, 1, dtype=torch.uint8), z(5, dtype=torch.int32), stream=s),
+    "grouped_gemm to mxfp8": lambda s: mx.grouped_gemm(
+        z(5, 32), z(4, 64, 16, dtype=torch.uint8), z(4, 64, 1, dtype=torch.uint8), z(5, dtype=torch.int32),
+        epilogue="split", out_dtype="mxfp8", stream=s),
+    "tile_weights": lambda s: mx.tile_weights(z(4, 64, 16, dtype=torch.uint8), z(4, 64, 1, dtype=torch.uint8),
+                                              stream=s),
+    "untile_weights": lambda s: mx.untile_weights(z(4, 64, 16, dtype=torch.uint8), z(4, 64, 1, dtype=torch.uint8),
+                                                  stream=s),
+    "combine": lambda s: mx.combine(z(10, 32), z(10, dtype=torch.int32), z(5, 2, dtype=torch.float32),
+                                    rms_next=True, stream=s),
+    "ffn": lambda s: _ffn().forward(z(5, 32), save=True, stream=s),
+    "ffn backward": lambda s: _ffn().backward(z(5, 32), z(5, 32), z(5, 64), stream=s),
+    "adapters": lambda s: mx.AdapterLinear(z(16, 32), z(2, 8, 32), z(2, 16, 8)).forward(
+        z(5, 32), z(5, dtype=torch.int32), stream=s),
+    "layer": lambda s: _layer().forward(z(5, 4, dtype=torch.float32), z(5, 32), stream=s),
+    "layer with a shared expert": lambda s: _layer(shared=_ffn()).forward(z(5, 4, dtype=torch.float32), z(5, 32),
+                                                                         stream=s),
+    "streamed prefill": lambda s: mx.prefill_streamed(
+        [z(64, dtype=torch.uint8)], [z(64, dtype=torch.uint8)], z(1, 5, 4, dtype=torch.float32), z(5, 32),
+        z(5, 32, dtype=torch.float32), T=5, H=32, I=32, E=4, k=2, num_layers=1, depth=1, compute_stream=s,
+        copy_stream=Stream("copy")),
+}
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_buffers_belong_to_the_stream_that_uses_them(world, name):
+    res = CALLS[name](world.side)
+    res = res if isinstance(res, tuple) else (res,)
+    assert world.lib.calls and all(world.side.cuda_stream in streams for _, streams in world.lib.calls)
+    assert world.made and {s.name for _, s in world.made} == {"side"}
+    # the caller goes on with the results on the current stream and frees them there
+    assert all(world.kept.get(id(t), set()) >= {"main", "side"} for t in res)
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_buffers_of_calls_on_the_current_stream(world, name):
+    CALLS[name](None)
+    assert {s.name for _, s in world.made} == {"main"}
+
+
+def test_a_layer_on_two_streams(world):
+    """The kept workspace is not taken to another stream, where it may still be in use; on one stream it stays."""
+    layer, logits, x = _layer(), z(5, 4, dtype=torch.float32), z(5, 32)
+    seen = []
+    for stream in (None, None, world.side, world.side, None):
+        layer.forward(logits, x, stream=stream)
+        seen.append(layer._ws)
+    assert seen[0] is seen[1] and seen[2] is seen[3]
+    assert len({t.data_ptr() for t in (seen[0], seen[2], seen[4])}) == 3
+
+
+def test_a_captured_layer_owns_its_memory_before_it_is_replayed(world):
+    """Replays may go to any stream: nothing earlier may still use the graph's buffers."""
+    _layer().capture(z(5, 4, dtype=torch.float32), z(5, 32))
+    assert world.main.synced
