@@ -498,8 +498,10 @@ moe_status moe_gated_ffn_backward(const moe_ffn_grad_args* args, void* stream);
  * A token's result depends on its own row and adapter only: infinities or NaN
  * in one adapter or token do not reach the others.
  * The low-rank row scales[a] * x A^T is held in fp32 and enters the second
- * product as it is, or (batches of more than 256 tokens) as the sum of two
- * numbers of type `dtype`: with fp16 its magnitude must stay below 65504 there.
+ * product as it is, or (batches of more than 256 tokens) as a sum of numbers of
+ * type `dtype`: three in bf16, which hold all of its 24 bits, two in fp16, which
+ * hold 22, of the row times a power of two of its own, so that its range is
+ * fp32's there too.
  *
  * Any order of tokens gives the same results; batches of more than 256 tokens
  * are fastest where the tokens of a request stand together, as prompts do.

@@ -181,14 +181,42 @@ __device__ __forceinline__ void gate_act_grad(int act, float g, float* a, float*
   }
 }
 
-// x = hi + lo in two 16-bit numbers: 16 (bf16) or 22 (fp16) bits of it.  An
-// overflowing hi stays infinite.
+// An fp32 number as a sum of 16-bit ones, the largest first: bf16 three, which
+// hold every bit of it (each takes the leading 8 of what is left, cut off, so
+// that none overflows), fp16 two, off by 2^-22 of it at most.  fp16's range is
+// the caller's to keep (row_scale below).  The parts behind an infinity or a
+// NaN are 0.
 template <typename E>
-__device__ __forceinline__ void split16(float x, E* hi, E* lo) {
-  const E h = (E)x;
-  const float d = x - (float)h;
-  *hi = h;
-  *lo = (E)(fabsf(d) < 3e38f ? d : 0.0f);
+struct Parts;
+template <>
+struct Parts<__bf16> {
+  static constexpr int N = 3;
+  static __device__ __forceinline__ void split(float x, __bf16 (&o)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const uint32_t top = __float_as_uint(x) & 0xffff0000u;
+      o[i] = __builtin_bit_cast(__bf16, (uint16_t)(top >> 16));
+      const float d = x - __uint_as_float(top);
+      x = fabsf(d) < 3e38f ? d : 0.0f;
+    }
+  }
+};
+template <>
+struct Parts<_Float16> {
+  static constexpr int N = 2;
+  static __device__ __forceinline__ void split(float x, _Float16 (&o)[N]) {
+    o[0] = (_Float16)x;
+    const float d = x - (float)o[0];
+    o[1] = (_Float16)(fabsf(d) < 3e38f ? d : 0.0f);
+  }
+};
+// The power of two that brings values of up to `top` below 2^15, the largest
+// above 2^14 (values below 2^-100 stay smaller), and its inverse.
+__device__ __forceinline__ float row_scale(float top, float* inverse) {
+  int e = (int)(__float_as_uint(top) >> 23) - 126;   // top < 2^e; infinity: 129
+  e = min(max(e, -100), 128);
+  *inverse = __uint_as_float((uint32_t)(112 + e) << 23);
+  return __uint_as_float((uint32_t)(142 - e) << 23);
 }
 
 #endif

@@ -276,9 +276,10 @@ __device__ __forceinline__ void dense_tile(const DenseJob& p, int m0, int nt, ch
   }
 
   // each adapter present in the wave's rows in turn: its product goes to sums of
-  // its own, which only that adapter's rows take up.  s enters as two 16-bit
-  // operands (its high and low part), so that it is not rounded to one.  Two
-  // or four 16-deep steps are loaded together, and all rows where there are
+  // its own, which only that adapter's rows take up.  s enters in two or three
+  // 16-bit parts (Parts), so that it is not rounded to one, and in fp16 times a
+  // power of two of its row's own, which is taken out of the sums: any fp32
+  // value of s counts, as it does in the kernels of few tokens.  Two or four 16-deep steps are loaded together, and all rows where there are
   // registers for it (256 accumulators leave none: they would have to leave the
   // matrix cores' registers at once): the time is the loads' latency.
   if constexpr (LORA) {
@@ -340,14 +341,26 @@ __device__ __forceinline__ void dense_tile(const DenseJob& p, int m0, int nt, ch
 #pragma unroll
         for (int fm = f0; fm < f0 + FB; ++fm) {
           if (!__ballot(mine[fm - f0])) continue;
-          v8 hi[HS], lo[HS];
+          constexpr int NP = Parts<E>::N;
+          float scale = 1.0f, unscale = 1.0f;
+          if constexpr (std::is_same<E, _Float16>::value) {
+            float top = 0.0f;
+#pragma unroll
+            for (int h = 0; h < HS; ++h)
+#pragma unroll
+              for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(sv[fm - f0][h].v[e]));
+            top = fmaxf(top, __shfl_xor(top, 32));   // the row's other half
+            scale = row_scale(top, &unscale);
+          }
+          v8 part[NP][HS];
 #pragma unroll
           for (int h = 0; h < HS; ++h)
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              E x, y;
-              split16(sv[fm - f0][h].v[e], &x, &y);
-              hi[h][e] = x, lo[h][e] = y;
+              E x[NP];
+              Parts<E>::split(sv[fm - f0][h].v[e] * scale, x);
+#pragma unroll
+              for (int i = 0; i < NP; ++i) part[i][h][e] = x[i];
             }
 #pragma unroll
           for (int fn = 0; fn < FN; ++fn) {
@@ -355,9 +368,11 @@ __device__ __forceinline__ void dense_tile(const DenseJob& p, int m0, int nt, ch
 #pragma unroll
             for (int q = 0; q < 16; ++q) t[q] = 0.0f;
 #pragma unroll
-            for (int h = 0; h < HS; ++h) t = mfma32(bv[h][fn], hi[h], mfma32(bv[h][fn], lo[h], t));
+            for (int h = 0; h < HS; ++h)
 #pragma unroll
-            for (int q = 0; q < 16; ++q) acc[fm][fn][q] += mine[fm - f0] ? t[q] : 0.0f;
+              for (int i = NP - 1; i >= 0; --i) t = mfma32(bv[h][fn], part[i][h], t);
+#pragma unroll
+            for (int q = 0; q < 16; ++q) acc[fm][fn][q] += mine[fm - f0] ? t[q] * unscale : 0.0f;
           }
         }
       }
