@@ -182,32 +182,56 @@ __device__ __forceinline__ void gate_act_grad(int act, float g, float* a, float*
 }
 
 // An fp32 number as a sum of 16-bit ones, the largest first: bf16 three, which
-// hold every bit of it (each takes the leading 8 of what is left, cut off, so
-// that none overflows), fp16 two, off by 2^-22 of it at most.  fp16's range is
-// the caller's to keep (row_scale below).  The parts behind an infinity or a
-// NaN are 0.
+// hold every bit of it, fp16 two, off by 2^-22 of it at most; fp16's range is
+// the caller's to keep (row_scale below).  Each takes the leading bits of what
+// is left, cut off: so none overflows and all have the number's sign.  A part
+// with nothing left is the smallest number of that sign (2^-133, or 2^-24
+// beside a row's 2^14) where the whole is not 0: a product with an infinity is
+// then that infinity in every part, as it is for the whole.
 template <typename E>
 struct Parts;
 template <>
 struct Parts<__bf16> {
   static constexpr int N = 3;
-  static __device__ __forceinline__ void split(float x, __bf16 (&o)[N]) {
+  static __device__ __forceinline__ void split(const float (&x)[8], Vec<__bf16>::v8 (&o)[N]) {
+    uint32_t w[N][4];
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const uint32_t top = __float_as_uint(x) & 0xffff0000u;
-      o[i] = __builtin_bit_cast(__bf16, (uint16_t)(top >> 16));
-      const float d = x - __uint_as_float(top);
-      x = fabsf(d) < 3e38f ? d : 0.0f;
+    for (int j = 0; j < 4; ++j) {
+      uint32_t t[N][2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float a = fabsf(x[2 * j + i]), least = fminf(a, 0x1p-133f);
+        t[0][i] = __float_as_uint(a) & 0xffff0000u;
+        const float d = fmaxf(a - __uint_as_float(t[0][i]), least);   // (`least` behind an infinity)
+        t[1][i] = __float_as_uint(d) & 0xffff0000u;
+        t[2][i] = __float_as_uint(fmaxf(d - __uint_as_float(t[1][i]), least));
+      }
+      const uint32_t sign = high_halves(__float_as_uint(x[2 * j]), __float_as_uint(x[2 * j + 1])) & 0x80008000u;
+#pragma unroll
+      for (int k = 0; k < N; ++k) w[k][j] = high_halves(t[k][0], t[k][1]) | sign;
     }
+#pragma unroll
+    for (int k = 0; k < N; ++k) o[k] = __builtin_bit_cast(Vec<__bf16>::v8, w[k]);
+  }
+  static __device__ __forceinline__ uint32_t high_halves(uint32_t a, uint32_t b) {
+    return __builtin_amdgcn_perm(b, a, 0x07060302u);
   }
 };
 template <>
 struct Parts<_Float16> {
   static constexpr int N = 2;
-  static __device__ __forceinline__ void split(float x, _Float16 (&o)[N]) {
-    o[0] = (_Float16)x;
-    const float d = x - (float)o[0];
-    o[1] = (_Float16)(fabsf(d) < 3e38f ? d : 0.0f);
+  static __device__ __forceinline__ void split(const float (&x)[8], Vec<_Float16>::v8 (&o)[N]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const auto top = __builtin_amdgcn_cvt_pkrtz(x[2 * j], x[2 * j + 1]);   // cut off
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float a = fabsf(x[2 * j + i]);
+        const float rest = fmaxf(a - fabsf((float)top[i]), fminf(a, 0x1p-24f));
+        o[0][2 * j + i] = (_Float16)top[i];
+        o[1][2 * j + i] = (_Float16)copysignf(rest, x[2 * j + i]);
+      }
+    }
   }
 };
 // The power of two that brings values of up to `top` below 2^15, the largest

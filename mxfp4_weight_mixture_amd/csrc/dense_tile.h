@@ -354,14 +354,16 @@ __device__ __forceinline__ void dense_tile(const DenseJob& p, int m0, int nt, ch
           }
           v8 part[NP][HS];
 #pragma unroll
-          for (int h = 0; h < HS; ++h)
+          for (int h = 0; h < HS; ++h) {
+            v8 x[NP];
+            if constexpr (std::is_same<E, _Float16>::value) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              E x[NP];
-              Parts<E>::split(sv[fm - f0][h].v[e] * scale, x);
-#pragma unroll
-              for (int i = 0; i < NP; ++i) part[i][h][e] = x[i];
+              for (int e = 0; e < 8; ++e) sv[fm - f0][h].v[e] *= scale;
             }
+            Parts<E>::split(sv[fm - f0][h].v, x);
+#pragma unroll
+            for (int i = 0; i < NP; ++i) part[i][h] = x[i];
+          }
 #pragma unroll
           for (int fn = 0; fn < FN; ++fn) {
             v16f t;

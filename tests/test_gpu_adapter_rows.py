@@ -71,3 +71,45 @@ def test_precision_and_range(T, N, base, dtype):
     bound = F32 * low + split + 2 * (r + 2) * F32 * low + (r + 4) * F32 * (main.abs() + ref.abs())
     over = (got - ref - main).abs() - bound
     assert got.isfinite().all() and over.max() <= 0, (over.max().item(), ids[over.amax(1).argmax()].item())
+
+
+@pytest.mark.parametrize("T,N", SIZES)
+@pytest.mark.parametrize("base", ["random", None])
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_infinities_in_an_adapter(T, N, base, dtype):
+    """An infinity in B gives infinities of the right sign (NaN where it meets a zero or one of the other sign),
+    whatever the number of tokens; an infinite scale gives infinities of the signs of x A^T and B."""
+    R, n = 24, 4
+    x = du.normal((T, K), 1.0, dtype, T)
+    ids = (torch.arange(T, device="cuda") * 5 // 30 % (n + 1) - 1).int()
+    a, b = du.normal((n, R, K), K ** -0.5, dtype, T + 1), du.normal((n, N, R), 1.0, dtype, T + 2)
+    w = du.normal((N, K), K ** -0.5, dtype, T + 3) if base else None
+    scales, ranks = torch.tensor([0.5, 1.0, 2.0, 1.0], device="cuda"), [24, 24, 16, 1]
+    f = mx.AdapterLinear(w, a, b, scales=scales, ranks=torch.tensor(ranks, dtype=torch.int32, device="cuda"))
+    clean = f.forward(x, ids, out_dtype=F)
+    cols = [0, 5, 17, 70, N - 1]
+    b[0, 0, 3], b[0, 5, 23], b[1, 17, 0], b[2, 70, 15] = float("inf"), float("-inf"), float("inf"), float("-inf")
+    b[1, N - 1, 4], b[1, N - 1, 9], a[2, 15] = float("inf"), float("-inf"), 0.0
+    b[2, 70, 16] = float("inf")   # behind the rank
+    scales[3] = float("inf")
+    got = f.forward(x, ids, out_dtype=F)
+    low = torch.stack([torch.mm(x.double(), a[max(i, 0)].double().t()) for i in range(n)])   # [n][T][R]
+    rest = torch.ones(N, dtype=torch.bool)
+    rest[cols] = False
+    for i in range(-1, n):
+        rows = (ids == i).nonzero()[:, 0]
+        if i < 0 or rows.numel() == 0:
+            assert torch.equal(got[rows], clean[rows])
+            continue
+        r = ranks[i]
+        s = scales[i].double() * low[i][rows][:, :r]
+        if i == 3:
+            assert torch.equal(got[rows], (s * b[i, :, 0].double()).float())
+            continue
+        if i != 2:
+            assert torch.equal(got[rows][:, rest], clean[rows][:, rest]) and got[rows][:, rest].isfinite().all()
+        want = (s[:, None, :] * b[i, cols, :r].double()).sum(2)
+        at = got[rows][:, cols].double()
+        assert torch.equal(at.isnan(), want.isnan()), i
+        assert torch.equal(at.isposinf(), want.isposinf()) and torch.equal(at.isneginf(), want.isneginf()), i
+    assert T == 3 or (ids < 0).any() and got[ids == 0].isinf().any() and (T < 100 or got[ids == 2].isnan().any())
