@@ -451,6 +451,9 @@ typedef struct moe_ffn_args {
 
 size_t     moe_gated_ffn_workspace_size(int32_t T, int32_t H, int32_t I);
 moe_status moe_gated_ffn_forward(const moe_ffn_args* args, void* stream);
+/* forward's checks alone: its status for these arguments, with nothing enqueued
+ * (for a caller whose other work must not start before a refusal). */
+moe_status moe_gated_ffn_check(const moe_ffn_args* args);
 
 /* The block's gradients from dout and the gate_up that forward kept:
  *   dh = dout * w2;  d_gate = dh * up * act'(gate);  d_up = dh * act(gate)

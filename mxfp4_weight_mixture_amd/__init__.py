@@ -129,6 +129,7 @@ def _load():
         "moe_layer_graph_destroy": (ctypes.c_int, [_vp]),
         "moe_gated_ffn_workspace_size": (_sz, [_i32, _i32, _i32]),
         "moe_gated_ffn_forward": (ctypes.c_int, [ctypes.POINTER(FfnArgs), _vp]),
+        "moe_gated_ffn_check": (ctypes.c_int, [ctypes.POINTER(FfnArgs)]),
         "moe_gated_ffn_grad_workspace_size": (_sz, [_i32, _i32, _i32]),
         "moe_gated_ffn_backward": (ctypes.c_int, [ctypes.POINTER(FfnGradArgs), _vp]),
         "moe_adapter_workspace_size": (_sz, [_i32, _i32, _i32, _i32, _i32]),
@@ -401,6 +402,14 @@ class GatedFFN:
         gate_up [T][2I] for backward(), True in fp32, "half" in the weights' type (half the memory, one more
         rounding in the gradients).
         """
+        a, out, gate_up, ws = self._prepare(x, add, out, out_dtype, save, stream)
+        _check(lib.moe_gated_ffn_forward(ctypes.byref(a), _stream(stream)))
+        _keep_until_done(stream, out, gate_up)
+        return (out, gate_up) if save else out
+
+    def _prepare(self, x, add, out, out_dtype=None, save=False, stream=None):
+        """forward's arguments, checked by the binding, and the buffers of one call: (arguments, out, gate_up,
+        workspace)."""
         _on_current_device(self.device, stream)
         a = FfnArgs.from_buffer_copy(self._fwd)
         a.x_stride = _rows("x", x, None, self.H, (self.dtype,), self.device)
@@ -431,9 +440,7 @@ class GatedFFN:
             ws = _u8(n, self.device)
         a.x, a.w1, a.w2, a.out = x.data_ptr(), self.w1.data_ptr(), self.w2.data_ptr(), out.data_ptr()
         a.workspace, a.workspace_bytes = ws.data_ptr(), n
-        _check(lib.moe_gated_ffn_forward(ctypes.byref(a), _stream(stream)))
-        _keep_until_done(stream, out, gate_up)
-        return (out, gate_up) if save else out
+        return a, out, gate_up, ws
 
     def backward(self, dout: torch.Tensor, x: torch.Tensor, gate_up: torch.Tensor, *, dx=True, dw1=True, dw2=True,
                  dw_dtype: Optional[torch.dtype] = None, accumulate: bool = False, stream=None):
@@ -639,11 +646,19 @@ class Layer:
             with _allocate_on(stream):
                 out = torch.empty((T, self.H), dtype=torch.float32, device=logits.device)
         args = self._args(T, logits, x, x_scales, out, x_next, ws)
+        # the shared expert may refuse its tensors: before the routed experts are enqueued
+        shared = None if x_shared is None else self._prepare_shared(x_shared, out, stream)
         _check(lib.moe_layer_forward(ctypes.byref(args), _stream(stream)))
+        if shared is not None:
+            _check(lib.moe_gated_ffn_forward(ctypes.byref(shared[0]), _stream(stream)))
         _keep_until_done(stream, ws, out)   # (routing() shows the workspace to the caller)
-        if x_shared is not None:
-            self.shared.forward(x_shared, add=out, out=out, stream=stream)
         return out
+
+    def _prepare_shared(self, x_shared, out, stream=None):
+        """The shared expert's call that adds to `out`, every check made."""
+        call = self.shared._prepare(x_shared, out, out, stream=stream)
+        _check(lib.moe_gated_ffn_check(ctypes.byref(call[0])))
+        return call
 
     def capture(self, logits: torch.Tensor, x: torch.Tensor, x_scales: Optional[torch.Tensor] = None,
                 out: Optional[torch.Tensor] = None, x_next: Optional[torch.Tensor] = None,
@@ -668,12 +683,12 @@ class LayerGraph:
     The graph owns its workspace and keeps the tensors it was captured on:
     replay() runs the five steps with one launch, reading the current contents
     of logits / x / x_scales and writing `out` (and x_next); a shared expert
-    follows as launches of its own.  Replays on one graph must not overlap each
-    other.
+    follows as launches of its own, on a workspace that the graph owns too.
+    Replays on one graph must not overlap each other.
     """
 
     def __init__(self, layer: Layer, logits, x, x_scales=None, out=None, x_next=None, x_shared=None):
-        self.x_shared = layer._shared_input(x, x_scales, x_shared, x_next)
+        x_shared = layer._shared_input(x, x_scales, x_shared, x_next)
         T = logits.shape[0]
         dev = logits.device
         self.layer, self.T = layer, T
@@ -681,6 +696,8 @@ class LayerGraph:
         self.out = out if out is not None else torch.empty((T, layer.H), dtype=torch.float32, device=dev)
         self.ws = _u8(layer.workspace_bytes(T), dev)
         args = layer._args(T, logits, x, x_scales, self.out, x_next, self.ws)
+        self.shared, self.x_shared = layer.shared, x_shared
+        self._shared_call = None if x_shared is None else layer._prepare_shared(x_shared, self.out)
         # replays may run on any stream: what the current one still does with these buffers' memory ends here
         if not torch.cuda.is_current_stream_capturing():
             torch.cuda.current_stream(dev).synchronize()
@@ -693,9 +710,11 @@ class LayerGraph:
     def replay(self, stream=None) -> torch.Tensor:
         if not self._h:
             raise MoeError(STATUS["MOE_ERR_INVALID_ARG"], "graph already destroyed")
+        if self._shared_call is not None:
+            _on_current_device(self.shared.device, stream)
         _check(lib.moe_layer_graph_launch(self._h, _stream(stream)))
-        if self.x_shared is not None:
-            self.layer.shared.forward(self.x_shared, add=self.out, out=self.out, stream=stream)
+        if self._shared_call is not None:
+            _check(lib.moe_gated_ffn_forward(ctypes.byref(self._shared_call[0]), _stream(stream)))
         return self.out
 
     def routing(self):

@@ -60,7 +60,7 @@ size_t moe_gated_ffn_workspace_size(int32_t T, int32_t H, int32_t I) {
   return ffn_ws(T, H, I).total;
 }
 
-moe_status moe_gated_ffn_forward(const moe_ffn_args* a, void* stream) {
+moe_status moe_gated_ffn_check(const moe_ffn_args* a) {
   const char* what = "gated FFN";
   clear_error();
   if (!a) return fail(MOE_ERR_INVALID_ARG, "%s: null args", what);
@@ -70,8 +70,7 @@ moe_status moe_gated_ffn_forward(const moe_ffn_args* a, void* stream) {
   MXMOE_TRY(check_stride(what, "x_stride", a->x_stride, a->H));
   MXMOE_TRY(check_stride(what, "out_stride", a->out_stride, a->H));
   if (a->add) MXMOE_TRY(check_stride(what, "add_stride", a->add_stride, a->H));
-  const Ws w = ffn_ws(a->T, a->H, a->I);
-  const size_t need = w.total;
+  const size_t need = ffn_ws(a->T, a->H, a->I).total;
   if (a->T > 0) {
     if (!a->x || !a->w1 || !a->w2 || !a->out) return fail(MOE_ERR_INVALID_ARG, "%s: null pointer", what);
     if (!a->workspace || a->workspace_bytes < need)
@@ -86,8 +85,13 @@ moe_status moe_gated_ffn_forward(const moe_ffn_args* a, void* stream) {
                        span("add", in_place ? nullptr : a->add, T, H, a->add_stride, a->out_dtype)};
     MXMOE_TRY(check_spans(what, out, 3, in, 4));
   }
-  MXMOE_TRY(check_device());
+  return check_device();
+}
+
+moe_status moe_gated_ffn_forward(const moe_ffn_args* a, void* stream) {
+  MXMOE_TRY(moe_gated_ffn_check(a));
   if (a->T == 0) return MOE_OK;
+  const Ws w = ffn_ws(a->T, a->H, a->I);
   uint8_t* ws = static_cast<uint8_t*>(a->workspace);
   const hipStream_t s = (hipStream_t)stream;
 

@@ -30,7 +30,7 @@ class Library:
         def call(*args):
             if name.endswith(("_workspace_size", "_bytes")):
                 return 64
-            if name.endswith("_offset"):
+            if name.endswith(("_offset", "_check")):   # (nothing enqueued)
                 return 0
             self.calls.append((name, [a.value for a in args if isinstance(a, ctypes.c_void_p)]))
             return 0
@@ -146,3 +146,30 @@ def test_a_captured_layer_owns_its_memory_before_it_is_replayed(world):
     """Replays may go to any stream: nothing earlier may still use the graph's buffers."""
     _layer().capture(z(5, 4, dtype=torch.float32), z(5, 32))
     assert world.main.synced
+
+
+def test_a_refused_shared_expert_comes_before_any_launch(world):
+    """What the library refuses of the shared expert's tensors is refused before the routed experts are enqueued,
+    in a call and in a captured layer."""
+    order = []
+
+    class Refusing(Library):
+        def __getattr__(self, name):
+            if name == "moe_last_error_message":
+                return lambda: b"refused"
+            call = super().__getattr__(name)
+            if name not in ("moe_gated_ffn_check", "moe_gated_ffn_forward"):
+                return lambda *a: (order.append(name), call(*a))[1]
+            return lambda *a: (order.append(name), mx.STATUS["MOE_ERR_SHAPE"])[1]
+
+    mx.lib = Refusing()
+    layer, logits, x = _layer(shared=_ffn()), z(5, 4, dtype=torch.float32), z(5, 32)
+    with pytest.raises(mx.MoeError, match="refused"):
+        layer.forward(logits, x)
+    with pytest.raises(mx.MoeError, match="refused"):
+        layer.capture(logits, x)
+    assert "moe_layer_forward" not in order and "moe_layer_graph_create" not in order
+    # nothing of the call's tensors fits: the binding's own checks come first, too
+    with pytest.raises(ValueError, match="out"):
+        layer.forward(logits, x, out=z(6, 32, dtype=torch.float32))
+    assert "moe_layer_forward" not in order
