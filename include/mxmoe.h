@@ -449,6 +449,7 @@ typedef struct moe_ffn_args {
   size_t      workspace_bytes;
 } moe_ffn_args;
 
+/* (0 for sizes outside the limits above, as for the two queries below) */
 size_t     moe_gated_ffn_workspace_size(int32_t T, int32_t H, int32_t I);
 moe_status moe_gated_ffn_forward(const moe_ffn_args* args, void* stream);
 /* forward's checks alone: its status for these arguments, with nothing enqueued

@@ -13,6 +13,8 @@
 namespace mxmoe {
 namespace {
 
+constexpr int kMaxAdapters = 65536, kMaxRank = 256;
+
 // s of few tokens.  A block takes one token and four rows of its adapter's A,
 // its four waves a quarter of K each: tokens of a decode batch have adapters
 // of their own, so there is little to share, and the time is one trip to memory.
@@ -136,7 +138,8 @@ using namespace mxmoe;
 extern "C" {
 
 size_t moe_adapter_workspace_size(int32_t T, int32_t K, int32_t N, int32_t num_adapters, int32_t R) {
-  if (T < 0 || K < 1 || N < 1 || num_adapters < 0 || R < 1) return 0;
+  if (T < 0 || T > kMaxTokens || K < 1 || K > kMaxWidth || N < 1 || N > kMaxWidth) return 0;
+  if (num_adapters < 0 || num_adapters > kMaxAdapters || R < 1 || R > kMaxRank) return 0;
   return adapter_ws_bytes(T, K, N, R);
 }
 
@@ -147,10 +150,10 @@ moe_status moe_adapter_linear(const moe_adapter_args* a, void* stream) {
   MXMOE_TRY(check_width(what, "K", a->K));
   MXMOE_TRY(check_width(what, "N", a->N));
   MXMOE_TRY(check_tokens(what, a->T, a->N));
-  if (a->num_adapters < 0 || a->num_adapters > 65536)
-    return fail(MOE_ERR_SHAPE, "%s: num_adapters = %d outside [0, 65536]", what, a->num_adapters);
-  if (a->R < 8 || a->R > 256 || a->R % 8)
-    return fail(MOE_ERR_SHAPE, "%s: R = %d must be a multiple of 8 in [8, 256]", what, a->R);
+  if (a->num_adapters < 0 || a->num_adapters > kMaxAdapters)
+    return fail(MOE_ERR_SHAPE, "%s: num_adapters = %d outside [0, %d]", what, a->num_adapters, kMaxAdapters);
+  if (a->R < 8 || a->R > kMaxRank || a->R % 8)
+    return fail(MOE_ERR_SHAPE, "%s: R = %d must be a multiple of 8 in [8, %d]", what, a->R, kMaxRank);
   const bool gate = a->epilogue != MOE_EPI_NONE;
   if (gate && a->epilogue != MOE_EPI_SWIGLU_SPLIT && a->epilogue != MOE_EPI_SWIGLU_INTERLEAVED)
     return fail(MOE_ERR_INVALID_ARG, "%s: bad epilogue %d", what, a->epilogue);

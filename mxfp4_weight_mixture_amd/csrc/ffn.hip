@@ -23,6 +23,11 @@ moe_status check_block(const char* what, int T, int H, int I, int layout, int ac
   return check_dtype16(what, dtype);
 }
 
+// Sizes that a call may take, as far as the size queries' arithmetic needs it.
+bool within_limits(int T, int H, int I) {
+  return T >= 0 && T <= kMaxTokens && H > 0 && H <= kMaxWidth && I > 0 && I <= kMaxWidth;
+}
+
 // Workspaces: h, for the gradients d_gate_up and h; then the products' scratch
 // (they run one after the other).
 struct Ws {
@@ -56,7 +61,7 @@ using namespace mxmoe;
 extern "C" {
 
 size_t moe_gated_ffn_workspace_size(int32_t T, int32_t H, int32_t I) {
-  if (T < 0 || H < 1 || I < 1) return 0;
+  if (!within_limits(T, H, I)) return 0;
   return ffn_ws(T, H, I).total;
 }
 
@@ -119,7 +124,7 @@ moe_status moe_gated_ffn_forward(const moe_ffn_args* a, void* stream) {
 }
 
 size_t moe_gated_ffn_grad_workspace_size(int32_t T, int32_t H, int32_t I) {
-  if (T < 0 || H < 1 || I < 1) return 0;
+  if (!within_limits(T, H, I)) return 0;
   return grad_ws(T, H, I).total;
 }
 
