@@ -460,7 +460,9 @@ moe_status moe_gated_ffn_check(const moe_ffn_args* args);
  *   dh = dout * w2;  d_gate = dh * up * act'(gate);  d_up = dh * act(gate)
  *   dx = d_gate_up * w1;  dw1 = d_gate_up^T * x;  dw2 = dout^T * h
  * (the gradient of `add` is dout).  Any of dx, dw1, dw2 may be NULL: it is not
- * computed.  d_gate_up and h are rounded once to `dtype`.  With accumulate
+ * computed.  d_gate_up and h are rounded once to `dtype`, the operands of the
+ * products that follow: in fp16 a d_gate_up below 2^-25 becomes 0 and one of
+ * 65520 or more infinite, so scale dout as fp16 training does.  With accumulate
  * dw1 and dw2 hold earlier gradients and are added to, in fp32, before their
  * rounding.  T == 0 writes zeros to dw1 and dw2 (leaves them with accumulate).
  * Deterministic: no atomics.  Size, stride and overlap rules as above. */

@@ -172,6 +172,9 @@ def _u8(n: int, device) -> torch.Tensor:
     return torch.empty(max(int(n), 1), dtype=torch.uint8, device=device)
 
 
+_CURRENT = contextlib.nullcontext()
+
+
 def _allocate_on(stream):
     """Context in which a call allocates its buffers: on the stream that uses them.
 
@@ -179,7 +182,7 @@ def _allocate_on(stream):
     stream that the block belongs to: that stream's order protects what still runs.  A
     block of the current stream would reach `stream`, which does not wait for it, while
     earlier work of the current stream still uses it."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+    return _CURRENT if stream is None else torch.cuda.stream(stream)
 
 
 def _keep_until_done(stream, *tensors):
@@ -373,7 +376,9 @@ class GatedFFN:
     fp16; fp32 accumulation; h = act(..) * (..) is rounded once to the weights' type.
 
     The object holds no buffers of its own: calls from several streams or threads, and calls captured into
-    graphs, are independent of each other.
+    graphs, are independent of each other.  Autograd does not record the calls, results carry no history: a
+    training step calls backward() itself.  fp16 gradients have fp16's range on the way, too (what backward
+    keeps of the gate's and up's gradients is 0 below 2^-25 and infinite from 65520 on): scale the loss.
     """
 
     def __init__(self, w1: torch.Tensor, w2: torch.Tensor, layout: str = "split", act: str = "silu"):
@@ -498,7 +503,8 @@ class AdapterLinear:
     elsewhere), lora_a [num_adapters][R][K], lora_b [num_adapters][N][R], scales fp32 and ranks int32
     [num_adapters].  epilogue "split" or "interleaved": w's rows are gate and up, out = act(gate) * up.
 
-    Adapters may be replaced in place between calls.  No buffers are held (see GatedFFN).
+    Adapters may be replaced in place between calls.  No buffers are held and nothing is recorded by autograd
+    (see GatedFFN); there is no backward pass.
     """
 
     def __init__(self, w: Optional[torch.Tensor], lora_a: torch.Tensor, lora_b: torch.Tensor, *,

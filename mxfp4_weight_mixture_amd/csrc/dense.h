@@ -41,7 +41,12 @@ struct DenseJob {
 
 // Token counts up to this are decode batches: their adapters differ from token
 // to token.  (By size, not by what the ids hold: a row's result does not depend
-// on its neighbours'.)
+// on its neighbours'.)  Measured on both sides, 4096 x 4096, 48 adapters of rank
+// 16, as a decode batch / as a prompt, us: 256 mixed tokens 27 / 61, 256 in runs
+// 28 / 34; 512 mixed 49 / 79, 512 in runs 47 / 47; 2048 in runs 173 / 80.  With
+// 7 adapters of rank 64, 2216 x 1544: 256 mixed 36 / 52, 256 in runs 35 / 32, 512
+// mixed 51 / 53, 512 in runs 49 / 42.  So mixed batches of 257 to 1024 tokens pay
+// for the prompts of that size (257 mixed tokens of the first: 170, against 44).
 constexpr int kFewTokens = 256;
 
 // Scratch of a product: M, N, K, epi, ta, tb and whether there are ids decide.
@@ -156,7 +161,9 @@ __device__ __forceinline__ v4f mfma16(Vec<_Float16>::v8 a, Vec<_Float16>::v8 b, 
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
 
-// sigmoid, exact at both ends: e^-z overflows to infinity and the reciprocal is 0
+// sigmoid, exact at both ends: e^-z overflows to infinity and the reciprocal is 0.
+// Hardware exp2 and reciprocal, 1 ulp each: off by (2 + |z|) 2^-23 of the result
+// at most, against 2^-8 (bf16) or 2^-11 (fp16) when h is rounded
 __device__ __forceinline__ float sigmoid(float z) { return __builtin_amdgcn_rcpf(1.0f + __expf(-z)); }
 
 // act(g) and act'(g).  The tanh GELU is g * sigmoid(2 p(g)) with

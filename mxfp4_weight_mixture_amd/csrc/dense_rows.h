@@ -106,7 +106,11 @@ __device__ __forceinline__ void finish_plain(const DenseJob& p, int m, int n, F8
   }
   store8<E>(p.c, p.c_dtype, (size_t)m * p.ldc + n, v);
 }
-// Gate: g, u are the pre-activations of gate indices [i, i + 8).
+// Gate: g, u are the pre-activations of gate indices [i, i + 8).  The gate is
+// taken of the fp32 sums; h is rounded once, to the 16 bits that the second
+// product's matrix instructions take.  Two parts of it, as the adapters' small
+// rows have, would double that product, a third of the block's work, for an
+// error of the output 0.7 times as large.
 template <typename E>
 __device__ __forceinline__ void finish_gate(const DenseJob& p, int m, int i, F8 g, F8 u) {
   const int I = p.N >> 1;
@@ -135,7 +139,9 @@ __device__ __forceinline__ void finish_gate(const DenseJob& p, int m, int i, F8 
   for (int e = 0; e < 8; ++e) h.v[e] = gate_act(p.act, g.v[e]) * u.v[e];
   store8<E>(p.c, p.c_dtype, (size_t)m * p.ldc + i, h);
 }
-// Gate gradient: d are dh's columns [i, i + 8).
+// Gate gradient: d are dh's columns [i, i + 8), in fp32.  h and the gradients of
+// gate and up are rounded once each, to the next products' 16-bit operands, in
+// fp16 with its range: the loss is scaled for it, as for dout itself.
 template <typename E>
 __device__ __forceinline__ void finish_gate_grad(const DenseJob& p, int m, int i, F8 d) {
   if (p.partial) return store8<E>(p.partial, MOE_FLOAT_FP32, (size_t)m * p.N + i, d);

@@ -12,7 +12,10 @@
 // against 34 us, 1552 x 1096 x 517 9.0 against 11.9).  Long rows do better in
 // stages of 64 k, a whole line per row and load (192 x 4096 x 4096 15.0 against
 // 17.4 us, 100 x 7168 x 7168 22.4 against 27.0), short ones do not (517 x 1096
-// x 1552 8.7 against 8.2).
+// x 1552 8.7 against 8.2).  The sides meet lower than the choice at K = 4096:
+// 100 x 4096 outputs take 7.1 us in 32-deep stages and 7.9 in 64-deep ones at
+// K = 1552, 8.3 and 8.9 at 2560, 14.4 and 12.5 at 3584; 512 x 4096 take 17.6 and
+// 18.7, 24.1 and 22.0, 31.4 and 26.8.
 //
 // Adapters: each thread adds its row's low-rank product to its eight columns,
 // so mixed adapters cost no more than equal ones.
