@@ -643,11 +643,14 @@ class Layer:
         T = logits.shape[0]
         n = self.workspace_bytes(T)
         ws, on = self._ws, torch.cuda.current_stream(logits.device) if stream is None else stream
-        # a call on another stream gets a workspace of its own: the kept one may still be in use
-        if ws is None or ws.numel() < n or self._ws_stream != on:
+        with _allocate_on(stream):
+            captured = torch.cuda.is_current_stream_capturing()
+        # a call on another stream gets a workspace of its own (the kept one may still be in use), and one that
+        # the caller captures does too: its graph goes on using it, and owns its memory
+        if ws is None or ws.numel() < n or self._ws_stream != on or captured:
             with _allocate_on(stream):
                 ws = _u8(n, logits.device)
-            self._ws, self._ws_stream = ws, on
+            self._ws, self._ws_stream = ws, None if captured else on
         if out is None:
             with _allocate_on(stream):
                 out = torch.empty((T, self.H), dtype=torch.float32, device=logits.device)

@@ -87,3 +87,36 @@ def test_results_read_late_on_the_current_stream(calls, name):
         call(1 - r % 2, side)
         torch.cuda.synchronize()
         _same(copies, want[r % 2], (name, r))
+
+
+def test_layers_in_two_captured_graphs():
+    """One layer captured into two graphs, with eager calls of other sizes between: replays of both at once, and
+    after a larger call has replaced the layer's workspace, give the eager results."""
+    s = gen.LayerShape(T=300, H=512, I=256, E=8, k=2, act="bf16", cfg_id=411, layout="split")
+    li = gen.layer_inputs(s)
+    shared = mx.GatedFFN(du.normal((512, 512), 512 ** -0.5, BF, 5), du.normal((512, 256), 256 ** -0.5, BF, 6))
+    layer = mx.Layer(*device_weights(s), k=2, layout="split", shared=shared)
+    logits = torch.from_numpy(li.logits).to("cuda")
+    x = device_x(li)[0]
+    layer.forward(logits, x)
+    torch.cuda.synchronize()
+    runs = []
+    for T in (300, 200):
+        lg, xx = logits[:T].clone(), x[:T].clone()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = layer.forward(lg, xx)
+        runs.append((g, lg, xx, out))
+    side = torch.cuda.Stream()
+    for k in range(4):
+        for _, _, xx, _ in runs:
+            xx.copy_(du.normal(tuple(xx.shape), 1.0, BF, 50 + k))
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            runs[1][0].replay()
+        runs[0][0].replay()
+        torch.cuda.synchronize()
+        for _, lg, xx, out in runs:
+            assert torch.equal(layer.forward(lg, xx), out), k
+        layer.forward(torch.cat([logits] * (k + 2)), torch.cat([x] * (k + 2)))
+        torch.cuda.synchronize()

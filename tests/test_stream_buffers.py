@@ -173,3 +173,17 @@ def test_a_refused_shared_expert_comes_before_any_launch(world):
     with pytest.raises(ValueError, match="out"):
         layer.forward(logits, x, out=z(6, 32, dtype=torch.float32))
     assert "moe_layer_forward" not in order
+
+
+def test_captured_calls_of_a_layer_share_no_workspace(world, monkeypatch):
+    """Graphs that a caller captures keep the memory they were captured on: no two calls in captures, and none
+    outside, use one workspace, whatever stream they are captured on."""
+    layer, logits, x = _layer(), z(5, 4, dtype=torch.float32), z(5, 32)
+    held = []
+    for capturing, stream in ((False, None), (True, None), (True, None), (False, None), (True, world.side),
+                              (False, world.side), (False, world.side)):
+        monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing)
+        layer.forward(logits, x, stream=stream)
+        held.append(layer._ws)
+    assert held[5] is held[6]
+    assert len({id(t) for t in held[:6]}) == 6
