@@ -621,6 +621,12 @@ class Layer:
                          x_next=x_next.data_ptr() if x_next is not None else None,
                          workspace=ws.data_ptr(), workspace_bytes=ws.numel(), w_format=self.w_format)
 
+    def _check_out(self, out, T, device):
+        """The routed experts' sum is written as contiguous fp32 [T][H]."""
+        if out.dtype != torch.float32 or not out.is_contiguous() or out.numel() < T * self.H or out.device != device:
+            raise ValueError(f"out must be a contiguous torch.float32 tensor of {(T, self.H)} on {device}: got "
+                             f"{out.dtype} {tuple(out.shape)}, strides {out.stride()}, on {out.device}")
+
     def _shared_input(self, x, x_scales, x_shared, x_next):
         """The shared expert's activations, [T][H] in its type: x itself where that is what x holds."""
         if self.shared is None:
@@ -654,6 +660,7 @@ class Layer:
         if out is None:
             with _allocate_on(stream):
                 out = torch.empty((T, self.H), dtype=torch.float32, device=logits.device)
+        self._check_out(out, T, logits.device)
         args = self._args(T, logits, x, x_scales, out, x_next, ws)
         # the shared expert may refuse its tensors: before the routed experts are enqueued
         shared = None if x_shared is None else self._prepare_shared(x_shared, out, stream)
@@ -703,6 +710,7 @@ class LayerGraph:
         self.layer, self.T = layer, T
         self.logits, self.x, self.x_scales, self.x_next = logits, x, x_scales, x_next
         self.out = out if out is not None else torch.empty((T, layer.H), dtype=torch.float32, device=dev)
+        layer._check_out(self.out, T, dev)
         self.ws = _u8(layer.workspace_bytes(T), dev)
         args = layer._args(T, logits, x, x_scales, self.out, x_next, self.ws)
         self.shared, self.x_shared = layer.shared, x_shared

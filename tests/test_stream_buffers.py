@@ -187,3 +187,19 @@ def test_captured_calls_of_a_layer_share_no_workspace(world, monkeypatch):
         held.append(layer._ws)
     assert held[5] is held[6]
     assert len({id(t) for t in held[:6]}) == 6
+
+
+@pytest.mark.parametrize("shared", [False, True])
+@pytest.mark.parametrize("bad", [lambda: z(5, 32), lambda: z(4, 32, dtype=torch.float32),
+                                 lambda: z(5, 40, dtype=torch.float32)[:, :32],
+                                 lambda: z(32, 5, dtype=torch.float32).t()])
+def test_a_layer_refuses_results_it_would_not_fill(world, bad, shared):
+    """The routed experts' sum is fp32, [T][H], row behind row: another type, fewer rows or rows further apart are
+    refused before anything is enqueued."""
+    layer, logits, x = _layer(**(dict(shared=_ffn()) if shared else {})), z(5, 4, dtype=torch.float32), z(5, 32)
+    for call in (layer.forward, layer.capture):
+        with pytest.raises(ValueError, match="out"):
+            call(logits, x, out=bad())
+    assert not world.lib.calls
+    layer.forward(logits, x, out=z(5, 32, dtype=torch.float32))
+    assert world.lib.calls
