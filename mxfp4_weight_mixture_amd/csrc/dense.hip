@@ -119,9 +119,10 @@ moe_status launch_join(const DenseJob& j, int splits, const float* partial, hipS
 
 // Few rows: 64 rows of 7168 x 7168 20.2 us, 23.1 in 64 x 64 tiles, of 4096 x 4096
 // 10.2 and 13.7, of 2216 x 1544 5.9 and 8.7 (33 rows 18.2 and 21.4, 8.8 and 11.7,
-// 5.8 and 8.1); more rows would leave the LDS no room for a turn of 64 k.
-// And B's rows contiguous and a block's rows (16 or 32; of a split gate
-// also their up rows, I rows behind) within 31 bits of the first.
+// 5.8 and 8.1; the same weights each time, from the last-level cache); more rows
+// would leave the LDS no room for a turn of 64 k.
+// B's rows are contiguous, and a block's rows (16 or 32; of a split gate
+// also their up rows, I rows behind) lie within 31 bits of the first.
 bool takes_few(const DenseJob& j) {
   const int64_t reach = j.epi == kEpiGate && !j.interleaved ? (int64_t)(j.N / 2 + 16) * j.ldb * 2 : 0;
   return j.M <= 64 && j.epi != kEpiGateGrad && !j.ta && !j.tb && reach < (1ll << 30);

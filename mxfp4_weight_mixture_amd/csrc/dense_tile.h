@@ -14,8 +14,9 @@
 // wave has read all of stage s, so stage s + NST may overwrite it, and
 // every wave's part of stage s + 1 has landed.
 //
-// Measured: 8192 x 7168 x 7168 in 0.67 ms (1.26 PFLOP/s, a library product 0.66),
-// both operands of 4096 x 4096 x 8192 stored [K][rows] in 0.21 ms (1.32).  The
+// Measured: 8192 x 7168 x 7168 in 0.64 to 0.66 ms (1.28 to 1.32 PFLOP/s, a library
+// product 0.53 to 0.64), 0.72 to 0.75 with the gate; both operands of 4096 x 4096
+// x 8192 stored [K][rows] in 0.22 ms (1.27).  The
 // loop takes 1242 to 1366 clocks a stage of 1024 clocks' matrix work, 1065
 // without its DMA; the clock is at 1.4 to 1.7 GHz then (power limit).
 //
