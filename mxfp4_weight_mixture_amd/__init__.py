@@ -186,9 +186,10 @@ def _allocate_on(stream):
 
 
 def _keep_until_done(stream, *tensors):
-    """A call's results, allocated on `stream` or given by the caller: both that stream and
-    the current one, where the caller goes on with them, use them.  Tell the caching allocator
-    so, so that it does not hand their memory out again before either has finished."""
+    """A call's results, allocated on `stream` or given by the caller, and the inputs given with
+    the call: both that stream and the current one, where the caller made them or goes on with
+    them, use them.  Tell the caching allocator so, so that it does not hand their memory out
+    again before either has finished, however soon the caller drops them."""
     if stream is None:
         return
     current = torch.cuda.current_stream(stream.device)
@@ -226,7 +227,7 @@ def route(logits: torch.Tensor, k: int, stream=None):
         ids = torch.empty((T, k), dtype=torch.int32, device=logits.device)
         w = torch.empty((T, k), dtype=torch.float32, device=logits.device)
     _check(lib.moe_route(_ptr(logits), T, E, k, _ptr(ids), _ptr(w), _stream(stream)))
-    _keep_until_done(stream, ids, w)
+    _keep_until_done(stream, ids, w, logits)
     return ids, w
 
 
@@ -242,7 +243,7 @@ def permute(topk_ids: torch.Tensor, E: int, stream=None):
         ws = _u8(n, dev)
     _check(lib.moe_permute(_ptr(topk_ids), T, E, k, _ptr(off), _ptr(ps), _ptr(dr), _ptr(ws), n,
                            _stream(stream)))
-    _keep_until_done(stream, off, ps, dr)
+    _keep_until_done(stream, off, ps, dr, topk_ids)
     return off, ps, dr
 
 
@@ -283,7 +284,7 @@ def grouped_gemm(a: torch.Tensor, w_packed: torch.Tensor, w_scales: torch.Tensor
     with _allocate_on(stream):
         ws = _u8(n, a.device)
     _check(lib.moe_mxfp4_grouped_gemm(ctypes.byref(args), _ptr(ws), n, _stream(stream)))
-    _keep_until_done(stream, c, c_scales)
+    _keep_until_done(stream, c, c_scales, a, w_packed, w_scales, expert_offsets, a_scales, a_gather)
     return (c, c_scales) if c_dt == 2 else c
 
 
@@ -298,7 +299,7 @@ def tile_weights(w_packed: torch.Tensor, w_scales: torch.Tensor, epilogue: str =
     _check(lib.moe_mxfp4_tile_weights(_ptr(w_packed), _ptr(w_scales), E, N, 2 * K2,
                                       {"none": 0, "split": 1, "interleaved": 2}[epilogue], _ptr(tp), _ptr(ts),
                                       _stream(stream)))
-    _keep_until_done(stream, tp, ts)
+    _keep_until_done(stream, tp, ts, w_packed, w_scales)
     return tp, ts
 
 
@@ -310,7 +311,7 @@ def untile_weights(t_packed: torch.Tensor, t_scales: torch.Tensor, epilogue: str
     _check(lib.moe_mxfp4_untile_weights(_ptr(t_packed), _ptr(t_scales), E, N, 2 * K2,
                                         {"none": 0, "split": 1, "interleaved": 2}[epilogue], _ptr(wp), _ptr(ws),
                                         _stream(stream)))
-    _keep_until_done(stream, wp, ws)
+    _keep_until_done(stream, wp, ws, t_packed, t_scales)
     return wp, ws
 
 
@@ -325,7 +326,7 @@ def combine(y: torch.Tensor, dest_row: torch.Tensor, topk_w: torch.Tensor, *, rm
     dt = 1 if y.dtype == torch.bfloat16 else 0
     _check(lib.moe_combine(_ptr(y), dt, _ptr(dest_row), _ptr(topk_w), T, k, H, _ptr(out), _ptr(xn),
                            _stream(stream)))
-    _keep_until_done(stream, out, xn)
+    _keep_until_done(stream, out, xn, y, dest_row, topk_w)
     return (out, xn) if rms_next else out
 
 
@@ -409,7 +410,7 @@ class GatedFFN:
         """
         a, out, gate_up, ws = self._prepare(x, add, out, out_dtype, save, stream)
         _check(lib.moe_gated_ffn_forward(ctypes.byref(a), _stream(stream)))
-        _keep_until_done(stream, out, gate_up)
+        _keep_until_done(stream, out, gate_up, x, add, self.w1, self.w2)
         return (out, gate_up) if save else out
 
     def _prepare(self, x, add, out, out_dtype=None, save=False, stream=None):
@@ -491,7 +492,7 @@ class GatedFFN:
         a.dout, a.x, a.w1, a.w2 = dout.data_ptr(), x.data_ptr(), self.w1.data_ptr(), self.w2.data_ptr()
         a.gate_up, a.workspace, a.workspace_bytes = gate_up.data_ptr(), ws.data_ptr(), n
         _check(lib.moe_gated_ffn_backward(ctypes.byref(a), _stream(stream)))
-        _keep_until_done(stream, dx, dw1, dw2)
+        _keep_until_done(stream, dx, dw1, dw2, dout, x, gate_up, self.w1, self.w2)
         return dx, dw1, dw2
 
 
@@ -574,7 +575,7 @@ class AdapterLinear:
             a.ranks = self.ranks.data_ptr()
         a.workspace, a.workspace_bytes = ws.data_ptr(), n
         _check(lib.moe_adapter_linear(ctypes.byref(a), _stream(stream)))
-        _keep_until_done(stream, out)
+        _keep_until_done(stream, out, x, ids, add, self.w, self.lora_a, self.lora_b, self.scales, self.ranks)
         return out
 
 
@@ -667,7 +668,10 @@ class Layer:
         _check(lib.moe_layer_forward(ctypes.byref(args), _stream(stream)))
         if shared is not None:
             _check(lib.moe_gated_ffn_forward(ctypes.byref(shared[0]), _stream(stream)))
-        _keep_until_done(stream, ws, out)   # (routing() shows the workspace to the caller)
+        # (routing() shows the workspace to the caller)
+        _keep_until_done(stream, ws, out, logits, x, x_scales, x_next, x_shared, self.w1p, self.w1s, self.w2p, self.w2s)
+        if shared is not None:
+            _keep_until_done(stream, self.shared.w1, self.shared.w2)
         return out
 
     def _prepare_shared(self, x_shared, out, stream=None):
@@ -700,7 +704,8 @@ class LayerGraph:
     replay() runs the five steps with one launch, reading the current contents
     of logits / x / x_scales and writing `out` (and x_next); a shared expert
     follows as launches of its own, on a workspace that the graph owns too.
-    Replays on one graph must not overlap each other.
+    Replays on one graph must not overlap each other.  Capturing waits for what
+    the current stream still has to do.
     """
 
     def __init__(self, layer: Layer, logits, x, x_scales=None, out=None, x_next=None, x_shared=None):
@@ -807,7 +812,6 @@ def prefill_streamed(host_blobs: Sequence[torch.Tensor], slots: Sequence[torch.T
         # a copy on the compute stream would serialise the pipeline
         copy_stream = _copy_stream_for(x.device)
     _check(lib.moe_layer_prefill_streamed(ctypes.byref(args), cs, _stream(copy_stream)))
-    _keep_until_done(compute_stream, workspace)
-    if copy_stream != torch.cuda.current_stream(x.device):
-        workspace.record_stream(copy_stream)
+    _keep_until_done(compute_stream, workspace, logits, x, out, layer_inputs, *slots)
+    _keep_until_done(copy_stream, workspace, logits, *slots)
     return workspace

@@ -280,9 +280,10 @@ __device__ __forceinline__ void dense_tile(const DenseJob& p, int m0, int nt, ch
   // its own, which only that adapter's rows take up.  s enters in two or three
   // 16-bit parts (Parts), so that it is not rounded to one, and in fp16 times a
   // power of two of its row's own, which is taken out of the sums: any fp32
-  // value of s counts, as it does in the kernels of few tokens.  Two or four 16-deep steps are loaded together, and all rows where there are
-  // registers for it (256 accumulators leave none: they would have to leave the
-  // matrix cores' registers at once): the time is the loads' latency.
+  // value of s counts, as it does in the kernels of few tokens.  Two or four
+  // 16-deep steps are loaded together, and all rows where there are registers
+  // for it (256 accumulators leave none: they would have to leave the matrix
+  // cores' registers at once): the time is the loads' latency.
   if constexpr (LORA) {
     constexpr int HS = FM * FN == 4 ? 4 : 2, FB = FM * FN > 8 ? 1 : FM;   // steps, fragment rows together
     auto add_adapters = [&](auto F0) {

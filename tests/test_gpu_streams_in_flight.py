@@ -120,3 +120,28 @@ def test_layers_in_two_captured_graphs():
             assert torch.equal(layer.forward(lg, xx), out), k
         layer.forward(torch.cat([logits] * (k + 2)), torch.cat([x] * (k + 2)))
         torch.cuda.synchronize()
+
+
+def test_inputs_dropped_at_once():
+    """Inputs and weights made for one call on a side stream, dropped when it returns, while the current stream
+    allocates and fills memory of their sizes and the side stream is far behind."""
+    T, H, I = 3000, 2048, 1024
+    make = lambda: (du.normal((2 * I, H), H ** -0.5, BF, 1), du.normal((H, I), I ** -0.5, BF, 2),
+                    du.normal((T, H), 1.0, BF, 3), du.normal((T, H), 1.0, BF, 4))
+    w1, w2, x, add = make()
+    want = mx.GatedFFN(w1, w2).forward(x, add=add)
+    a = torch.randn(4096, 4096, device="cuda")
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        w1, w2, x, add = make()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            for _ in range(5):
+                a @ a
+        got = mx.GatedFFN(w1, w2).forward(x, add=add, stream=side)
+        sizes = [t.numel() for t in (w1, w2, x, add)]
+        del w1, w2, x, add
+        junk = [torch.full((n,), float("nan"), dtype=BF, device="cuda") for n in sizes]
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+        del junk

@@ -203,3 +203,63 @@ def test_a_layer_refuses_results_it_would_not_fill(world, bad, shared):
     assert not world.lib.calls
     layer.forward(logits, x, out=z(5, 32, dtype=torch.float32))
     assert world.lib.calls
+
+
+def _codes(*shape):
+    return z(*shape, dtype=torch.uint8)
+
+
+def _fp32(*shape):
+    return z(*shape, dtype=torch.float32)
+
+
+def _int32(*shape):
+    return z(*shape, dtype=torch.int32)
+
+
+# name -> (call of a stream and its inputs, the inputs)
+TAKES = {
+    "route": (lambda s, lg: mx.route(lg, 2, stream=s), lambda: [_fp32(5, 4)]),
+    "permute": (lambda s, ids: mx.permute(ids, 4, stream=s), lambda: [_int32(5, 2)]),
+    "grouped_gemm": (lambda s, a, w, ws, off, sc, ga: mx.grouped_gemm(a, w, ws, off, a_scales=sc, a_gather=ga, stream=s),
+                     lambda: [_codes(5, 32), _codes(4, 64, 16), _codes(4, 64, 1), _int32(5), _codes(5, 1), _int32(5)]),
+    "tile_weights": (lambda s, w, ws: mx.tile_weights(w, ws, stream=s), lambda: [_codes(4, 64, 16), _codes(4, 64, 1)]),
+    "untile_weights": (lambda s, w, ws: mx.untile_weights(w, ws, stream=s),
+                       lambda: [_codes(4, 64, 16), _codes(4, 64, 1)]),
+    "combine": (lambda s, y, d, w: mx.combine(y, d, w, stream=s), lambda: [z(10, 32), _int32(10), _fp32(5, 2)]),
+    "ffn": (lambda s, x, add: _ffn().forward(x, add=add, stream=s), lambda: [z(5, 32), z(5, 32)]),
+    "ffn backward": (lambda s, d, x, gu: _ffn().backward(d, x, gu, stream=s), lambda: [z(5, 32), z(5, 32), z(5, 64)]),
+    "adapters": (lambda s, x, ids, add: mx.AdapterLinear(z(16, 32), z(2, 8, 32), z(2, 16, 8)).forward(
+        x, ids, add=add, stream=s), lambda: [z(5, 32), _int32(5), z(5, 16)]),
+    "layer": (lambda s, lg, x, xs: _layer().forward(lg, x, xs, stream=s), lambda: [_fp32(5, 4), _codes(5, 32),
+                                                                                   _codes(5, 1)]),
+    "layer to x_next": (lambda s, lg, x, xn: _layer().forward(lg, x, x_next=xn, stream=s),
+                        lambda: [_fp32(5, 4), z(5, 32), z(5, 32)]),
+    "layer with a shared expert": (lambda s, lg, x, xs, sh: _layer(shared=_ffn()).forward(lg, x, xs, x_shared=sh, stream=s),
+                                   lambda: [_fp32(5, 4), _codes(5, 32), _codes(5, 1), z(5, 32)]),
+    "streamed prefill": (lambda s, slot, lg, x, out, li: mx.prefill_streamed(
+        [_codes(64)], [slot], lg, x, out, T=5, H=32, I=32, E=4, k=2, num_layers=1, depth=1, layer_inputs=li,
+        compute_stream=s, copy_stream=Stream("copy")),
+        lambda: [_codes(64), _fp32(1, 5, 4), z(5, 32), _fp32(5, 32), z(1, 5, 32)]),
+}
+
+
+@pytest.mark.parametrize("name", ["ffn", "ffn backward", "adapters", "layer", "layer with a shared expert"])
+def test_weights_live_as_long_as_the_streams_work(world, name, monkeypatch):
+    """So may the weights, with the object that holds them."""
+    made = []
+    monkeypatch.setitem(globals(), "z", lambda *a, _z=z, **k: made.append(_z(*a, **k)) or made[-1])
+    call, make = TAKES[name]
+    call(world.side, *make())
+    assert len(made) >= 4 and all("side" in world.kept.get(id(t), ()) for t in made)
+
+
+@pytest.mark.parametrize("name", TAKES)
+def test_inputs_live_as_long_as_the_streams_work(world, name):
+    """A caller may drop its inputs at once: the allocator keeps their memory until the stream is done with them."""
+    call, make = TAKES[name]
+    inputs = make()
+    call(world.side, *inputs)
+    assert all("side" in world.kept.get(id(t), ()) for t in inputs)
+    if name == "streamed prefill":   # the slots are filled, the logits read on the copy stream
+        assert all("copy" in world.kept.get(id(t), ()) for t in inputs[:2])
