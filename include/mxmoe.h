@@ -542,6 +542,108 @@ typedef struct moe_adapter_args {
 size_t     moe_adapter_workspace_size(int32_t T, int32_t K, int32_t N, int32_t num_adapters, int32_t R);
 moe_status moe_adapter_linear(const moe_adapter_args* args, void* stream);
 
+/* ------------------------------------- the norm before a layer, with MXFP8 -- */
+
+/* Root-mean-square norm with the residual's addition:
+ *   r   = x (+ residual, rounded to residual_dtype and written to residual_out)
+ *   out = r / sqrt(mean(r^2) + eps) * weight             over a row of H
+ * The norm is taken of r as it is kept, so that the backward pass and a later
+ * addition see the number that was normed.  out is written in out_dtype, or as
+ * MXFP8 (codes and scales: what the layer and the grouped GEMM take), or both;
+ * each is rounded once, from the fp32 value.  An MXFP8 block's scale is the
+ * smallest power of two that brings its 32 values to 448 or below, so none
+ * saturates; codes are rounded to nearest even; a block that holds an infinity
+ * or NaN has scale byte 255 and NaN codes.  Squares are summed in fp32: rows
+ * whose sum of squares passes 3.4e38 come out as zeros.
+ *
+ * Sizes: 0 <= T < 2^22 (T == 0 enqueues nothing), H a multiple of 8 in
+ * [8, 32768], of 32 with codes.  Row strides are in elements, multiples of 8, at
+ * least H and at most 2^21; every pointer is 16-byte aligned, `scales` 1-byte;
+ * weight, codes and scales are contiguous.  eps is finite and not negative.
+ * residual_out may be `residual` or x itself, out may be x itself (same pointer,
+ * type and stride); apart from that no output may overlap an input or another
+ * output. */
+typedef struct moe_norm_args {
+  int32_t     T, H;
+  int32_t     dtype;             /* the 16-bit type: MOE_FLOAT_BF16 or MOE_FLOAT_FP16 */
+  int32_t     x_dtype;           /* each of these `dtype` or MOE_FLOAT_FP32 */
+  int32_t     residual_dtype;    /* residual and residual_out */
+  int32_t     weight_dtype;
+  int32_t     out_dtype;
+  float       eps;
+  const void* x;                 /* device [T][H] */
+  const void* residual;          /* device [T][H] or NULL */
+  const void* weight;            /* device [H] */
+  void*       residual_out;      /* device out [T][H], with residual (NULL without) */
+  void*       out;               /* device out [T][H] or NULL */
+  uint8_t*    codes;             /* device out E4M3 [T][H] or NULL */
+  uint8_t*    scales;            /* device out E8M0 [T][H/32], with codes */
+  int64_t     x_stride, residual_stride, residual_out_stride, out_stride;
+} moe_norm_args;
+
+moe_status moe_rms_norm_forward(const moe_norm_args* args, void* stream);
+
+/* The norm's gradients, with x the values that were normed (forward's r):
+ *   u = x / sqrt(mean(x^2) + eps);  g = dout * weight
+ *   dx = (g - u * mean(g * u)) / sqrt(mean(x^2) + eps) (+ dresidual)
+ *   dweight = sum over the rows of dout * u
+ * dx is the gradient of forward's x and of its residual alike; dresidual is what
+ * reaches residual_out from elsewhere.  For MXFP8 outputs dout is the gradient
+ * of the values that the codes stand for (their rounding counts as the
+ * identity).  Either of dx and dweight may be NULL.  With accumulate dweight
+ * holds an earlier gradient and is added to, in fp32, before its rounding.
+ * T == 0 writes zeros to dweight (leaves it with accumulate).  Deterministic: no
+ * atomics.  dx may be dout or dresidual itself (same pointer, type and stride).
+ * Sizes, strides and alignment as above. */
+typedef struct moe_norm_grad_args {
+  int32_t     T, H;
+  int32_t     dtype;             /* the 16-bit type */
+  int32_t     dout_dtype;        /* each of these `dtype` or MOE_FLOAT_FP32 */
+  int32_t     x_dtype;
+  int32_t     weight_dtype;
+  int32_t     dresidual_dtype;
+  int32_t     dx_dtype;
+  int32_t     dw_dtype;
+  int32_t     accumulate;        /* 0 or 1 */
+  float       eps;
+  const void* dout;              /* device [T][H] */
+  const void* x;                 /* device [T][H] */
+  const void* weight;            /* device [H] */
+  const void* dresidual;         /* device [T][H] or NULL */
+  void*       dx;                /* device out [T][H] or NULL */
+  void*       dweight;           /* device out [H] or NULL */
+  int64_t     dout_stride, x_stride, dresidual_stride, dx_stride;
+  void*       workspace;         /* device, >= moe_rms_norm_grad_workspace_size() */
+  size_t      workspace_bytes;
+} moe_norm_grad_args;
+
+/* (0 for sizes outside the limits above) */
+size_t     moe_rms_norm_grad_workspace_size(int32_t T, int32_t H);
+moe_status moe_rms_norm_backward(const moe_norm_grad_args* args, void* stream);
+
+/* ------------------------------------ gradients of the combine and the router -- */
+
+/* The combine's gradients (out[t] = sum_j topk_w[t][j] * y[dest_row[t*k + j]]):
+ *   dy[dest_row[t*k + j]] = topk_w[t][j] * dout[t]
+ *   dtopk_w[t][j]         = sum_h y[dest_row[t*k + j]][h] * dout[t][h]
+ * dout is fp32, as the combine's out; dy is rounded once, dtopk_w is fp32.  Either
+ * may be NULL; y is read for dtopk_w only.  A dest_row outside [0, T*k) has no
+ * row: nothing is written for it and its dtopk_w is 0.  Rows of dy that no
+ * dest_row names are left as they were.  0 <= T < 2^22, 1 <= k <= 64, H a multiple
+ * of 8 in [8, 262144]; y, dout and dy contiguous and 16-byte aligned;
+ * no output may overlap an input or the other output. */
+moe_status moe_combine_backward(const float* dout, const void* y, int32_t y_dtype /* moe_float_dtype */,
+                                const int32_t* dest_row, const float* topk_w, int32_t T, int32_t k, int32_t H,
+                                void* dy, int32_t dy_dtype /* moe_float_dtype */, float* dtopk_w, void* stream);
+
+/* The routing's gradient: topk_w is the softmax over a token's k kept logits, so
+ *   dlogits[t][topk_ids[t][j]] = w_j * (dtopk_w_j - sum_i w_i * dtopk_w_i)
+ * and 0 for the experts that were not kept.  An id outside [0, E) has no logit;
+ * an id that a token lists twice gets the sum.  0 <= T < 2^26, E and k as for
+ * moe_route. */
+moe_status moe_route_backward(const float* dtopk_w, const int32_t* topk_ids, const float* topk_w, int32_t T,
+                              int32_t E, int32_t k, float* dlogits, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

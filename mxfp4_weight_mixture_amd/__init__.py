@@ -12,7 +12,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
-from typing import Optional, Sequence
+from typing import NamedTuple, Optional, Sequence
 
 import torch
 
@@ -97,6 +97,21 @@ class AdapterArgs(ctypes.Structure):
                 ("workspace_bytes", _sz)]
 
 
+class NormArgs(ctypes.Structure):
+    _fields_ = [("T", _i32), ("H", _i32), ("dtype", _i32), ("x_dtype", _i32), ("residual_dtype", _i32),
+                ("weight_dtype", _i32), ("out_dtype", _i32), ("eps", ctypes.c_float), ("x", _vp), ("residual", _vp),
+                ("weight", _vp), ("residual_out", _vp), ("out", _vp), ("codes", _vp), ("scales", _vp),
+                ("x_stride", _i64), ("residual_stride", _i64), ("residual_out_stride", _i64), ("out_stride", _i64)]
+
+
+class NormGradArgs(ctypes.Structure):
+    _fields_ = [("T", _i32), ("H", _i32), ("dtype", _i32), ("dout_dtype", _i32), ("x_dtype", _i32),
+                ("weight_dtype", _i32), ("dresidual_dtype", _i32), ("dx_dtype", _i32), ("dw_dtype", _i32),
+                ("accumulate", _i32), ("eps", ctypes.c_float), ("dout", _vp), ("x", _vp), ("weight", _vp),
+                ("dresidual", _vp), ("dx", _vp), ("dweight", _vp), ("dout_stride", _i64), ("x_stride", _i64),
+                ("dresidual_stride", _i64), ("dx_stride", _i64), ("workspace", _vp), ("workspace_bytes", _sz)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is not built; run `python -m mxfp4_weight_mixture_amd.build`")
@@ -134,6 +149,11 @@ def _load():
         "moe_gated_ffn_backward": (ctypes.c_int, [ctypes.POINTER(FfnGradArgs), _vp]),
         "moe_adapter_workspace_size": (_sz, [_i32, _i32, _i32, _i32, _i32]),
         "moe_adapter_linear": (ctypes.c_int, [ctypes.POINTER(AdapterArgs), _vp]),
+        "moe_rms_norm_forward": (ctypes.c_int, [ctypes.POINTER(NormArgs), _vp]),
+        "moe_rms_norm_grad_workspace_size": (_sz, [_i32, _i32]),
+        "moe_rms_norm_backward": (ctypes.c_int, [ctypes.POINTER(NormGradArgs), _vp]),
+        "moe_combine_backward": (ctypes.c_int, [_vp, _vp, _i32, _vp, _vp, _i32, _i32, _i32, _vp, _i32, _vp, _vp]),
+        "moe_route_backward": (ctypes.c_int, [_vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp]),
     }
     for name, (res, args) in sigs.items():
         fn = getattr(lib, name)
@@ -328,6 +348,61 @@ def combine(y: torch.Tensor, dest_row: torch.Tensor, topk_w: torch.Tensor, *, rm
                            _stream(stream)))
     _keep_until_done(stream, out, xn, y, dest_row, topk_w)
     return (out, xn) if rms_next else out
+
+
+def combine_backward(dout: torch.Tensor, y: Optional[torch.Tensor], dest_row: torch.Tensor, topk_w: torch.Tensor, *,
+                     dy=True, dy_dtype: Optional[torch.dtype] = None, dw: bool = True, stream=None):
+    """moe_combine_backward: dout fp32 [T][H], y [T*k][H] (as the combine took it, or fp16) ->
+    (dy [T*k][H], dtopk_w fp32 [T][k]).
+
+    dy: True allocates it in dy_dtype (default y's type), a tensor receives it, False or None skips it.  dw:
+    False skips dtopk_w, y may then be None.
+    """
+    T, k = topk_w.shape
+    dev = topk_w.device
+    _on_current_device(dev, stream)
+    any_float = tuple(FLOAT_DTYPE)
+    _flat("topk_w", topk_w, (T, k), (torch.float32,), dev)
+    if dout.dim() != 2:
+        raise ValueError(f"dout has shape {tuple(dout.shape)}, not ({T}, H)")
+    H = dout.shape[1]
+    _flat("dout", dout, (T, H), (torch.float32,), dev)
+    if dest_row.dim() == 2:
+        dest_row = dest_row.reshape(-1)
+    _flat("dest_row", dest_row, (T * k,), (torch.int32,), dev)
+    if dw or y is not None:
+        if y is None:
+            raise ValueError("dtopk_w needs y")
+        _flat("y", y, (T * k, H), any_float, dev)
+    with _allocate_on(stream):
+        if dy is True:
+            dy = torch.empty((T * k, H), dtype=dy_dtype or (y.dtype if y is not None else torch.float32), device=dev)
+        elif dy is False:
+            dy = None
+        dtopk_w = torch.empty((T, k), dtype=torch.float32, device=dev) if dw else None
+    if dy is not None:
+        _flat("dy", dy, (T * k, H), any_float if dy_dtype is None else (dy_dtype,), dev)
+    _check(lib.moe_combine_backward(_ptr(dout), _ptr(y), 0 if y is None else FLOAT_DTYPE[y.dtype], _ptr(dest_row),
+                                    _ptr(topk_w), T, k, H, _ptr(dy), 0 if dy is None else FLOAT_DTYPE.get(dy.dtype, -1),
+                                    _ptr(dtopk_w), _stream(stream)))
+    _keep_until_done(stream, dy, dtopk_w, dout, y, dest_row, topk_w)
+    return dy, dtopk_w
+
+
+def route_backward(dtopk_w: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tensor, E: int, stream=None):
+    """moe_route_backward: the gradient of the k kept weights, fp32 [T][k] -> dlogits fp32 [T][E]."""
+    T, k = topk_w.shape
+    dev = topk_w.device
+    _on_current_device(dev, stream)
+    _flat("topk_w", topk_w, (T, k), (torch.float32,), dev)
+    _flat("dtopk_w", dtopk_w, (T, k), (torch.float32,), dev)
+    _flat("topk_ids", topk_ids, (T, k), (torch.int32,), dev)
+    with _allocate_on(stream):
+        dlogits = torch.empty((T, max(E, 0)), dtype=torch.float32, device=dev)
+    _check(lib.moe_route_backward(_ptr(dtopk_w), _ptr(topk_ids), _ptr(topk_w), T, E, k, _ptr(dlogits),
+                                  _stream(stream)))
+    _keep_until_done(stream, dlogits, dtopk_w, topk_ids, topk_w)
+    return dlogits
 
 
 # --------------------------------------------- dense 16-bit projections
@@ -577,6 +652,129 @@ class AdapterLinear:
         _check(lib.moe_adapter_linear(ctypes.byref(a), _stream(stream)))
         _keep_until_done(stream, out, x, ids, add, self.w, self.lora_a, self.lora_b, self.scales, self.ranks)
         return out
+
+
+class NormOutput(NamedTuple):
+    """What RMSNorm.forward gives; None for what was not asked for."""
+    out: Optional[torch.Tensor]        # [T][H], 16 bits or fp32
+    residual: Optional[torch.Tensor]   # x + residual as it is kept: what was normed
+    codes: Optional[torch.Tensor]      # E4M3 codes uint8 [T][H]
+    scales: Optional[torch.Tensor]     # E8M0 scales uint8 [T][H/32]
+
+
+class RMSNorm:
+    """The root-mean-square norm before a layer, with the residual's addition and MXFP8 outputs.
+
+    r = x (+ residual), out = r / sqrt(mean(r^2) + eps) * weight over rows of H.  weight [H] in bf16, fp16 or fp32.
+    x, residual and the outputs are of one 16-bit type (the weight's, or else x's, or bf16) or fp32, each on its
+    own: x may be a layer's fp32 sum beside a bf16 residual.  No buffers are held and nothing is recorded by
+    autograd (see GatedFFN).
+    """
+
+    def __init__(self, weight: torch.Tensor, eps: float = 1e-6):
+        if weight.dim() != 1 or weight.dtype not in FLOAT_DTYPE:
+            raise ValueError(f"weight is {weight.dtype} {tuple(weight.shape)}, not [H] of {list(FLOAT_DTYPE)}")
+        if not weight.is_cuda or not weight.is_contiguous():
+            raise ValueError("weight must be a contiguous device tensor")
+        self.weight, self.eps = weight, float(eps)
+        self.H, self.device = weight.shape[0], weight.device
+
+    def _type16(self, *tensors):
+        """The 16-bit type of a call; every tensor is of it or fp32."""
+        for t in (self.weight, *tensors):
+            if t is not None and t.dtype in (torch.bfloat16, torch.float16):
+                return t.dtype
+        return torch.bfloat16
+
+    def forward(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None, *, out=True,
+                out_dtype: Optional[torch.dtype] = None, residual_out: Optional[torch.Tensor] = None,
+                mxfp8: bool = False, stream=None) -> NormOutput:
+        """moe_rms_norm_forward: x [T][H], residual [T][H] -> NormOutput.
+
+        residual_out receives the sum, in the residual's type; it may be `residual` itself.  out: True allocates
+        it in out_dtype (default the 16-bit type), a tensor receives it (x itself is allowed), False skips it.
+        mxfp8 adds codes and scales, as Layer.forward and grouped_gemm take them.
+        """
+        _on_current_device(self.device, stream)
+        d16 = self._type16(x, residual)
+        types = (d16, torch.float32)
+        a = NormArgs(H=self.H, dtype=FLOAT_DTYPE[d16], eps=self.eps, weight=self.weight.data_ptr(),
+                     weight_dtype=FLOAT_DTYPE[self.weight.dtype])
+        a.x_stride = _rows("x", x, None, self.H, types, self.device)
+        T = a.T = x.shape[0]
+        a.x, a.x_dtype = x.data_ptr(), FLOAT_DTYPE[x.dtype]
+        if residual is not None:
+            a.residual_stride = _rows("residual", residual, T, self.H, types, self.device)
+            if residual_out is None:
+                with _allocate_on(stream):
+                    residual_out = torch.empty((T, self.H), dtype=residual.dtype, device=self.device)
+            a.residual_out_stride = _rows("residual_out", residual_out, T, self.H, (residual.dtype,), self.device)
+            a.residual, a.residual_out = residual.data_ptr(), residual_out.data_ptr()
+            a.residual_dtype = FLOAT_DTYPE[residual.dtype]
+        elif residual_out is not None:
+            raise ValueError("residual_out without a residual")
+        codes = scales = None
+        with _allocate_on(stream):
+            if out is True:
+                out = torch.empty((T, self.H), dtype=out_dtype or d16, device=self.device)
+            elif out is False:
+                out = None
+            if mxfp8:
+                codes = torch.empty((T, self.H), dtype=torch.uint8, device=self.device)
+                scales = torch.empty((T, self.H // 32), dtype=torch.uint8, device=self.device)
+                a.codes, a.scales = codes.data_ptr(), scales.data_ptr()
+        if out is not None:
+            a.out_stride = _rows("out", out, T, self.H, types if out_dtype is None else (out_dtype,), self.device)
+            a.out, a.out_dtype = out.data_ptr(), FLOAT_DTYPE.get(out.dtype, -1)
+        elif not mxfp8:
+            raise ValueError("no output: neither out nor mxfp8")
+        _check(lib.moe_rms_norm_forward(ctypes.byref(a), _stream(stream)))
+        _keep_until_done(stream, out, residual_out, codes, scales, x, residual, self.weight)
+        return NormOutput(out, residual_out, codes, scales)
+
+    def backward(self, dout: torch.Tensor, x: torch.Tensor, *, dresidual: Optional[torch.Tensor] = None, dx=True,
+                 dweight=True, dw_dtype: Optional[torch.dtype] = None, accumulate: bool = False, stream=None):
+        """moe_rms_norm_backward: (dx, dweight) from dout [T][H] and the values x that were normed (forward's x, or
+        its NormOutput.residual).
+
+        dx is the gradient of forward's x and residual alike; dresidual, the gradient that reaches the kept sum
+        from elsewhere, is added to it.  dx and dweight: True allocates (dx in the 16-bit type, dweight in
+        dw_dtype, default the weight's type), a tensor receives, False or None skips.  dx may be dout or
+        dresidual itself.  accumulate: the given dweight is added to.
+        """
+        _on_current_device(self.device, stream)
+        d16 = self._type16(x, dout, dresidual)
+        types = (d16, torch.float32)
+        a = NormGradArgs(H=self.H, dtype=FLOAT_DTYPE[d16], eps=self.eps, weight=self.weight.data_ptr(),
+                         weight_dtype=FLOAT_DTYPE[self.weight.dtype], accumulate=int(accumulate))
+        a.dout_stride = _rows("dout", dout, None, self.H, types, self.device)
+        T = a.T = dout.shape[0]
+        a.x_stride = _rows("x", x, T, self.H, types, self.device)
+        a.dout, a.dout_dtype, a.x, a.x_dtype = (dout.data_ptr(), FLOAT_DTYPE[dout.dtype], x.data_ptr(),
+                                                FLOAT_DTYPE[x.dtype])
+        if dresidual is not None:
+            a.dresidual_stride = _rows("dresidual", dresidual, T, self.H, types, self.device)
+            a.dresidual, a.dresidual_dtype = dresidual.data_ptr(), FLOAT_DTYPE[dresidual.dtype]
+        if accumulate and not isinstance(dweight, torch.Tensor):
+            raise ValueError("accumulate needs the tensor to add to")
+        n = lib.moe_rms_norm_grad_workspace_size(T, self.H)
+        with _allocate_on(stream):
+            if dx is True:
+                dx = torch.empty((T, self.H), dtype=d16, device=self.device)
+            if dweight is True:
+                dweight = torch.empty(self.H, dtype=dw_dtype or self.weight.dtype, device=self.device)
+            ws = _u8(n, self.device)
+        dx, dweight = (None if t is False else t for t in (dx, dweight))
+        if dx is not None:
+            a.dx_stride = _rows("dx", dx, T, self.H, types, self.device)
+            a.dx, a.dx_dtype = dx.data_ptr(), FLOAT_DTYPE[dx.dtype]
+        if dweight is not None:
+            _flat("dweight", dweight, (self.H,), types if dw_dtype is None else (dw_dtype,), self.device)
+            a.dweight, a.dw_dtype = dweight.data_ptr(), FLOAT_DTYPE.get(dweight.dtype, -1)
+        a.workspace, a.workspace_bytes = ws.data_ptr(), n
+        _check(lib.moe_rms_norm_backward(ctypes.byref(a), _stream(stream)))
+        _keep_until_done(stream, dx, dweight, dout, x, dresidual, self.weight)
+        return dx, dweight
 
 
 class Layer:
