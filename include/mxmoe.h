@@ -644,6 +644,87 @@ moe_status moe_combine_backward(const float* dout, const void* y, int32_t y_dtyp
 moe_status moe_route_backward(const float* dtopk_w, const int32_t* topk_ids, const float* topk_w, int32_t T,
                               int32_t E, int32_t k, float* dlogits, void* stream);
 
+/* -------------------------------- routed experts with 16-bit weights -- */
+
+/* The gated feed-forward block of moe_gated_ffn_forward, one set of weights for
+ * each expert: row r with expert_offsets[e] <= r < expert_offsets[e + 1] gets
+ *   gate_up[r] = x_r * w1[e]^T;  h = act(gate) * up;  out[r] = h * w2[e]^T
+ * where x_r is row r of x, or with `gather` row gather[r] / gather_div of it
+ * (moe_permute's perm_src and k, as in the MXFP4 grouped GEMM); a gathered row
+ * outside [0, tokens) counts as zeros.  Experts may have any number of rows, none
+ * included; rows outside [expert_offsets[0], expert_offsets[E]) are not read and
+ * their outputs are left as they were (a part of the experts that one device
+ * holds; a padded batch).  Offsets ascend; what exceeds [0, rows] is cut.
+ * Accumulation and roundings as in moe_gated_ffn_forward.
+ *
+ * Sizes: 0 <= rows <= 2^28 (0 enqueues nothing), 1 <= E <= 8192, H and I multiples
+ * of 8 in [8, 262144], fewer than 2^24 tiles of 64 x 64 in `rows` + 64 * min(E, rows)
+ * rows of max(H, 2I); with gather, tokens * x_stride < 2^30.  Strides, alignment and
+ * overlap as for moe_gated_ffn_forward; w1, w2, gate_up are contiguous. */
+typedef struct moe_expert_ffn_args {
+  int32_t        rows, H, I, E;
+  int32_t        layout;         /* MOE_EPI_SWIGLU_SPLIT or _INTERLEAVED: w1's row order */
+  int32_t        gate_act;       /* moe_gate_act */
+  int32_t        dtype;          /* x, w1, w2: MOE_FLOAT_BF16 or MOE_FLOAT_FP16 */
+  int32_t        out_dtype;      /* `dtype` or MOE_FLOAT_FP32 */
+  int32_t        save_dtype;     /* gate_up: `dtype` or MOE_FLOAT_FP32 */
+  int32_t        tokens;         /* rows of x, with gather */
+  int32_t        gather_div;     /* >= 1 with gather, 0 without */
+  const void*    x;              /* device [rows][H], with gather [tokens][H] */
+  const int32_t* gather;         /* device [rows] or NULL */
+  const int32_t* expert_offsets; /* device [E + 1] */
+  const void*    w1;             /* device [E][2I][H] */
+  const void*    w2;             /* device [E][H][I] */
+  void*          out;            /* device out [rows][H] */
+  void*          gate_up;        /* device out [rows][2I], kept for the backward pass, or NULL */
+  int64_t        x_stride, out_stride;
+  void*          workspace;      /* device, >= moe_expert_ffn_workspace_size() */
+  size_t         workspace_bytes;
+} moe_expert_ffn_args;
+
+/* (0 for sizes outside the limits above, as for the query below) */
+size_t     moe_expert_ffn_workspace_size(int32_t rows, int32_t H, int32_t I, int32_t E);
+moe_status moe_expert_ffn_forward(const moe_expert_ffn_args* args, void* stream);
+
+/* The experts' gradients from dout and the gate_up that forward kept, row by row
+ * as moe_gated_ffn_backward, dw1[e] and dw2[e] summed over expert e's rows (zeros,
+ * or with accumulate left as they are, where it has none).
+ * dx without gather: [rows][H], rows outside the experts' left as they were.
+ * With gather dx is [tokens][H], each token's gradient summed over its rows:
+ *   dx[t] = sum_{j < gather_div} dx_row[dest_row[t * gather_div + j]]
+ * with moe_permute's dest_row; a dest_row outside the experts' rows counts as
+ * none.  The rows' gradients are held in fp32 until they are summed.
+ * Any of dx, dw1, dw2 may be NULL.  Deterministic: no atomics. */
+typedef struct moe_expert_ffn_grad_args {
+  int32_t        rows, H, I, E;
+  int32_t        layout, gate_act;
+  int32_t        dtype;          /* dout, x, w1, w2 */
+  int32_t        save_dtype;     /* gate_up: `dtype` or MOE_FLOAT_FP32 */
+  int32_t        dx_dtype;       /* `dtype` or MOE_FLOAT_FP32 */
+  int32_t        dw_dtype;       /* dw1 and dw2: `dtype` or MOE_FLOAT_FP32 */
+  int32_t        accumulate;     /* 0 or 1: dw1 and dw2 are added to */
+  int32_t        tokens;         /* rows of x and dx, with gather */
+  int32_t        gather_div;     /* >= 1 with gather, 0 without */
+  const void*    dout;           /* device [rows][H] */
+  const void*    x;              /* device [rows][H], with gather [tokens][H] (read for dw1 only) */
+  const int32_t* gather;         /* device [rows] or NULL */
+  const int32_t* dest_row;       /* device [tokens * gather_div], for dx with gather */
+  const int32_t* expert_offsets; /* device [E + 1] */
+  const void*    w1;             /* device [E][2I][H] (read for dx only) */
+  const void*    w2;             /* device [E][H][I] */
+  const void*    gate_up;        /* device [rows][2I] */
+  void*          dx;             /* device out or NULL */
+  void*          dw1;            /* device out [E][2I][H] or NULL */
+  void*          dw2;            /* device out [E][H][I] or NULL */
+  int64_t        dout_stride, x_stride, dx_stride;
+  void*          workspace;      /* device, >= moe_expert_ffn_grad_workspace_size() */
+  size_t         workspace_bytes;
+} moe_expert_ffn_grad_args;
+
+/* gathered: 1 for calls with gather, else 0 */
+size_t     moe_expert_ffn_grad_workspace_size(int32_t rows, int32_t H, int32_t I, int32_t E, int32_t gathered);
+moe_status moe_expert_ffn_backward(const moe_expert_ffn_grad_args* args, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

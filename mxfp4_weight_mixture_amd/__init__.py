@@ -112,6 +112,23 @@ class NormGradArgs(ctypes.Structure):
                 ("dresidual_stride", _i64), ("dx_stride", _i64), ("workspace", _vp), ("workspace_bytes", _sz)]
 
 
+class ExpertFfnArgs(ctypes.Structure):
+    _fields_ = [("rows", _i32), ("H", _i32), ("I", _i32), ("E", _i32), ("layout", _i32), ("gate_act", _i32),
+                ("dtype", _i32), ("out_dtype", _i32), ("save_dtype", _i32), ("tokens", _i32), ("gather_div", _i32),
+                ("x", _vp), ("gather", _vp), ("expert_offsets", _vp), ("w1", _vp), ("w2", _vp), ("out", _vp),
+                ("gate_up", _vp), ("x_stride", _i64), ("out_stride", _i64), ("workspace", _vp),
+                ("workspace_bytes", _sz)]
+
+
+class ExpertFfnGradArgs(ctypes.Structure):
+    _fields_ = [("rows", _i32), ("H", _i32), ("I", _i32), ("E", _i32), ("layout", _i32), ("gate_act", _i32),
+                ("dtype", _i32), ("save_dtype", _i32), ("dx_dtype", _i32), ("dw_dtype", _i32), ("accumulate", _i32),
+                ("tokens", _i32), ("gather_div", _i32), ("dout", _vp), ("x", _vp), ("gather", _vp), ("dest_row", _vp),
+                ("expert_offsets", _vp), ("w1", _vp), ("w2", _vp), ("gate_up", _vp), ("dx", _vp), ("dw1", _vp),
+                ("dw2", _vp), ("dout_stride", _i64), ("x_stride", _i64), ("dx_stride", _i64), ("workspace", _vp),
+                ("workspace_bytes", _sz)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is not built; run `python -m mxfp4_weight_mixture_amd.build`")
@@ -153,6 +170,10 @@ def _load():
         "moe_rms_norm_grad_workspace_size": (_sz, [_i32, _i32]),
         "moe_rms_norm_backward": (ctypes.c_int, [ctypes.POINTER(NormGradArgs), _vp]),
         "moe_combine_backward": (ctypes.c_int, [_vp, _vp, _i32, _vp, _vp, _i32, _i32, _i32, _vp, _i32, _vp, _vp]),
+        "moe_expert_ffn_workspace_size": (_sz, [_i32, _i32, _i32, _i32]),
+        "moe_expert_ffn_forward": (ctypes.c_int, [ctypes.POINTER(ExpertFfnArgs), _vp]),
+        "moe_expert_ffn_grad_workspace_size": (_sz, [_i32, _i32, _i32, _i32, _i32]),
+        "moe_expert_ffn_backward": (ctypes.c_int, [ctypes.POINTER(ExpertFfnGradArgs), _vp]),
         "moe_route_backward": (ctypes.c_int, [_vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp]),
     }
     for name, (res, args) in sigs.items():
@@ -652,6 +673,136 @@ class AdapterLinear:
         _check(lib.moe_adapter_linear(ctypes.byref(a), _stream(stream)))
         _keep_until_done(stream, out, x, ids, add, self.w, self.lora_a, self.lora_b, self.scales, self.ranks)
         return out
+
+
+class ExpertFFN:
+    """The routed experts with 16-bit weights: GatedFFN with one set of weights for each expert.
+
+    Rows come in expert order, row r with expert_offsets[e] <= r < expert_offsets[e + 1] belongs to expert e:
+    out[r] = (act(x Wg[e]^T) * (x Wu[e]^T)) W2[e]^T with x row r of x, or with gather row gather[r] // gather_div
+    of it.  permute's results are what the calls take: expert_offsets, gather=perm_src with gather_div=k, and
+    dest_row.  w1 [E][2I][H], w2 [E][H][I]; layouts, activations, types and rounding as in GatedFFN, which also
+    says what the object holds and what autograd sees.  Rows of no expert (before the first offset or behind the
+    last) are neither read nor written.
+    """
+
+    def __init__(self, w1: torch.Tensor, w2: torch.Tensor, layout: str = "split", act: str = "silu"):
+        _weight("w1", w1)
+        _weight("w2", w2)
+        if w1.dim() != 3 or w2.dim() != 3 or w1.shape != (w2.shape[0], 2 * w2.shape[2], w2.shape[1]):
+            raise ValueError(f"w1 {tuple(w1.shape)} and w2 {tuple(w2.shape)} are not [E][2I][H] and [E][H][I]")
+        if w1.dtype != w2.dtype or w1.device != w2.device:
+            raise ValueError("w1 and w2 differ in type or device")
+        if layout not in LAYOUT or act not in GATE_ACT:
+            raise ValueError(f"layout {layout!r} / act {act!r}: not {list(LAYOUT)} / {list(GATE_ACT)}")
+        self.w1, self.w2, self.layout, self.act = w1, w2, layout, act
+        self.E, self.H, self.I = w2.shape
+        self.dtype, self.device = w1.dtype, w1.device
+        self._dtypes = (self.dtype, torch.float32)
+        same = dict(H=self.H, I=self.I, E=self.E, layout=LAYOUT[layout], gate_act=GATE_ACT[act],
+                    dtype=FLOAT_DTYPE[self.dtype], w1=w1.data_ptr(), w2=w2.data_ptr())
+        self._fwd, self._bwd = ExpertFfnArgs(**same), ExpertFfnGradArgs(**same)
+
+    def _take_rows(self, a, x, expert_offsets, gather, gather_div):
+        """x, its gather and the offsets into the arguments `a`; returns the number of rows."""
+        _flat("expert_offsets", expert_offsets, (self.E + 1,), (torch.int32,), self.device)
+        a.x_stride = _rows("x", x, None, self.H, (self.dtype,), self.device)
+        rows = x.shape[0]
+        if gather is not None:
+            rows = gather.numel()
+            _flat("gather", gather, (rows,), (torch.int32,), self.device)
+            a.gather, a.gather_div, a.tokens = gather.data_ptr(), gather_div, x.shape[0]
+        elif gather_div != 1:
+            raise ValueError("gather_div without gather")
+        a.rows, a.x, a.expert_offsets = rows, x.data_ptr(), expert_offsets.data_ptr()
+        return rows
+
+    def forward(self, x: torch.Tensor, expert_offsets: torch.Tensor, *, gather: Optional[torch.Tensor] = None,
+                gather_div: int = 1, out: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None,
+                save=False, stream=None):
+        """moe_expert_ffn_forward: x [rows][H], or [T][H] with gather int32 [rows] -> out [rows][H], or (out,
+        gate_up) with save.
+
+        out_dtype: the weights' type (default) or torch.float32 (what combine takes beside bf16).  save: keep the
+        pre-activations gate_up [rows][2I] for backward(), True in fp32, "half" in the weights' type.
+        """
+        _on_current_device(self.device, stream)
+        a = ExpertFfnArgs.from_buffer_copy(self._fwd)
+        rows = self._take_rows(a, x, expert_offsets, gather, gather_div)
+        if out is None:
+            with _allocate_on(stream):
+                out = torch.empty((rows, self.H), device=self.device, dtype=out_dtype or self.dtype)
+        a.out_stride = _rows("out", out, rows, self.H, self._dtypes, self.device)
+        if out_dtype is not None and out.dtype != out_dtype:
+            raise ValueError(f"out is {out.dtype}, out_dtype {out_dtype}")
+        a.out, a.out_dtype = out.data_ptr(), FLOAT_DTYPE[out.dtype]
+        gate_up = None
+        if save not in (False, True, "half"):
+            raise ValueError(f"save is {save!r}, not False, True or 'half'")
+        a.save_dtype = a.dtype
+        n = lib.moe_expert_ffn_workspace_size(rows, self.H, self.I, self.E)
+        with _allocate_on(stream):
+            if save:
+                gate_up = torch.empty((rows, 2 * self.I), device=self.device,
+                                      dtype=self.dtype if save == "half" else torch.float32)
+                a.save_dtype, a.gate_up = FLOAT_DTYPE[gate_up.dtype], gate_up.data_ptr()
+            ws = _u8(n, self.device)
+        a.workspace, a.workspace_bytes = ws.data_ptr(), n
+        _check(lib.moe_expert_ffn_forward(ctypes.byref(a), _stream(stream)))
+        _keep_until_done(stream, out, gate_up, x, expert_offsets, gather, self.w1, self.w2)
+        return (out, gate_up) if save else out
+
+    def backward(self, dout: torch.Tensor, x: torch.Tensor, expert_offsets: torch.Tensor, gate_up: torch.Tensor, *,
+                 gather: Optional[torch.Tensor] = None, gather_div: int = 1, dest_row: Optional[torch.Tensor] = None,
+                 dx=True, dw1=True, dw2=True, dw_dtype: Optional[torch.dtype] = None, accumulate: bool = False,
+                 stream=None):
+        """moe_expert_ffn_backward: (dx, dw1, dw2) from dout [rows][H], x and forward's gate_up.
+
+        Without gather dx is [rows][H]; with gather it is [T][H], every token's gradient summed over its rows, and
+        dest_row int32 [T * gather_div] is needed.  dx, dw1, dw2: True allocates the gradient, a tensor receives
+        it, False or None skips it.  dw_dtype: type of the weight gradients made here, the weights' (default) or
+        torch.float32.  accumulate: the given dw1 and dw2 are added to.
+        """
+        _on_current_device(self.device, stream)
+        a = ExpertFfnGradArgs.from_buffer_copy(self._bwd)
+        rows = self._take_rows(a, x, expert_offsets, gather, gather_div)
+        a.dout_stride = _rows("dout", dout, rows, self.H, (self.dtype,), self.device)
+        _flat("gate_up", gate_up, (rows, 2 * self.I), self._dtypes, self.device)
+        if accumulate and (dw1 is True or dw2 is True):
+            raise ValueError("accumulate needs the tensors to add to")
+        if gather is not None and dx is not None and dx is not False:
+            if dest_row is None:
+                raise ValueError("dx of gathered rows needs dest_row")
+            dest_row = dest_row.reshape(-1) if dest_row.dim() == 2 else dest_row
+            _flat("dest_row", dest_row, (x.shape[0] * gather_div,), (torch.int32,), self.device)
+            a.dest_row = dest_row.data_ptr()
+        dw_dtype = dw_dtype or next((g.dtype for g in (dw1, dw2) if isinstance(g, torch.Tensor)), self.dtype)
+        n = lib.moe_expert_ffn_grad_workspace_size(rows, self.H, self.I, self.E, int(gather is not None))
+
+        def grad(g, shape, dtype):
+            if g is True:
+                return torch.empty(shape, dtype=dtype, device=self.device)
+            return None if g is False else g
+
+        with _allocate_on(stream):
+            dx = grad(dx, (x.shape[0], self.H), self.dtype)
+            dw1 = grad(dw1, self.w1.shape, dw_dtype)
+            dw2 = grad(dw2, self.w2.shape, dw_dtype)
+            ws = _u8(n, self.device)
+        a.dx_dtype = a.dtype
+        if dx is not None:
+            a.dx_stride = _rows("dx", dx, x.shape[0], self.H, self._dtypes, self.device)
+            a.dx_dtype, a.dx = FLOAT_DTYPE[dx.dtype], dx.data_ptr()
+        a.dw_dtype = FLOAT_DTYPE.get(dw_dtype, -1)
+        if dw1 is not None:
+            a.dw1 = _flat("dw1", dw1, self.w1.shape, (dw_dtype,), self.device).data_ptr()
+        if dw2 is not None:
+            a.dw2 = _flat("dw2", dw2, self.w2.shape, (dw_dtype,), self.device).data_ptr()
+        a.accumulate, a.save_dtype = int(accumulate), FLOAT_DTYPE[gate_up.dtype]
+        a.dout, a.gate_up, a.workspace, a.workspace_bytes = dout.data_ptr(), gate_up.data_ptr(), ws.data_ptr(), n
+        _check(lib.moe_expert_ffn_backward(ctypes.byref(a), _stream(stream)))
+        _keep_until_done(stream, dx, dw1, dw2, dout, x, expert_offsets, gate_up, gather, dest_row, self.w1, self.w2)
+        return dx, dw1, dw2
 
 
 class NormOutput(NamedTuple):

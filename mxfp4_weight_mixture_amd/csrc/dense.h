@@ -37,6 +37,10 @@ struct DenseJob {
   // K split over blocks: where the block's part of the sums goes, fp32 [M][N]
   // (set by the kernels; null: the sums are whole)
   float* partial;
+  // rows of A picked by index (grouped products; null: row m of a): row
+  // gather[m] / gather_div of the gather_rows there are, zeros outside them
+  const int32_t* gather;
+  int gather_div, gather_rows;
 };
 
 // Token counts up to this are decode batches: their adapters differ from token

@@ -108,6 +108,22 @@ struct Operand {
       }
     }
   }
+  // rows [r0, r0 + ROWS) of p.gather, whose rows of A all lie within 2^31 bytes
+  __device__ __forceinline__ void init_gather(const DenseJob& p, int r0, int wave, int lane) {
+    static_assert(!T, "rows are gathered where K is contiguous");
+    up_mask = 0;
+    up_off = 0;
+    base = static_cast<const char*>(p.a);
+    stage_step = BK * 2;
+#pragma unroll
+    for (int j = 0; j < LOADS; ++j) {
+      const int r = (wave * LOADS + j) * (64 / CPR) + lane / CPR;
+      const int c = (lane % CPR) ^ swz(r);
+      if (j == 0) kk = c * 8;
+      const int g = r0 + r < p.M ? p.gather[r0 + r] : -1, row = g / p.gather_div;
+      off[j] = g >= 0 && row < p.gather_rows ? (uint32_t)(row * p.lda * 2 + c * 16) : kOut;
+    }
+  }
   // rows of B in gate / up blocks of 32
   __device__ __forceinline__ void init_gate(const DenseJob& p, int nt, int wave, int lane) {
     const int I = p.N >> 1, i0 = nt * (ROWS / 2);
@@ -170,7 +186,7 @@ __device__ __forceinline__ void tile_at(int t, int mt, int nt, int* m, int* n) {
 }
 
 // The C tile of 64 FM rows from m0 and the nt-th 64 FN columns of B.
-template <typename E, bool TA, bool TB, int EPI, bool LORA, int FM, int FN, int NST, int BK>
+template <typename E, bool TA, bool TB, int EPI, bool LORA, int FM, int FN, int NST, int BK, bool GATHER = false>
 __device__ __forceinline__ void dense_tile(const DenseJob& p, int m0, int nt, char* lds) {
   typedef typename Vec<E>::v8 v8;
   constexpr int BM = 64 * FM, BN = 64 * FN;
@@ -197,7 +213,8 @@ __device__ __forceinline__ void dense_tile(const DenseJob& p, int m0, int nt, ch
   }
   A a;
   B b;
-  a.init(p.a, p.lda, p.M, m0, wave, lane);
+  if constexpr (GATHER) a.init_gather(p, m0, wave, lane);
+  else a.init(p.a, p.lda, p.M, m0, wave, lane);
   if constexpr (EPI == kEpiGate) b.init_gate(p, nt, wave, lane);
   else b.init(p.b, p.ldb, p.N, nt * BN, wave, lane);
   const int K = p.K, nst = (K + BK - 1) / BK;

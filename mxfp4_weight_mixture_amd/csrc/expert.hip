@@ -1,0 +1,526 @@
+// The routed experts with 16-bit weights: entry points, and products grouped by
+// expert.
+//
+// Forward: x w1[e]^T with the gate in its epilogue, h w2[e]^T.  Backward: dh =
+// dout w2[e] with the gate's derivative in its epilogue, dx rows = d_gate_up
+// w1[e], dw1[e] = d_gate_up^T x and dw2[e] = dout^T h over expert e's rows.
+//
+// The rows of an expert are known on the device only, so a one-block kernel
+// first lists the row tiles: whole ones of 256 rows and one for an expert's
+// remainder, filed by what it needs (more than 128 rows, 65 to 128, up to 64).
+// Every product of the call then takes its tiles from that list, the large ones
+// first; the grid is what the rows could need at most, and blocks past the
+// list's end return.  A weight gradient has the same tiles for every expert and
+// the expert's rows as its K.
+#include <algorithm>
+
+#include "dense_tile.h"
+
+namespace mxmoe {
+namespace {
+
+constexpr int kMaxExperts = 8192;
+constexpr int kClasses = 3;
+
+// The list of row tiles: how many of each class, then their entries.
+struct RowTile {
+  int32_t expert, row, rows, pad;   // rows [row, row + rows) of `expert`
+};
+struct RowPlan {
+  int32_t count[8];
+  __host__ __device__ RowTile* list(int cls, int cap) {
+    return reinterpret_cast<RowTile*>(this + 1) + (size_t)cls * cap;
+  }
+};
+// Row tiles that the rows can make at most, in any class.
+int tile_cap(int rows, int E) { return rows / 256 + std::min(E, rows) + 1; }
+size_t plan_bytes(int rows, int E) {
+  return align_up(sizeof(RowPlan) + (size_t)kClasses * tile_cap(rows, E) * sizeof(RowTile), 256);
+}
+
+// Expert e's rows, cut to [0, rows).
+__device__ __forceinline__ void expert_rows(const int32_t* offsets, int e, int rows, int* first, int* count) {
+  const int a = min(max(offsets[e], 0), rows), b = min(max(offsets[e + 1], a), rows);
+  *first = a, *count = b - a;
+}
+__device__ __forceinline__ int remainder_class(int rows) { return rows > 128 ? 0 : rows > 64 ? 1 : 2; }
+
+// One block; thread t lists experts [t per, (t + 1) per) behind those of the
+// threads before it.
+__global__ __launch_bounds__(1024) void plan_rows_kernel(const int32_t* offsets, int E, int rows, int cap,
+                                                         RowPlan* plan) {
+  __shared__ int sums[16][kClasses];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, per = (E + 1023) >> 10;
+  const int e0 = min((int)threadIdx.x * per, E), e1 = min(e0 + per, E);
+  int n[kClasses] = {0, 0, 0}, at[kClasses];
+  for (int e = e0; e < e1; ++e) {
+    int first, count;
+    expert_rows(offsets, e, rows, &first, &count);
+    n[0] += count >> 8;
+    if (count & 255) n[remainder_class(count & 255)]++;
+  }
+#pragma unroll
+  for (int c = 0; c < kClasses; ++c) {
+    int v = n[c];   // inclusive sum over the wave's lanes
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const int u = __shfl_up(v, off);
+      if (lane >= off) v += u;
+    }
+    if (lane == 63) sums[wave][c] = v;
+    at[c] = v - n[c];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int c = 0; c < kClasses; ++c) {
+    int total = 0;
+    for (int w = 0; w < 16; ++w) {
+      if (w == wave) at[c] += total;
+      total += sums[w][c];
+    }
+    if (threadIdx.x == 0) plan->count[c] = min(total, cap);
+  }
+  for (int e = e0; e < e1; ++e) {
+    int first, count;
+    expert_rows(offsets, e, rows, &first, &count);
+    for (int r = 0; r < count; r += 256) {
+      const int m = min(count - r, 256), c = m == 256 ? 0 : remainder_class(m);
+      // (offsets that do not ascend could ask for more than the list holds)
+      if (at[c] < cap) plan->list(c, cap)[at[c]] = RowTile{e, first + r, m, 0};
+      ++at[c];
+    }
+  }
+}
+
+// A product for every expert: the job of rows 0 and expert 0, and how far the
+// next expert's weights are.
+struct GroupJob {
+  DenseJob job;
+  RowPlan* plan;
+  int cap;
+  int64_t b_step;   // elements
+};
+
+// The job of one row tile.
+__device__ __forceinline__ DenseJob tile_job(const GroupJob& g, const RowTile& t) {
+  DenseJob p = g.job;
+  const int64_t row = t.row;
+  p.M = t.rows;
+  if (p.gather) p.gather += row;
+  else p.a = static_cast<const char*>(p.a) + row * p.lda * 2;
+  p.b = static_cast<const char*>(p.b) + t.expert * g.b_step * 2;
+  p.c = static_cast<char*>(p.c) + row * p.ldc * (p.c_dtype == MOE_FLOAT_FP32 ? 4 : 2);
+  if (p.gu) {
+    const int64_t width = p.epi == kEpiGate ? p.N : 2 * (int64_t)p.N;
+    p.gu = static_cast<char*>(p.gu) + row * width * (p.gu_dtype == MOE_FLOAT_FP32 ? 4 : 2);
+  }
+  if (p.h) p.h = static_cast<char*>(p.h) + row * p.N * 2;
+  return p;
+}
+
+__device__ __forceinline__ int up8(int v) { return (v + 7) & ~7; }
+
+// Tiles of 256 columns (128 gate and 128 up ones); each class's blocks begin at
+// a multiple of 8, so that its run on every XCD is contiguous.  Tiles of 256
+// rows go in groups that share an expert's weights in the L2; the other classes
+// have one tile an expert, whose rows stay in the L2 while all its columns pass.
+template <typename E, bool TB, int EPI, bool GATHER>
+__global__ __launch_bounds__(256, 1) void group_tile_kernel(GroupJob g) {
+  __shared__ __attribute__((aligned(1024))) char lds[kTileLds];
+  const int cols = EPI == kEpiGate ? 128 : 256, width = EPI == kEpiGate ? g.job.N >> 1 : g.job.N;
+  const int nts = (width + cols - 1) / cols;
+  const int n0 = g.plan->count[0], n1 = g.plan->count[1], n2 = g.plan->count[2];
+  int b = blockIdx.x;
+  if (b < up8(n0 * nts)) {
+    if (b >= n0 * nts) return;
+    int mt, nt;
+    tile_at(xcd_run(b, n0 * nts), n0, nts, &mt, &nt);
+    const DenseJob p = tile_job(g, g.plan->list(0, g.cap)[mt]);
+    dense_tile<E, false, TB, EPI, false, 4, 4, 4, 32, GATHER>(p, 0, nt, lds);
+    return;
+  }
+  b -= up8(n0 * nts);
+  if (b < up8(n1 * nts)) {
+    if (b >= n1 * nts) return;
+    const int t = xcd_run(b, n1 * nts);
+    const DenseJob p = tile_job(g, g.plan->list(1, g.cap)[t / nts]);
+    dense_tile<E, false, TB, EPI, false, 2, 4, 3, 64, GATHER>(p, 0, t % nts, lds);
+    return;
+  }
+  b -= up8(n1 * nts);
+  if (b >= n2 * nts) return;
+  const int t = xcd_run(b, n2 * nts);
+  const DenseJob p = tile_job(g, g.plan->list(2, g.cap)[t / nts]);
+  dense_tile<E, false, TB, EPI, false, 1, 4, 3, 64, GATHER>(p, 0, t % nts, lds);
+}
+
+// Weight gradients: C[e] = A^T B over expert e's rows, both stored [rows][..].
+template <typename E, int F>
+__global__ __launch_bounds__(256, 1) void group_grad_kernel(GroupJob g, const int32_t* offsets, int experts, int rows) {
+  __shared__ __attribute__((aligned(1024))) char lds[kTileLds];
+  constexpr int TILE = 64 * F;
+  const int mts = (g.job.M + TILE - 1) / TILE, nts = (g.job.N + TILE - 1) / TILE;
+  const int t = xcd_run(blockIdx.x, gridDim.x), e = t / (mts * nts);
+  int first, mt, nt;
+  DenseJob p = g.job;
+  expert_rows(offsets, e, rows, &first, &p.K);
+  if (p.K == 0 && p.add) return;
+  tile_at(t % (mts * nts), mts, nts, &mt, &nt);
+  p.a = static_cast<const char*>(p.a) + (int64_t)first * p.lda * 2;
+  p.b = static_cast<const char*>(p.b) + (int64_t)first * p.ldb * 2;
+  const int64_t step = (int64_t)e * p.M * p.ldc * (p.c_dtype == MOE_FLOAT_FP32 ? 4 : 2);
+  p.c = static_cast<char*>(p.c) + step;
+  if (p.add) p.add = static_cast<const char*>(p.add) + step;
+  if constexpr (F == 4) dense_tile<E, true, true, kEpiPlain, false, 4, 4, 4, 32>(p, mt * TILE, nt, lds);
+  else dense_tile<E, true, true, kEpiPlain, false, 2, 2, 4, 64>(p, mt * TILE, nt, lds);
+}
+
+// x's rows in expert order (the weight gradient's products take no gather).
+template <typename E>
+__global__ __launch_bounds__(256) void gather_rows_kernel(DenseJob p, const int32_t* offsets, int experts, int rows,
+                                                          void* out) {
+  const int lo = max(offsets[0], 0), hi = min(offsets[experts], rows);
+  for (int64_t r = lo + (int64_t)blockIdx.x; r < hi; r += gridDim.x) {
+    const int g = p.gather[r], row = g / p.gather_div;
+    const bool in = g >= 0 && row < p.gather_rows;
+    for (int v = threadIdx.x; v < p.K >> 3; v += 256) {
+      uint4 q{};
+      if (in) q = *reinterpret_cast<const uint4*>(static_cast<const E*>(p.a) + row * p.lda + 8 * v);
+      *reinterpret_cast<uint4*>(static_cast<E*>(out) + r * p.K + 8 * v) = q;
+    }
+  }
+}
+
+// dx[t] = the sum of the token's rows, in slot order.
+template <typename E>
+__global__ __launch_bounds__(512) void sum_rows_kernel(const float* __restrict__ dxr, const int32_t* __restrict__ dest,
+                                                       const int32_t* __restrict__ offsets, int experts, int rows,
+                                                       int div, int H, void* __restrict__ dx, int dx_dtype,
+                                                       int64_t dx_stride) {
+  const int64_t t = blockIdx.x;
+  const int lo = max(offsets[0], 0), hi = min(offsets[experts], rows);
+  for (int v = threadIdx.x; v < H >> 3; v += blockDim.x) {
+    F8 s{};
+    for (int j0 = 0; j0 < div; j0 += 8) {
+      F8 r[8];
+      bool in[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int d = j0 + j < div ? dest[t * div + j0 + j] : -1;
+        in[j] = d >= lo && d < hi;
+        if (in[j]) r[j] = load8<E>(dxr, MOE_FLOAT_FP32, (size_t)d * H + 8 * v);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (in[j])
+#pragma unroll
+          for (int e = 0; e < 8; ++e) s.v[e] += r[j].v[e];
+    }
+    store8<E>(dx, dx_dtype, t * dx_stride + 8 * v, s);
+  }
+}
+
+// ---- launches ------------------------------------------------------------
+struct Group {
+  int rows, E;
+  const int32_t* offsets;
+  RowPlan* plan;
+};
+
+moe_status launch_plan(const Group& g, hipStream_t s) {
+  hipLaunchKernelGGL(plan_rows_kernel, dim3(1), dim3(1024), 0, s, g.offsets, g.E, g.rows, tile_cap(g.rows, g.E), g.plan);
+  MXMOE_HIP(hipGetLastError());
+  return MOE_OK;
+}
+
+template <typename E>
+moe_status launch_group_typed(const Group& g, const DenseJob& j, int64_t b_step, hipStream_t s) {
+  const GroupJob q{j, g.plan, tile_cap(g.rows, g.E), b_step};
+  const int cols = j.epi == kEpiGate ? 128 : 256, width = j.epi == kEpiGate ? j.N / 2 : j.N;
+  const int64_t blocks = (int64_t)(g.rows / 256 + std::min(g.E, g.rows)) * ((width + cols - 1) / cols) + 16;
+  const dim3 grid((unsigned)blocks), block(256);
+  if (j.epi == kEpiGate && j.gather) hipLaunchKernelGGL((group_tile_kernel<E, false, kEpiGate, true>), grid, block, 0, s, q);
+  else if (j.epi == kEpiGate) hipLaunchKernelGGL((group_tile_kernel<E, false, kEpiGate, false>), grid, block, 0, s, q);
+  else if (j.epi == kEpiGateGrad) hipLaunchKernelGGL((group_tile_kernel<E, true, kEpiGateGrad, false>), grid, block, 0, s, q);
+  else if (j.tb) hipLaunchKernelGGL((group_tile_kernel<E, true, kEpiPlain, false>), grid, block, 0, s, q);
+  else hipLaunchKernelGGL((group_tile_kernel<E, false, kEpiPlain, false>), grid, block, 0, s, q);
+  MXMOE_HIP(hipGetLastError());
+  return MOE_OK;
+}
+moe_status launch_group(const Group& g, const DenseJob& j, int64_t b_step, hipStream_t s) {
+  return j.dtype == MOE_FLOAT_BF16 ? launch_group_typed<__bf16>(g, j, b_step, s)
+                                   : launch_group_typed<_Float16>(g, j, b_step, s);
+}
+
+template <typename E>
+moe_status launch_grad_typed(const Group& g, const DenseJob& j, hipStream_t s) {
+  const GroupJob q{j, nullptr, 0, 0};
+  auto tiles = [&](int n) { return (int64_t)g.E * ((j.M + n - 1) / n) * ((j.N + n - 1) / n); };
+  if (tiles(256) >= 512)
+    hipLaunchKernelGGL((group_grad_kernel<E, 4>), dim3((unsigned)tiles(256)), dim3(256), 0, s, q, g.offsets, g.E, g.rows);
+  else
+    hipLaunchKernelGGL((group_grad_kernel<E, 2>), dim3((unsigned)tiles(128)), dim3(256), 0, s, q, g.offsets, g.E, g.rows);
+  MXMOE_HIP(hipGetLastError());
+  return MOE_OK;
+}
+moe_status launch_grad(const Group& g, const DenseJob& j, hipStream_t s) {
+  return j.dtype == MOE_FLOAT_BF16 ? launch_grad_typed<__bf16>(g, j, s) : launch_grad_typed<_Float16>(g, j, s);
+}
+
+// ---- checks and workspaces -------------------------------------------------
+moe_status check_experts(const char* what, int rows, int H, int I, int E, int layout, int act, int dtype) {
+  MXMOE_TRY(check_width(what, "H", H));
+  MXMOE_TRY(check_width(what, "I", I));
+  if (E < 1 || E > kMaxExperts) return fail(MOE_ERR_SHAPE, "%s: E = %d outside [1, %d]", what, E, kMaxExperts);
+  if (rows < 0 || rows > kMaxTokens) return fail(MOE_ERR_SHAPE, "%s: rows = %d outside [0, %d]", what, rows, kMaxTokens);
+  const int64_t wide = std::max(H, 2 * I);
+  if (((int64_t)rows / 64 + std::min(E, rows) + 1) * ((wide + 63) / 64) >= 1 << 24)
+    return fail(MOE_ERR_SHAPE, "%s: %d rows of %lld are too many for one launch", what, rows, (long long)wide);
+  if ((int64_t)E * ((H + 63) / 64) * ((2 * I + 63) / 64) >= 1ll << 26)
+    return fail(MOE_ERR_SHAPE, "%s: %d experts of %d x %d are too many for one launch", what, E, 2 * I, H);
+  if (layout != MOE_EPI_SWIGLU_SPLIT && layout != MOE_EPI_SWIGLU_INTERLEAVED)
+    return fail(MOE_ERR_INVALID_ARG, "%s: layout %d must be a SWIGLU epilogue", what, layout);
+  if (act != MOE_GATE_SILU && act != MOE_GATE_GELU)
+    return fail(MOE_ERR_INVALID_ARG, "%s: bad gate_act %d", what, act);
+  return check_dtype16(what, dtype);
+}
+bool within_limits(int rows, int H, int I, int E) {
+  return rows >= 0 && rows <= kMaxTokens && H > 0 && H <= kMaxWidth && I > 0 && I <= kMaxWidth && E > 0 &&
+         E <= kMaxExperts;
+}
+moe_status check_gather(const char* what, const int32_t* gather, int rows, int tokens, int div, int64_t stride) {
+  if (div < 0 || (div == 0 && gather))
+    return fail(MOE_ERR_SHAPE, "%s: gather_div = %d must be at least 1 with gather, 0 without", what, div);
+  if (div == 0) return MOE_OK;
+  if (!gather && rows > 0) return fail(MOE_ERR_INVALID_ARG, "%s: null pointer (gather)", what);
+  if (tokens < 0) return fail(MOE_ERR_SHAPE, "%s: tokens = %d < 0", what, tokens);
+  if (tokens * stride >= 1ll << 30)
+    return fail(MOE_ERR_SHAPE, "%s: gathered rows reach over %lld elements, past 2^30", what, (long long)(tokens * stride));
+  return MOE_OK;
+}
+// Index arrays: 4-byte aligned, apart from every output.
+moe_status check_words(const char* what, const Span* out, int n_out, const Span* words, int n) {
+  for (int i = 0; i < n; ++i) {
+    if (reinterpret_cast<uintptr_t>(words[i].p) & 3)
+      return fail(MOE_ERR_INVALID_ARG, "%s: %s is not 4-byte aligned", what, words[i].name);
+    for (int j = 0; j < n_out; ++j)
+      if (overlap(out[j], words[i]))
+        return fail(MOE_ERR_INVALID_ARG, "%s: %s overlaps %s", what, out[j].name, words[i].name);
+  }
+  return MOE_OK;
+}
+
+struct ForwardWs {
+  size_t h, total;
+};
+ForwardWs forward_ws(int rows, int H, int I, int E) {
+  ForwardWs w{};
+  w.h = plan_bytes(rows, E);
+  w.total = w.h + align_up((size_t)rows * I * 2, 256) + 256;
+  return w;
+}
+struct GradWs {
+  size_t dgu, h, x, dx, total;   // x in expert order and dx by row: gathered calls
+};
+GradWs grad_ws(int rows, int H, int I, int E, bool gathered) {
+  GradWs w{};
+  w.dgu = plan_bytes(rows, E);
+  w.h = w.dgu + align_up((size_t)rows * 2 * I * 2, 256);
+  w.x = w.h + align_up((size_t)rows * I * 2, 256);
+  w.dx = w.x + (gathered ? align_up((size_t)rows * H * 2, 256) : 0);
+  w.total = w.dx + (gathered ? align_up((size_t)rows * H * 4, 256) : 0) + 256;
+  return w;
+}
+
+}  // namespace
+}  // namespace mxmoe
+
+using namespace mxmoe;
+
+extern "C" {
+
+size_t moe_expert_ffn_workspace_size(int32_t rows, int32_t H, int32_t I, int32_t E) {
+  return within_limits(rows, H, I, E) ? forward_ws(rows, H, I, E).total : 0;
+}
+
+moe_status moe_expert_ffn_forward(const moe_expert_ffn_args* a, void* stream) {
+  const char* what = "expert FFN";
+  clear_error();
+  if (!a) return fail(MOE_ERR_INVALID_ARG, "%s: null args", what);
+  MXMOE_TRY(check_experts(what, a->rows, a->H, a->I, a->E, a->layout, a->gate_act, a->dtype));
+  MXMOE_TRY(check_dtype_or_fp32(what, "out_dtype", a->out_dtype, a->dtype));
+  MXMOE_TRY(check_dtype_or_fp32(what, "save_dtype", a->save_dtype, a->dtype));
+  MXMOE_TRY(check_stride(what, "x_stride", a->x_stride, a->H));
+  MXMOE_TRY(check_stride(what, "out_stride", a->out_stride, a->H));
+  MXMOE_TRY(check_gather(what, a->gather, a->rows, a->tokens, a->gather_div, a->x_stride));
+  const int64_t rows = a->rows, H = a->H, I = a->I, E = a->E;
+  const ForwardWs w = forward_ws(a->rows, a->H, a->I, a->E);
+  if (rows > 0) {
+    if ((!a->x && !(a->gather && a->tokens == 0)) || !a->expert_offsets || !a->w1 || !a->w2 || !a->out)
+      return fail(MOE_ERR_INVALID_ARG, "%s: null pointer", what);
+    if (!a->workspace || a->workspace_bytes < w.total)
+      return fail(MOE_ERR_WORKSPACE, "%s: workspace %zu bytes, need %zu", what, a->workspace_bytes, w.total);
+    const Span out[] = {span("out", a->out, rows, H, a->out_stride, a->out_dtype),
+                        span("gate_up", a->gate_up, rows, 2 * I, 2 * I, a->save_dtype),
+                        {"workspace", a->workspace, w.total}};
+    const Span in[] = {span("x", a->x, a->gather ? a->tokens : rows, H, a->x_stride, a->dtype),
+                       span("w1", a->w1, E * 2 * I, H, H, a->dtype), span("w2", a->w2, E * H, I, I, a->dtype)};
+    MXMOE_TRY(check_spans(what, out, 3, in, 3));
+    const Span words[] = {{"expert_offsets", a->expert_offsets, (size_t)(E + 1) * 4},
+                          {"gather", a->gather, a->gather ? (size_t)rows * 4 : 0}};
+    MXMOE_TRY(check_words(what, out, 3, words, 2));
+  }
+  MXMOE_TRY(check_device());
+  if (rows == 0) return MOE_OK;
+  const hipStream_t s = (hipStream_t)stream;
+  uint8_t* const ws = static_cast<uint8_t*>(a->workspace);
+  const Group g{a->rows, a->E, a->expert_offsets, reinterpret_cast<RowPlan*>(ws)};
+  MXMOE_TRY(launch_plan(g, s));
+
+  DenseJob j{};
+  j.dtype = a->dtype;
+  j.act = a->gate_act;
+  j.interleaved = a->layout == MOE_EPI_SWIGLU_INTERLEAVED;
+  j.a = a->x, j.lda = a->x_stride;
+  j.gather = a->gather, j.gather_div = a->gather_div, j.gather_rows = a->tokens;
+  j.b = a->w1, j.ldb = H;
+  j.N = 2 * a->I, j.K = a->H;
+  j.epi = kEpiGate;
+  j.c = ws + w.h, j.ldc = I, j.c_dtype = a->dtype;
+  j.gu = a->gate_up, j.gu_dtype = a->save_dtype;
+  MXMOE_TRY(launch_group(g, j, 2 * I * H, s));
+
+  j.a = ws + w.h, j.lda = I;
+  j.gather = nullptr;
+  j.b = a->w2, j.ldb = I;
+  j.N = a->H, j.K = a->I;
+  j.epi = kEpiPlain;
+  j.gu = nullptr;
+  j.c = a->out, j.ldc = a->out_stride, j.c_dtype = a->out_dtype;
+  return launch_group(g, j, H * I, s);
+}
+
+size_t moe_expert_ffn_grad_workspace_size(int32_t rows, int32_t H, int32_t I, int32_t E, int32_t gathered) {
+  return within_limits(rows, H, I, E) ? grad_ws(rows, H, I, E, gathered != 0).total : 0;
+}
+
+moe_status moe_expert_ffn_backward(const moe_expert_ffn_grad_args* a, void* stream) {
+  const char* what = "expert FFN backward";
+  clear_error();
+  if (!a) return fail(MOE_ERR_INVALID_ARG, "%s: null args", what);
+  MXMOE_TRY(check_experts(what, a->rows, a->H, a->I, a->E, a->layout, a->gate_act, a->dtype));
+  MXMOE_TRY(check_dtype_or_fp32(what, "save_dtype", a->save_dtype, a->dtype));
+  MXMOE_TRY(check_dtype_or_fp32(what, "dx_dtype", a->dx_dtype, a->dtype));
+  MXMOE_TRY(check_dtype_or_fp32(what, "dw_dtype", a->dw_dtype, a->dtype));
+  if (a->accumulate != 0 && a->accumulate != 1)
+    return fail(MOE_ERR_INVALID_ARG, "%s: accumulate %d must be 0 or 1", what, a->accumulate);
+  MXMOE_TRY(check_stride(what, "dout_stride", a->dout_stride, a->H));
+  if (a->dw1) MXMOE_TRY(check_stride(what, "x_stride", a->x_stride, a->H));
+  if (a->dx) MXMOE_TRY(check_stride(what, "dx_stride", a->dx_stride, a->H));
+  MXMOE_TRY(check_gather(what, a->gather, a->rows, a->tokens, a->gather_div, a->dw1 ? a->x_stride : 0));
+  const bool gathered = a->gather_div > 0;
+  if (gathered && (int64_t)a->tokens * a->gather_div >= 1ll << 31)
+    return fail(MOE_ERR_SHAPE, "%s: tokens * gather_div overflows int32", what);
+  const int64_t rows = a->rows, H = a->H, I = a->I, E = a->E;
+  const int64_t x_rows = gathered ? a->tokens : rows, slots = gathered ? x_rows * a->gather_div : 0;
+  const GradWs w = grad_ws(a->rows, a->H, a->I, a->E, gathered);
+  if (gathered && a->dx && x_rows > 0 && !a->dest_row) return fail(MOE_ERR_INVALID_ARG, "%s: dx with gather needs dest_row", what);
+  if (gathered && x_rows >= 1 << 22) return fail(MOE_ERR_SHAPE, "%s: tokens = %d, past 2^22", what, a->tokens);
+  if (rows > 0) {
+    if (!a->dout || !a->expert_offsets || !a->w2 || !a->gate_up || (a->dw1 && !a->x && x_rows > 0) || (a->dx && !a->w1))
+      return fail(MOE_ERR_INVALID_ARG, "%s: null pointer", what);
+    if (!a->workspace || a->workspace_bytes < w.total)
+      return fail(MOE_ERR_WORKSPACE, "%s: workspace %zu bytes, need %zu", what, a->workspace_bytes, w.total);
+  } else if (((gathered && a->dx && x_rows > 0) || a->dw1 || a->dw2) && !a->expert_offsets) {
+    return fail(MOE_ERR_INVALID_ARG, "%s: null pointer", what);
+  }
+  const Span out[] = {span("dx", a->dx, x_rows, H, a->dx_stride, a->dx_dtype),
+                      span("dw1", a->dw1, E * 2 * I, H, H, a->dw_dtype), span("dw2", a->dw2, E * H, I, I, a->dw_dtype),
+                      {"workspace", a->workspace, rows > 0 ? w.total : 0}};
+  const Span in[] = {span("dout", a->dout, rows, H, a->dout_stride, a->dtype),
+                     span("x", a->dw1 ? a->x : nullptr, x_rows, H, a->x_stride, a->dtype),
+                     span("w1", a->dx ? a->w1 : nullptr, E * 2 * I, H, H, a->dtype),
+                     span("w2", a->w2, E * H, I, I, a->dtype),
+                     span("gate_up", a->gate_up, rows, 2 * I, 2 * I, a->save_dtype)};
+  MXMOE_TRY(check_spans(what, out, 4, in, 5));
+  const Span words[] = {{"expert_offsets", a->expert_offsets, (size_t)(E + 1) * 4},
+                        {"gather", a->gather, a->gather ? (size_t)rows * 4 : 0},
+                        {"dest_row", a->dx ? a->dest_row : nullptr, a->dx ? (size_t)slots * 4 : 0}};
+  MXMOE_TRY(check_words(what, out, 4, words, 3));
+  MXMOE_TRY(check_device());
+  if (!a->dx && !a->dw1 && !a->dw2) return MOE_OK;
+  const hipStream_t s = (hipStream_t)stream;
+  uint8_t* const ws = static_cast<uint8_t*>(a->workspace);
+  const Group g{a->rows, a->E, a->expert_offsets, reinterpret_cast<RowPlan*>(ws)};
+
+  DenseJob j{};
+  j.dtype = a->dtype;
+  j.act = a->gate_act;
+  j.interleaved = a->layout == MOE_EPI_SWIGLU_INTERLEAVED;
+  const bool any = rows > 0;
+  if (any) {
+    MXMOE_TRY(launch_plan(g, s));
+    // the gradients of gate and up, and h
+    j.a = a->dout, j.lda = a->dout_stride;
+    j.b = a->w2, j.ldb = I, j.tb = 1;
+    j.N = a->I, j.K = a->H;
+    j.epi = kEpiGateGrad;
+    j.gu = const_cast<void*>(a->gate_up), j.gu_dtype = a->save_dtype;
+    j.c = ws + w.dgu, j.ldc = 2 * I, j.c_dtype = a->dtype;
+    j.h = ws + w.h;
+    MXMOE_TRY(launch_group(g, j, H * I, s));
+  }
+  j.epi = kEpiPlain;
+  j.gu = j.h = nullptr;
+  if (a->dx && any) {
+    j.a = ws + w.dgu, j.lda = 2 * I;
+    j.b = a->w1, j.ldb = H, j.tb = 1;
+    j.N = a->H, j.K = 2 * a->I;
+    if (gathered) j.c = ws + w.dx, j.ldc = H, j.c_dtype = MOE_FLOAT_FP32;
+    else j.c = a->dx, j.ldc = a->dx_stride, j.c_dtype = a->dx_dtype;
+    MXMOE_TRY(launch_group(g, j, 2 * I * H, s));
+  }
+  if (a->dx && gathered && x_rows > 0) {
+    const dim3 grid((unsigned)x_rows), block(std::min(512, (a->H / 8 + 63) / 64 * 64));
+    const float* const dxr = reinterpret_cast<const float*>(ws + w.dx);
+    if (a->dtype == MOE_FLOAT_BF16)
+      hipLaunchKernelGGL((sum_rows_kernel<__bf16>), grid, block, 0, s, dxr, a->dest_row, a->expert_offsets, a->E, a->rows,
+                         a->gather_div, a->H, a->dx, a->dx_dtype, a->dx_stride);
+    else
+      hipLaunchKernelGGL((sum_rows_kernel<_Float16>), grid, block, 0, s, dxr, a->dest_row, a->expert_offsets, a->E,
+                         a->rows, a->gather_div, a->H, a->dx, a->dx_dtype, a->dx_stride);
+    MXMOE_HIP(hipGetLastError());
+  }
+  // the weights' gradients sum over the expert's rows
+  if (!any && a->accumulate) return MOE_OK;
+  j.ta = j.tb = 1;
+  j.c_dtype = a->dw_dtype;
+  if (a->dw1) {
+    j.a = ws + w.dgu, j.lda = 2 * I;
+    j.b = a->x, j.ldb = a->x_stride;
+    if (gathered && any) {
+      DenseJob q{};
+      q.a = a->x, q.lda = a->x_stride, q.K = a->H;
+      q.gather = a->gather, q.gather_div = a->gather_div, q.gather_rows = a->tokens;
+      hipLaunchKernelGGL((gather_rows_kernel<_Float16>), dim3((unsigned)std::min<int64_t>(rows, 1 << 20)), dim3(256), 0, s, q, a->expert_offsets,
+                         a->E, a->rows, ws + w.x);   // (any 16 bits)
+      MXMOE_HIP(hipGetLastError());
+      j.b = ws + w.x, j.ldb = H;
+    }
+    j.M = 2 * a->I, j.N = a->H;
+    j.c = a->dw1, j.ldc = H;
+    j.add = a->accumulate ? a->dw1 : nullptr, j.ldadd = H;
+    MXMOE_TRY(launch_grad(g, j, s));
+  }
+  if (a->dw2) {
+    j.a = a->dout, j.lda = a->dout_stride;
+    j.b = ws + w.h, j.ldb = I;
+    j.M = a->H, j.N = a->I;
+    j.c = a->dw2, j.ldc = I;
+    j.add = a->accumulate ? a->dw2 : nullptr, j.ldadd = I;
+    MXMOE_TRY(launch_grad(g, j, s));
+  }
+  return MOE_OK;
+}
+
+}  // extern "C"

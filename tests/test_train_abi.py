@@ -150,3 +150,90 @@ def test_norm_workspace_query():
     q = mx.lib.moe_rms_norm_grad_workspace_size
     assert q(4, 64) >= 4 * 64 * 4 and q(1 << 20, 7168) == q(1 << 21, 7168)
     assert q(-1, 64) == q(4, 0) == q(1 << 22, 64) == q(4, 40000) == 0
+
+
+def _expert(**kw):
+    d = dict(rows=8, H=64, I=32, E=3, layout=1, gate_act=0, dtype=0, out_dtype=0, save_dtype=2, tokens=4, gather_div=2,
+             x=P, gather=2 * P, expert_offsets=3 * P, w1=4 * P, w2=5 * P, out=6 * P, gate_up=7 * P, x_stride=64,
+             out_stride=64, workspace=8 * P, workspace_bytes=P)
+    d.update(kw)
+    return mx.ExpertFfnArgs(**d)
+
+
+@pytest.mark.parametrize("kw,status,needle", [
+    (dict(rows=-1), "MOE_ERR_SHAPE", "rows = -1"),
+    (dict(rows=(1 << 28) + 1), "MOE_ERR_SHAPE", "rows ="),
+    (dict(rows=1 << 20, I=1 << 16), "MOE_ERR_SHAPE", "too many"),
+    (dict(E=8192, I=1 << 15, H=1 << 10, x_stride=1 << 10, out_stride=1 << 10), "MOE_ERR_SHAPE", "experts of"),
+    (dict(H=60), "MOE_ERR_SHAPE", "H = 60"),
+    (dict(I=4), "MOE_ERR_SHAPE", "I = 4"),
+    (dict(E=0), "MOE_ERR_SHAPE", "E = 0"),
+    (dict(E=8193), "MOE_ERR_SHAPE", "E = 8193"),
+    (dict(layout=0), "MOE_ERR_INVALID_ARG", "layout"),
+    (dict(gate_act=2), "MOE_ERR_INVALID_ARG", "gate_act"),
+    (dict(dtype=2), "MOE_ERR_INVALID_ARG", "dtype"),
+    (dict(out_dtype=1), "MOE_ERR_INVALID_ARG", "out_dtype"),
+    (dict(save_dtype=1), "MOE_ERR_INVALID_ARG", "save_dtype"),
+    (dict(x_stride=56), "MOE_ERR_SHAPE", "x_stride"),
+    (dict(out_stride=68), "MOE_ERR_SHAPE", "out_stride"),
+    (dict(tokens=-1), "MOE_ERR_SHAPE", "tokens = -1"),
+    (dict(gather_div=0), "MOE_ERR_SHAPE", "gather_div = 0"),
+    (dict(tokens=1 << 24), "MOE_ERR_SHAPE", "2^30"),
+    (dict(x=None), "MOE_ERR_INVALID_ARG", "null"),
+    (dict(expert_offsets=None), "MOE_ERR_INVALID_ARG", "null"),
+    (dict(workspace=None), "MOE_ERR_WORKSPACE", "need"),
+    (dict(workspace_bytes=64), "MOE_ERR_WORKSPACE", "need"),
+    (dict(x=P + 8), "MOE_ERR_INVALID_ARG", "x is not 16-byte"),
+    (dict(gather=2 * P + 2), "MOE_ERR_INVALID_ARG", "gather is not 4-byte"),
+    (dict(out=P + 256), "MOE_ERR_INVALID_ARG", "out overlaps x"),
+    (dict(out=3 * P), "MOE_ERR_INVALID_ARG", "out overlaps expert_offsets"),
+    (dict(gate_up=6 * P + 512), "MOE_ERR_INVALID_ARG", "out and gate_up"),
+    (dict(workspace=5 * P - 256), "MOE_ERR_INVALID_ARG", "workspace overlaps w2"),
+])
+def test_expert_refusals(kw, status, needle):
+    _refused(mx.lib.moe_expert_ffn_forward(ctypes.byref(_expert(**kw)), None), status, needle)
+
+
+def _expert_grad(**kw):
+    d = dict(rows=8, H=64, I=32, E=3, layout=1, gate_act=0, dtype=0, save_dtype=2, dx_dtype=0, dw_dtype=0, accumulate=0,
+             tokens=4, gather_div=2, dout=P, x=2 * P, gather=3 * P, dest_row=4 * P, expert_offsets=5 * P, w1=6 * P,
+             w2=7 * P, gate_up=8 * P, dx=9 * P, dw1=10 * P, dw2=11 * P, dout_stride=64, x_stride=64, dx_stride=64,
+             workspace=12 * P, workspace_bytes=P)
+    d.update(kw)
+    return mx.ExpertFfnGradArgs(**d)
+
+
+@pytest.mark.parametrize("kw,status,needle", [
+    (dict(rows=-1), "MOE_ERR_SHAPE", "rows = -1"),
+    (dict(H=0), "MOE_ERR_SHAPE", "H = 0"),
+    (dict(E=-1), "MOE_ERR_SHAPE", "E = -1"),
+    (dict(save_dtype=1), "MOE_ERR_INVALID_ARG", "save_dtype"),
+    (dict(dx_dtype=1), "MOE_ERR_INVALID_ARG", "dx_dtype"),
+    (dict(dw_dtype=1), "MOE_ERR_INVALID_ARG", "dw_dtype"),
+    (dict(accumulate=2), "MOE_ERR_INVALID_ARG", "accumulate"),
+    (dict(dout_stride=60), "MOE_ERR_SHAPE", "dout_stride"),
+    (dict(x_stride=0), "MOE_ERR_SHAPE", "x_stride"),
+    (dict(dx_stride=66), "MOE_ERR_SHAPE", "dx_stride"),
+    (dict(gather_div=0), "MOE_ERR_SHAPE", "gather_div = 0"),
+    (dict(tokens=1 << 20, gather_div=1 << 12), "MOE_ERR_SHAPE", "overflows"),
+    (dict(dest_row=None), "MOE_ERR_INVALID_ARG", "dest_row"),
+    (dict(dout=None), "MOE_ERR_INVALID_ARG", "null"),
+    (dict(gate_up=None), "MOE_ERR_INVALID_ARG", "null"),
+    (dict(rows=0, expert_offsets=None), "MOE_ERR_INVALID_ARG", "null"),
+    (dict(workspace_bytes=64), "MOE_ERR_WORKSPACE", "need"),
+    (dict(dw1=10 * P + 8), "MOE_ERR_INVALID_ARG", "dw1 is not 16-byte"),
+    (dict(dx=P), "MOE_ERR_INVALID_ARG", "dx overlaps dout"),
+    (dict(dx=4 * P), "MOE_ERR_INVALID_ARG", "dx overlaps dest_row"),
+    (dict(dw2=7 * P), "MOE_ERR_INVALID_ARG", "dw2 overlaps w2"),
+    (dict(dw2=10 * P), "MOE_ERR_INVALID_ARG", "dw1 and dw2"),
+])
+def test_expert_backward_refusals(kw, status, needle):
+    _refused(mx.lib.moe_expert_ffn_backward(ctypes.byref(_expert_grad(**kw)), None), status, needle)
+
+
+def test_expert_workspace_queries():
+    f, b = mx.lib.moe_expert_ffn_workspace_size, mx.lib.moe_expert_ffn_grad_workspace_size
+    assert f(8, 64, 32, 3) >= 8 * 32 * 2 and b(8, 64, 32, 3, 0) >= 8 * 96 * 2
+    assert b(8, 64, 32, 3, 1) >= b(8, 64, 32, 3, 0) + 8 * 64 * 6
+    for bad in ((-1, 64, 32, 3), (8, 0, 32, 3), (8, 64, 1 << 19, 3), (8, 64, 32, 8193)):
+        assert f(*bad) == 0 and b(*bad, 1) == 0
