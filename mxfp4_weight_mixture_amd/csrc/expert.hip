@@ -101,8 +101,13 @@ struct GroupJob {
   int64_t b_step;   // elements
 };
 
-// The job of one row tile.
-__device__ __forceinline__ DenseJob tile_job(const GroupJob& g, const RowTile& t) {
+// The job of one row tile.  (What memory gives is the same for the whole block
+// but not to the compiler, which would keep the buffer resources' bases in vector
+// registers and read them back for every DMA: 1472 against 1340 us for 49152 x 4096
+// x 4096.)
+__device__ __forceinline__ DenseJob tile_job(const GroupJob& g, const RowTile& at) {
+  const RowTile t{__builtin_amdgcn_readfirstlane(at.expert), __builtin_amdgcn_readfirstlane(at.row),
+                  __builtin_amdgcn_readfirstlane(at.rows), 0};
   DenseJob p = g.job;
   const int64_t row = t.row;
   p.M = t.rows;
