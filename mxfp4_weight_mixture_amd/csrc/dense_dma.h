@@ -11,6 +11,15 @@ constexpr uint32_t kOut = 0x80000000u;   // an offset behind every resource's ra
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_at(const void* base) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, 0x7fffffff, 0x00020000);
 }
+// A pointer that is the same in every lane, in scalar registers whatever the
+// compiler made of its parts (a resource in vector registers is read back lane by
+// lane, in a loop, at every load).
+__device__ __forceinline__ const char* uniform_ptr(const void* p) {
+  const uint64_t a = reinterpret_cast<uint64_t>(p);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)a);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32));
+  return reinterpret_cast<const char*>((uint64_t)hi << 32 | lo);
+}
 // 16 bytes per lane, global -> LDS (lane i writes dst + 16 i)
 __device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t r, uint32_t voff, void* dst) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)dst, 16, voff, 0, 0, 0);

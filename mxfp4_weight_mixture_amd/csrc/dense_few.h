@@ -28,20 +28,27 @@ namespace {
 
 constexpr int kFewWaves = 8;
 
-template <typename E, int MB, int NB, int EPI, bool DMA, int D>
-__global__ __launch_bounds__(64 * kFewWaves) void few_kernel(DenseJob p) {
+// LDS of a block: the waves' turns (then their parts of the sums), and the sums.
+// (One array: with several, the compiler gives each alias scopes by which it
+// drains all LDS DMA before an LDS read.)
+template <int MB, int NB, bool DMA, int D, int W = kFewWaves>
+struct FewLds {
+  static constexpr int PITCH = 16 * NB + 4;
+  static constexpr int TURN = DMA ? (MB + NB) * 2048 : 0;         // bytes of a wave's turn: A, then weights
+  static constexpr int PART = W * MB * NB * 1024, XBUF = W * D * TURN;
+  static constexpr int BUF = XBUF > PART ? XBUF : PART;
+  static constexpr int BYTES = BUF + MB * 16 * PITCH * 4;
+};
+
+// Weight columns [block * COLS, + COLS) for all rows of A (up to 16 MB).
+template <typename E, int MB, int NB, int EPI, bool DMA, int D, bool GATHER = false, int WAVES = kFewWaves>
+__device__ __forceinline__ void few_block(const DenseJob& p, int block, char* lds) {
   typedef typename Vec<E>::v8 v8;
-  constexpr int WAVES = kFewWaves;
-  constexpr int COLS = NB * (EPI == kEpiGate ? 8 : 16), PITCH = 16 * NB + 4;
-  constexpr int TURN = DMA ? (MB + NB) * 2048 : 0;                // LDS bytes of a wave's turn: A, then weights
-  constexpr int PART = WAVES * MB * NB * 1024, XBUF = WAVES * D * TURN;
-  constexpr int BUF = XBUF > PART ? XBUF : PART;
-  // one array: with several, the compiler gives each alias scopes by which it
-  // drains all LDS DMA before an LDS read
-  __shared__ __attribute__((aligned(1024))) char lds[BUF + MB * 16 * PITCH * 4];
+  using L = FewLds<MB, NB, DMA, D, WAVES>;
+  constexpr int COLS = NB * (EPI == kEpiGate ? 8 : 16), PITCH = L::PITCH, TURN = L::TURN, BUF = L::BUF;
   float (*const sums)[PITCH] = reinterpret_cast<float (*)[PITCH]>(lds + BUF);   // padded: reads spread over the banks
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int width = EPI == kEpiGate ? p.N >> 1 : p.N, n0 = blockIdx.x * COLS;
+  const int width = EPI == kEpiGate ? p.N >> 1 : p.N, n0 = block * COLS;
   // weight row behind column c of the block's 16 NB
   auto b_row = [&](int c) {
     if (EPI != kEpiGate) return min(n0 + c, width - 1);
@@ -60,9 +67,13 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_kernel(DenseJob p) {
   constexpr int PER = DMA ? 2 : 1;
   uint32_t xoff[PER * MB], woff[PER * NB];
 #pragma unroll
-  for (int j = 0; j < PER * MB; ++j)
-    xoff[j] = (uint32_t)(min(DMA ? 8 * j + (lane >> 3) : 16 * j + l16, p.M - 1) * (p.lda * 2)) +
-              (DMA ? (c8 ^ ((j & 1) << 2)) * 16 : kl * 2);
+  for (int j = 0; j < PER * MB; ++j) {
+    int row = min(DMA ? 8 * j + (lane >> 3) : 16 * j + l16, p.M - 1);
+    const int g = GATHER ? p.gather[row] : 0;
+    if constexpr (GATHER) row = g / p.gather_div;
+    xoff[j] = (uint32_t)(row * (p.lda * 2)) + (DMA ? (c8 ^ ((j & 1) << 2)) * 16 : kl * 2);
+    if (GATHER && (g < 0 || row >= p.gather_rows)) xoff[j] = kOut;
+  }
 #pragma unroll
   for (int j = 0; j < PER * NB; ++j)
     woff[j] = (uint32_t)((b_row(DMA ? 8 * j + (lane >> 3) : 16 * j + l16) - row0) * (p.ldb * 2)) +
@@ -83,7 +94,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_kernel(DenseJob p) {
       for (int h = 0; h < 2; ++h) {
         const bool in = k + 32 * h + kl < K;
 #pragma unroll
-        for (int i = 0; i < MB; ++i) xr[u][h][i] = load16<E>(rx, in ? xoff[i] + 64 * h : kOut);
+        for (int i = 0; i < MB; ++i) xr[u][h][i] = load16<E>(rx, in ? xoff[i] + 64 * h : kOut);   // (kOut + 64: behind, too)
 #pragma unroll
         for (int n = 0; n < NB; ++n) wr[u][h][n] = load16<E>(rw, in ? woff[n] + 64 * h : kOut);
       }
@@ -204,6 +215,12 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_kernel(DenseJob p) {
     const int m = t / (2 * NB), c = t % (2 * NB) * 8;
     if (m < p.M && n0 + c < width) finish_plain<E>(p, m, n0 + c, sums8(m, c));
   }
+}
+
+template <typename E, int MB, int NB, int EPI, bool DMA, int D>
+__global__ __launch_bounds__(64 * kFewWaves) void few_kernel(DenseJob p) {
+  __shared__ __attribute__((aligned(1024))) char lds[FewLds<MB, NB, DMA, D>::BYTES];
+  few_block<E, MB, NB, EPI, DMA, D>(p, blockIdx.x, lds);
 }
 
 }  // namespace

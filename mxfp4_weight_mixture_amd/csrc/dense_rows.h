@@ -111,7 +111,7 @@ __device__ __forceinline__ void finish_plain(const DenseJob& p, int m, int n, F8
 // product's matrix instructions take.  Two parts of it, as the adapters' small
 // rows have, would double that product, a third of the block's work, for an
 // error of the output 0.7 times as large.
-template <typename E>
+template <typename E, bool KEEP = true>
 __device__ __forceinline__ void finish_gate(const DenseJob& p, int m, int i, F8 g, F8 u) {
   const int I = p.N >> 1;
   if (i + 8 > I) {
@@ -133,7 +133,7 @@ __device__ __forceinline__ void finish_gate(const DenseJob& p, int m, int i, F8 
 #pragma unroll
     for (int e = 0; e < 8; ++e) g.v[e] += a.v[e], u.v[e] += b.v[e];
   }
-  if (p.gu) store_pair<E>(p.gu, p.gu_dtype, (size_t)m * p.N, I, i, p.interleaved, g, u);
+  if (KEEP && p.gu) store_pair<E>(p.gu, p.gu_dtype, (size_t)m * p.N, I, i, p.interleaved, g, u);
   F8 h;
 #pragma unroll
   for (int e = 0; e < 8; ++e) h.v[e] = gate_act(p.act, g.v[e]) * u.v[e];
@@ -142,11 +142,10 @@ __device__ __forceinline__ void finish_gate(const DenseJob& p, int m, int i, F8 
 // Gate gradient: d are dh's columns [i, i + 8), in fp32.  h and the gradients of
 // gate and up are rounded once each, to the next products' 16-bit operands, in
 // fp16 with its range: the loss is scaled for it, as for dout itself.
+// g, u: the kept pre-activations.
 template <typename E>
-__device__ __forceinline__ void finish_gate_grad(const DenseJob& p, int m, int i, F8 d) {
-  if (p.partial) return store8<E>(p.partial, MOE_FLOAT_FP32, (size_t)m * p.N + i, d);
-  F8 g, u, h;
-  load_pair<E>(p.gu, p.gu_dtype, (size_t)m * 2 * p.N, p.N, i, p.interleaved, &g, &u);
+__device__ __forceinline__ void finish_gate_grad(const DenseJob& p, int m, int i, const F8& d, F8 g, F8 u) {
+  F8 h;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     float a, da;
@@ -157,6 +156,14 @@ __device__ __forceinline__ void finish_gate_grad(const DenseJob& p, int m, int i
   }
   store8<E>(p.h, p.dtype, (size_t)m * p.N + i, h);
   store_pair<E>(p.c, p.c_dtype, (size_t)m * p.ldc, p.N, i, p.interleaved, g, u);
+}
+
+template <typename E>
+__device__ __forceinline__ void finish_gate_grad(const DenseJob& p, int m, int i, const F8& d) {
+  if (p.partial) return store8<E>(p.partial, MOE_FLOAT_FP32, (size_t)m * p.N + i, d);
+  F8 g, u;
+  load_pair<E>(p.gu, p.gu_dtype, (size_t)m * 2 * p.N, p.N, i, p.interleaved, &g, &u);
+  finish_gate_grad<E>(p, m, i, d, g, u);
 }
 
 // Part z of `splits` of K, in whole 64-deep stages: the job's operands from

@@ -14,6 +14,7 @@
 // the expert's rows as its K.
 #include <algorithm>
 
+#include "dense_few.h"
 #include "dense_tile.h"
 
 namespace mxmoe {
@@ -21,10 +22,16 @@ namespace {
 
 constexpr int kMaxExperts = 8192;
 constexpr int kClasses = 3;
+// Tiles of an expert that go through all its columns together, so that they
+// share its weights' tiles in the L2.  (Groups of four that did not mind where an
+// expert ends: 32 experts of 1536 rows took 1737 us for 4096 x 4096 with the gate,
+// one expert of all those rows 1586.)
+constexpr int kTileGroup = 6;
 
 // The list of row tiles: how many of each class, then their entries.
 struct RowTile {
-  int32_t expert, row, rows, pad;   // rows [row, row + rows) of `expert`
+  int32_t expert, row, rows;   // rows [row, row + rows) of `expert`
+  int32_t group;               // its group's first tile << 4 | tiles, for an expert's whole tiles
 };
 struct RowPlan {
   int32_t count[8];
@@ -33,7 +40,7 @@ struct RowPlan {
   }
 };
 // Row tiles that the rows can make at most, in any class.
-int tile_cap(int rows, int E) { return rows / 256 + std::min(E, rows) + 1; }
+int tile_cap(int rows, int E) { return rows / 128 + std::min(E, rows) + 1; }
 size_t plan_bytes(int rows, int E) {
   return align_up(sizeof(RowPlan) + (size_t)kClasses * tile_cap(rows, E) * sizeof(RowTile), 256);
 }
@@ -43,21 +50,21 @@ __device__ __forceinline__ void expert_rows(const int32_t* offsets, int e, int r
   const int a = min(max(offsets[e], 0), rows), b = min(max(offsets[e + 1], a), rows);
   *first = a, *count = b - a;
 }
-__device__ __forceinline__ int remainder_class(int rows) { return rows > 128 ? 0 : rows > 64 ? 1 : 2; }
+__device__ __forceinline__ int tile_class(int rows) { return rows > 128 ? 0 : rows > 64 ? 1 : 2; }
 
 // One block; thread t lists experts [t per, (t + 1) per) behind those of the
 // threads before it.
-__global__ __launch_bounds__(1024) void plan_rows_kernel(const int32_t* offsets, int E, int rows, int cap,
+__global__ __launch_bounds__(1024) void plan_rows_kernel(const int32_t* offsets, int E, int rows, int whole, int cap,
                                                          RowPlan* plan) {
   __shared__ int sums[16][kClasses];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, per = (E + 1023) >> 10;
-  const int e0 = min((int)threadIdx.x * per, E), e1 = min(e0 + per, E);
-  int n[kClasses] = {0, 0, 0}, at[kClasses];
-  for (int e = e0; e < e1; ++e) {
-    int first, count;
-    expert_rows(offsets, e, rows, &first, &count);
-    n[0] += count >> 8;
-    if (count & 255) n[remainder_class(count & 255)]++;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, per = (E + blockDim.x - 1) / blockDim.x;
+  const int e0 = min((int)threadIdx.x * per, E), wc = tile_class(whole);
+  int n[kClasses] = {0, 0, 0}, at[kClasses], first = 0, count = 0;
+  for (int i = 0; i < per; ++i) {
+    count = 0;
+    if (e0 + i < E) expert_rows(offsets, e0 + i, rows, &first, &count);
+    n[wc] += count / whole;
+    if (count % whole) n[tile_class(count % whole)]++;
   }
 #pragma unroll
   for (int c = 0; c < kClasses; ++c) {
@@ -74,20 +81,43 @@ __global__ __launch_bounds__(1024) void plan_rows_kernel(const int32_t* offsets,
 #pragma unroll
   for (int c = 0; c < kClasses; ++c) {
     int total = 0;
-    for (int w = 0; w < 16; ++w) {
+    for (int w = 0; w < (int)blockDim.x >> 6; ++w) {
       if (w == wave) at[c] += total;
       total += sums[w][c];
     }
     if (threadIdx.x == 0) plan->count[c] = min(total, cap);
   }
-  for (int e = e0; e < e1; ++e) {
-    int first, count;
-    expert_rows(offsets, e, rows, &first, &count);
-    for (int r = 0; r < count; r += 256) {
-      const int m = min(count - r, 256), c = m == 256 ? 0 : remainder_class(m);
-      // (offsets that do not ascend could ask for more than the list holds)
-      if (at[c] < cap) plan->list(c, cap)[at[c]] = RowTile{e, first + r, m, 0};
-      ++at[c];
+  // (offsets that do not ascend could ask for more than the list holds)
+  auto put = [&](int c, int i, const RowTile& t) {
+    if (i < cap) plan->list(c, cap)[i] = t;
+  };
+  for (int i = 0; i < per; ++i) {
+    const int e = e0 + i;
+    if (per > 1) {   // (one expert a thread: still in registers)
+      count = 0;
+      if (e < E) expert_rows(offsets, e, rows, &first, &count);
+    }
+    const int rest = count % whole, rc = tile_class(rest), full = count / whole;
+    const int tiles = full + (rest && rc == wc);   // of the whole tiles' class
+    // those go out by the wave's lanes together: one expert may have any number
+    for (uint64_t has = __ballot(tiles > 0); has; has &= has - 1) {
+      const int l = __ffsll((unsigned long long)has) - 1;
+      const int le = __builtin_amdgcn_readlane(e, l), lf = __builtin_amdgcn_readlane(first, l);
+      const int lc = __builtin_amdgcn_readlane(count, l), lt = __builtin_amdgcn_readlane(tiles, l);
+      const int la = __builtin_amdgcn_readlane(at[wc], l);
+      // groups of equal size, the larger ones first
+      const int groups = (lt + kTileGroup - 1) / kTileGroup, small = lt / groups, more = lt - groups * small;
+      for (int k = lane; k < lt; k += 64) {
+        const bool big = k < more * (small + 1);
+        const int size = big ? small + 1 : small;
+        const int begin = big ? k / size * size : more * (small + 1) + (k - more * (small + 1)) / size * size;
+        put(wc, la + k, RowTile{le, lf + k * whole, min(lc - k * whole, whole), (la + begin) << 4 | size});
+      }
+    }
+    at[wc] += tiles;
+    if (rest && rc != wc) {
+      put(rc, at[rc], RowTile{e, first + full * whole, rest, at[rc] << 4 | 1});
+      ++at[rc];
     }
   }
 }
@@ -123,6 +153,16 @@ __device__ __forceinline__ DenseJob tile_job(const GroupJob& g, const RowTile& a
   return p;
 }
 
+// Unit t of a class of row tiles, nts column tiles each: a group's tiles side by
+// side, column by column.
+__device__ __forceinline__ RowTile unit_at(const GroupJob& g, int cls, int t, int nts, int* nt) {
+  const RowTile* const list = g.plan->list(cls, g.cap);
+  const int group = __builtin_amdgcn_readfirstlane(list[t / nts].group), first = group >> 4, tiles = group & 15;
+  const int in = t - first * nts;
+  *nt = in / tiles;
+  return list[first + in % tiles];
+}
+
 __device__ __forceinline__ int up8(int v) { return (v + 7) & ~7; }
 
 // Tiles of 256 columns (128 gate and 128 up ones); each class's blocks begin at
@@ -138,9 +178,8 @@ __global__ __launch_bounds__(256, 1) void group_tile_kernel(GroupJob g) {
   int b = blockIdx.x;
   if (b < up8(n0 * nts)) {
     if (b >= n0 * nts) return;
-    int mt, nt;
-    tile_at(xcd_run(b, n0 * nts), n0, nts, &mt, &nt);
-    const DenseJob p = tile_job(g, g.plan->list(0, g.cap)[mt]);
+    int nt;
+    const DenseJob p = tile_job(g, unit_at(g, 0, xcd_run(b, n0 * nts), nts, &nt));
     dense_tile<E, false, TB, EPI, false, 4, 4, 4, 32, GATHER>(p, 0, nt, lds);
     return;
   }
@@ -159,25 +198,115 @@ __global__ __launch_bounds__(256, 1) void group_tile_kernel(GroupJob g) {
   dense_tile<E, false, TB, EPI, false, 1, 4, 3, 64, GATHER>(p, 0, t % nts, lds);
 }
 
+// The same in tiles of up to 128 rows and 128 columns, two blocks per CU.
+constexpr int kNarrowLds = 72 << 10;
+template <typename E, bool TB, int EPI, bool GATHER>
+__global__ __launch_bounds__(256, 2) void group_narrow_kernel(GroupJob g) {
+  __shared__ __attribute__((aligned(1024))) char lds[kNarrowLds];
+  const int cols = EPI == kEpiGate ? 64 : 128, width = EPI == kEpiGate ? g.job.N >> 1 : g.job.N;
+  const int nts = (width + cols - 1) / cols;
+  const int n1 = g.plan->count[1], n2 = g.plan->count[2];
+  int b = blockIdx.x;
+  if (b < up8(n1 * nts)) {
+    if (b >= n1 * nts) return;
+    int nt;
+    const DenseJob p = tile_job(g, unit_at(g, 1, xcd_run(b, n1 * nts), nts, &nt));
+    dense_tile<E, false, TB, EPI, false, 2, 2, 4, 32, GATHER>(p, 0, nt, lds);
+    return;
+  }
+  b -= up8(n1 * nts);
+  if (b >= n2 * nts) return;
+  const int t = xcd_run(b, n2 * nts);
+  const DenseJob p = tile_job(g, g.plan->list(2, g.cap)[t / nts]);
+  dense_tile<E, false, TB, EPI, false, 1, 2, 3, 64, GATHER>(p, 0, t % nts, lds);
+}
+
+// Row tile y of all experts' in order, found from the offsets by every wave for
+// itself; none: rows 0.
+__device__ __forceinline__ RowTile nth_tile(const int32_t* offsets, int E, int rows, int whole, int y) {
+  const int lane = threadIdx.x & 63;
+  constexpr int C = 16;
+  for (int e0 = 0; e0 < E; e0 += 64 * C) {
+    int f[C], n[C];   // C times 64 experts, their loads in flight together
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      const int e = e0 + i * 64 + lane;
+      f[i] = n[i] = 0;
+      if (e < E) expert_rows(offsets, e, rows, &f[i], &n[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      const int mine = (n[i] + whole - 1) / whole;
+      uint64_t past = __ballot(mine > 0);   // the lanes up to whose expert there are more than y tiles
+      int upto = mine;                      // tiles of this lane's expert and those before it
+      if (__ballot(mine > 1)) {
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) {
+          const int u = __shfl_up(upto, off);
+          if (lane >= off) upto += u;
+        }
+        past = __ballot(upto > y);
+        if (!past) {
+          y -= __builtin_amdgcn_readlane(upto, 63);
+          continue;
+        }
+      } else {
+        const int c = __popcll(past);
+        if (y >= c) {
+          y -= c;
+          continue;
+        }
+        for (; y > 0; --y) past &= past - 1;
+        upto = 1;
+      }
+      const int l = __ffsll((unsigned long long)past) - 1;
+      const int r = (y - __builtin_amdgcn_readlane(upto - mine, l)) * whole;
+      return RowTile{e0 + i * 64 + l, __builtin_amdgcn_readlane(f[i], l) + r,
+                     min(__builtin_amdgcn_readlane(n[i], l) - r, whole), 0};
+    }
+  }
+  return RowTile{0, 0, 0, 0};
+}
+
+// Few rows (decode): a block takes 16 NB weight rows of one expert for up to 16 MB
+// of its rows, as the dense kernel of few rows does; bound by reading the weights
+// of the experts that have rows.  Four waves split K, not eight: an expert's
+// block is short (8 turns of 64 k a wave at K = 4096 would be 4), and with 48 or 32 KB
+// of LDS three to five blocks a CU cover each other's ends (192 rows, 256 experts
+// of 4096 x 2048: 1143 us, eight waves 1330).  Every block finds its rows by itself
+// from the offsets: no launch ahead of the product.
+constexpr int kGroupFewWaves = 4;
+template <typename E, int MB, int NB, int EPI, int D, bool GATHER>
+__global__ __launch_bounds__(64 * kGroupFewWaves) void group_few_kernel(GroupJob g, const int32_t* offsets, int experts,
+                                                                        int rows) {
+  __shared__ __attribute__((aligned(1024))) char lds[FewLds<MB, NB, true, D, kGroupFewWaves>::BYTES];
+  const RowTile t = nth_tile(offsets, experts, rows, 16 * MB, blockIdx.y);
+  if (t.rows == 0) return;
+  few_block<E, MB, NB, EPI, true, D, GATHER, kGroupFewWaves>(tile_job(g, t), blockIdx.x, lds);
+}
+
 // Weight gradients: C[e] = A^T B over expert e's rows, both stored [rows][..].
 template <typename E, int F>
-__global__ __launch_bounds__(256, 1) void group_grad_kernel(GroupJob g, const int32_t* offsets, int experts, int rows) {
-  __shared__ __attribute__((aligned(1024))) char lds[kTileLds];
+__global__ __launch_bounds__(256, F == 4 ? 1 : 2) void group_grad_kernel(GroupJob g, const int32_t* offsets, int experts,
+                                                                         int rows) {
+  __shared__ __attribute__((aligned(1024))) char lds[F == 4 ? kTileLds : kNarrowLds];
   constexpr int TILE = 64 * F;
   const int mts = (g.job.M + TILE - 1) / TILE, nts = (g.job.N + TILE - 1) / TILE;
   const int t = xcd_run(blockIdx.x, gridDim.x), e = t / (mts * nts);
   int first, mt, nt;
   DenseJob p = g.job;
   expert_rows(offsets, e, rows, &first, &p.K);
+  first = __builtin_amdgcn_readfirstlane(first), p.K = __builtin_amdgcn_readfirstlane(p.K);   // (as in tile_job)
   if (p.K == 0 && p.add) return;
   tile_at(t % (mts * nts), mts, nts, &mt, &nt);
-  p.a = static_cast<const char*>(p.a) + (int64_t)first * p.lda * 2;
-  p.b = static_cast<const char*>(p.b) + (int64_t)first * p.ldb * 2;
+  mt = __builtin_amdgcn_readfirstlane(mt), nt = __builtin_amdgcn_readfirstlane(nt);
+  p.a = uniform_ptr(static_cast<const char*>(p.a) + (int64_t)first * p.lda * 2);
+  p.b = uniform_ptr(static_cast<const char*>(p.b) + (int64_t)first * p.ldb * 2);
   const int64_t step = (int64_t)e * p.M * p.ldc * (p.c_dtype == MOE_FLOAT_FP32 ? 4 : 2);
   p.c = static_cast<char*>(p.c) + step;
   if (p.add) p.add = static_cast<const char*>(p.add) + step;
   if constexpr (F == 4) dense_tile<E, true, true, kEpiPlain, false, 4, 4, 4, 32>(p, mt * TILE, nt, lds);
-  else dense_tile<E, true, true, kEpiPlain, false, 2, 2, 4, 64>(p, mt * TILE, nt, lds);
+  else dense_tile<E, true, true, kEpiPlain, false, 2, 2, 4, 32>(p, mt * TILE, nt, lds);
 }
 
 // x's rows in expert order (the weight gradient's products take no gather).
@@ -230,20 +359,75 @@ struct Group {
   int rows, E;
   const int32_t* offsets;
   RowPlan* plan;
+  int whole;  // rows of a whole row tile: 256, or 128 for narrow tiles
+  int most;   // rows that an expert has at most where a token goes to it once
 };
 
+// A few rows an expert, and too few experts with rows for narrow tiles to fill the
+// chip: the weights stream in tiles of 32 rows of them.  Us with these kernels / in
+// narrow tiles: 256 experts of 4096 x 2048, 6 rows 61 / 67, 24 rows 198 / 207, 192
+// rows 1221 / 1081 (6.3 TB/s); 64 of 2048 x 1024, 64 rows 105 / 120; 8 of 4096 x
+// 3584, 2 rows 35 / 69, 16 rows 108 / 123, 128 rows 132 / 139.  Short rows of the
+// weights are better off in narrow tiles (64 of 1024 x 768, 512 rows 62 / 58), and
+// so are more than 16 rows an expert (16 of 1096 x 776, 256 rows 24.8 / 25.5).
+// A block's rows (of a split gate also their up rows) lie within 31 bits of the first.
+bool takes_few(const Group& g, const DenseJob& j) {
+  const int64_t reach = j.epi == kEpiGate && !j.interleaved ? (int64_t)(j.N / 2 + 16) * j.ldb * 2 : 0;
+  const int64_t n = std::min(g.E, g.rows);
+  return !j.tb && j.K >= 1024 && g.rows <= 16 * n && n * ((j.N + 127) / 128) <= 1024 && reach < (1ll << 30);
+}
+
+template <typename E, int MB, int NB, int D>
+moe_status launch_few(const Group& g, const DenseJob& j, int64_t b_step, hipStream_t s) {
+  const GroupJob q{j, nullptr, 0, b_step};
+  const dim3 grid((j.N + 16 * NB - 1) / (16 * NB), g.rows / (16 * MB) + std::min(g.E, g.rows)), block(64 * kGroupFewWaves);
+  if (j.epi == kEpiGate && j.gather)
+    hipLaunchKernelGGL((group_few_kernel<E, MB, NB, kEpiGate, D, true>), grid, block, 0, s, q, g.offsets, g.E, g.rows);
+  else if (j.epi == kEpiGate)
+    hipLaunchKernelGGL((group_few_kernel<E, MB, NB, kEpiGate, D, false>), grid, block, 0, s, q, g.offsets, g.E, g.rows);
+  else
+    hipLaunchKernelGGL((group_few_kernel<E, MB, NB, kEpiPlain, D, false>), grid, block, 0, s, q, g.offsets, g.E, g.rows);
+  MXMOE_HIP(hipGetLastError());
+  return MOE_OK;
+}
+
+// Tiles of 256 columns read the least for their products, but need many of them:
+// narrow ones where, with the rows spread evenly, they would leave a third of
+// the CUs idle (us, wide / narrow: 8 experts of 4096 x 2048, 1024 rows 172 / 135, 2048
+// rows 182 / 207; 16 of 1096 x 776, 1024 rows 48 / 36; 8 of 7168 x 3584, 512 rows, 224
+// tiles, 231 / 276), and where the weights' stream is what counts (256 of 4096 x 2048,
+// 384 rows 1724 / 1685, 6144 rows 2252 / 2224, 24576 rows 2384 / 2993).
+int whole_tile(int rows, int E, int H, int I) {
+  const int n = std::max(std::min(E, rows), 1), each = (rows + n - 1) / n;
+  const int64_t columns = ((H + 255) / 256 + (I + 127) / 128) / 2;   // of the two products, on average
+  return each <= 32 || n * ((each + 255) / 256) * columns <= 176 ? 128 : 256;
+}
+
 moe_status launch_plan(const Group& g, hipStream_t s) {
-  hipLaunchKernelGGL(plan_rows_kernel, dim3(1), dim3(1024), 0, s, g.offsets, g.E, g.rows, tile_cap(g.rows, g.E), g.plan);
+  const dim3 block(std::min(1024, (g.E + 63) / 64 * 64));
+  hipLaunchKernelGGL(plan_rows_kernel, dim3(1), block, 0, s, g.offsets, g.E, g.rows, g.whole,
+                     tile_cap(g.rows, g.E), g.plan);
   MXMOE_HIP(hipGetLastError());
   return MOE_OK;
 }
 
 template <typename E>
 moe_status launch_group_typed(const Group& g, const DenseJob& j, int64_t b_step, hipStream_t s) {
+  if (takes_few(g, j))
+    return g.most <= 16 ? launch_few<E, 1, 2, 2>(g, j, b_step, s) : launch_few<E, 2, 2, 1>(g, j, b_step, s);
   const GroupJob q{j, g.plan, tile_cap(g.rows, g.E), b_step};
-  const int cols = j.epi == kEpiGate ? 128 : 256, width = j.epi == kEpiGate ? j.N / 2 : j.N;
-  const int64_t blocks = (int64_t)(g.rows / 256 + std::min(g.E, g.rows)) * ((width + cols - 1) / cols) + 16;
+  const int cols = j.epi == kEpiGate ? g.whole / 2 : g.whole, width = j.epi == kEpiGate ? j.N / 2 : j.N;
+  const int64_t blocks = (int64_t)(g.rows / g.whole + std::min(g.E, g.rows)) * ((width + cols - 1) / cols) + 16;
   const dim3 grid((unsigned)blocks), block(256);
+  if (g.whole == 128) {
+    if (j.epi == kEpiGate && j.gather) hipLaunchKernelGGL((group_narrow_kernel<E, false, kEpiGate, true>), grid, block, 0, s, q);
+    else if (j.epi == kEpiGate) hipLaunchKernelGGL((group_narrow_kernel<E, false, kEpiGate, false>), grid, block, 0, s, q);
+    else if (j.epi == kEpiGateGrad) hipLaunchKernelGGL((group_narrow_kernel<E, true, kEpiGateGrad, false>), grid, block, 0, s, q);
+    else if (j.tb) hipLaunchKernelGGL((group_narrow_kernel<E, true, kEpiPlain, false>), grid, block, 0, s, q);
+    else hipLaunchKernelGGL((group_narrow_kernel<E, false, kEpiPlain, false>), grid, block, 0, s, q);
+    MXMOE_HIP(hipGetLastError());
+    return MOE_OK;
+  }
   if (j.epi == kEpiGate && j.gather) hipLaunchKernelGGL((group_tile_kernel<E, false, kEpiGate, true>), grid, block, 0, s, q);
   else if (j.epi == kEpiGate) hipLaunchKernelGGL((group_tile_kernel<E, false, kEpiGate, false>), grid, block, 0, s, q);
   else if (j.epi == kEpiGateGrad) hipLaunchKernelGGL((group_tile_kernel<E, true, kEpiGateGrad, false>), grid, block, 0, s, q);
@@ -261,7 +445,7 @@ template <typename E>
 moe_status launch_grad_typed(const Group& g, const DenseJob& j, hipStream_t s) {
   const GroupJob q{j, nullptr, 0, 0};
   auto tiles = [&](int n) { return (int64_t)g.E * ((j.M + n - 1) / n) * ((j.N + n - 1) / n); };
-  if (tiles(256) >= 512)
+  if (tiles(256) >= 512)   // (315 tiles of 256 x 256 and short K: 150 us the whole training step, in tiles of 128 x 128 134)
     hipLaunchKernelGGL((group_grad_kernel<E, 4>), dim3((unsigned)tiles(256)), dim3(256), 0, s, q, g.offsets, g.E, g.rows);
   else
     hipLaunchKernelGGL((group_grad_kernel<E, 2>), dim3((unsigned)tiles(128)), dim3(256), 0, s, q, g.offsets, g.E, g.rows);
@@ -359,16 +543,17 @@ moe_status moe_expert_ffn_forward(const moe_expert_ffn_args* a, void* stream) {
   MXMOE_TRY(check_stride(what, "out_stride", a->out_stride, a->H));
   MXMOE_TRY(check_gather(what, a->gather, a->rows, a->tokens, a->gather_div, a->x_stride));
   const int64_t rows = a->rows, H = a->H, I = a->I, E = a->E;
+  const bool gathered = a->gather_div > 0;
   const ForwardWs w = forward_ws(a->rows, a->H, a->I, a->E);
   if (rows > 0) {
-    if ((!a->x && !(a->gather && a->tokens == 0)) || !a->expert_offsets || !a->w1 || !a->w2 || !a->out)
+    if ((!a->x && !(gathered && a->tokens == 0)) || !a->expert_offsets || !a->w1 || !a->w2 || !a->out)
       return fail(MOE_ERR_INVALID_ARG, "%s: null pointer", what);
     if (!a->workspace || a->workspace_bytes < w.total)
       return fail(MOE_ERR_WORKSPACE, "%s: workspace %zu bytes, need %zu", what, a->workspace_bytes, w.total);
     const Span out[] = {span("out", a->out, rows, H, a->out_stride, a->out_dtype),
                         span("gate_up", a->gate_up, rows, 2 * I, 2 * I, a->save_dtype),
                         {"workspace", a->workspace, w.total}};
-    const Span in[] = {span("x", a->x, a->gather ? a->tokens : rows, H, a->x_stride, a->dtype),
+    const Span in[] = {span("x", a->x, gathered ? a->tokens : rows, H, a->x_stride, a->dtype),
                        span("w1", a->w1, E * 2 * I, H, H, a->dtype), span("w2", a->w2, E * H, I, I, a->dtype)};
     MXMOE_TRY(check_spans(what, out, 3, in, 3));
     const Span words[] = {{"expert_offsets", a->expert_offsets, (size_t)(E + 1) * 4},
@@ -379,8 +564,8 @@ moe_status moe_expert_ffn_forward(const moe_expert_ffn_args* a, void* stream) {
   if (rows == 0) return MOE_OK;
   const hipStream_t s = (hipStream_t)stream;
   uint8_t* const ws = static_cast<uint8_t*>(a->workspace);
-  const Group g{a->rows, a->E, a->expert_offsets, reinterpret_cast<RowPlan*>(ws)};
-  MXMOE_TRY(launch_plan(g, s));
+  const Group g{a->rows, a->E, a->expert_offsets, reinterpret_cast<RowPlan*>(ws),
+                whole_tile(a->rows, a->E, a->H, a->I), gathered ? std::min(a->rows, a->tokens) : a->rows};
 
   DenseJob j{};
   j.dtype = a->dtype;
@@ -393,16 +578,19 @@ moe_status moe_expert_ffn_forward(const moe_expert_ffn_args* a, void* stream) {
   j.epi = kEpiGate;
   j.c = ws + w.h, j.ldc = I, j.c_dtype = a->dtype;
   j.gu = a->gate_up, j.gu_dtype = a->save_dtype;
-  MXMOE_TRY(launch_group(g, j, 2 * I * H, s));
 
-  j.a = ws + w.h, j.lda = I;
-  j.gather = nullptr;
-  j.b = a->w2, j.ldb = I;
-  j.N = a->H, j.K = a->I;
-  j.epi = kEpiPlain;
-  j.gu = nullptr;
-  j.c = a->out, j.ldc = a->out_stride, j.c_dtype = a->out_dtype;
-  return launch_group(g, j, H * I, s);
+  DenseJob k = j;
+  k.a = ws + w.h, k.lda = I;
+  k.gather = nullptr;
+  k.b = a->w2, k.ldb = I;
+  k.N = a->H, k.K = a->I;
+  k.epi = kEpiPlain;
+  k.gu = nullptr;
+  k.c = a->out, k.ldc = a->out_stride, k.c_dtype = a->out_dtype;
+
+  if (!takes_few(g, j) || !takes_few(g, k)) MXMOE_TRY(launch_plan(g, s));
+  MXMOE_TRY(launch_group(g, j, 2 * I * H, s));
+  return launch_group(g, k, H * I, s);
 }
 
 size_t moe_expert_ffn_grad_workspace_size(int32_t rows, int32_t H, int32_t I, int32_t E, int32_t gathered) {
@@ -456,7 +644,8 @@ moe_status moe_expert_ffn_backward(const moe_expert_ffn_grad_args* a, void* stre
   if (!a->dx && !a->dw1 && !a->dw2) return MOE_OK;
   const hipStream_t s = (hipStream_t)stream;
   uint8_t* const ws = static_cast<uint8_t*>(a->workspace);
-  const Group g{a->rows, a->E, a->expert_offsets, reinterpret_cast<RowPlan*>(ws)};
+  const Group g{a->rows, a->E, a->expert_offsets, reinterpret_cast<RowPlan*>(ws),
+                whole_tile(a->rows, a->E, a->H, a->I), a->rows};
 
   DenseJob j{};
   j.dtype = a->dtype;
