@@ -204,7 +204,13 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+# the current stream's handle without a Stream object around it (0.1 us; torch.cuda.current_stream() takes 2.6)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream=None):
+    if stream is None and _raw_stream is not None and torch.cuda.is_initialized():
+        return ctypes.c_void_p(_raw_stream(torch.cuda.current_device()))
     s = torch.cuda.current_stream() if stream is None else stream
     return ctypes.c_void_p(s.cuda_stream)
 
@@ -443,7 +449,7 @@ def _rows(name, t, rows, cols, dtypes, device):
 
 def _flat(name, t, shape, dtypes, device):
     """Check a contiguous tensor of a given shape."""
-    if tuple(t.shape) != tuple(shape) or t.dtype not in dtypes or t.device != device or not t.is_contiguous():
+    if t.shape != shape or t.dtype not in dtypes or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {' or '.join(str(d) for d in dtypes)} tensor of shape "
                          f"{tuple(shape)} on {device}: got {t.dtype} {tuple(t.shape)}, strides {t.stride()}, "
                          f"on {t.device}")
@@ -829,6 +835,8 @@ class RMSNorm:
             raise ValueError("weight must be a contiguous device tensor")
         self.weight, self.eps = weight, float(eps)
         self.H, self.device = weight.shape[0], weight.device
+        same = dict(H=self.H, eps=self.eps, weight=weight.data_ptr(), weight_dtype=FLOAT_DTYPE[weight.dtype])
+        self._fwd, self._bwd = NormArgs(**same), NormGradArgs(**same)
 
     def _type16(self, *tensors):
         """The 16-bit type of a call; every tensor is of it or fp32."""
@@ -849,8 +857,8 @@ class RMSNorm:
         _on_current_device(self.device, stream)
         d16 = self._type16(x, residual)
         types = (d16, torch.float32)
-        a = NormArgs(H=self.H, dtype=FLOAT_DTYPE[d16], eps=self.eps, weight=self.weight.data_ptr(),
-                     weight_dtype=FLOAT_DTYPE[self.weight.dtype])
+        a = NormArgs.from_buffer_copy(self._fwd)
+        a.dtype = FLOAT_DTYPE[d16]
         a.x_stride = _rows("x", x, None, self.H, types, self.device)
         T = a.T = x.shape[0]
         a.x, a.x_dtype = x.data_ptr(), FLOAT_DTYPE[x.dtype]
@@ -858,16 +866,21 @@ class RMSNorm:
             a.residual_stride = _rows("residual", residual, T, self.H, types, self.device)
             if residual_out is None:
                 with _allocate_on(stream):
-                    residual_out = torch.empty((T, self.H), dtype=residual.dtype, device=self.device)
-            a.residual_out_stride = _rows("residual_out", residual_out, T, self.H, (residual.dtype,), self.device)
+                    residual_out = torch.empty_like(residual, memory_format=torch.contiguous_format)
+                a.residual_out_stride = self.H
+            else:
+                a.residual_out_stride = _rows("residual_out", residual_out, T, self.H, (residual.dtype,), self.device)
             a.residual, a.residual_out = residual.data_ptr(), residual_out.data_ptr()
             a.residual_dtype = FLOAT_DTYPE[residual.dtype]
         elif residual_out is not None:
             raise ValueError("residual_out without a residual")
+        if out is not True and out is not False and out is not None:
+            a.out_stride = _rows("out", out, T, self.H, types if out_dtype is None else (out_dtype,), self.device)
         codes = scales = None
         with _allocate_on(stream):
             if out is True:
-                out = torch.empty((T, self.H), dtype=out_dtype or d16, device=self.device)
+                out = torch.empty_like(x, dtype=out_dtype or d16, memory_format=torch.contiguous_format)
+                a.out_stride = self.H
             elif out is False:
                 out = None
             if mxfp8:
@@ -875,7 +888,6 @@ class RMSNorm:
                 scales = torch.empty((T, self.H // 32), dtype=torch.uint8, device=self.device)
                 a.codes, a.scales = codes.data_ptr(), scales.data_ptr()
         if out is not None:
-            a.out_stride = _rows("out", out, T, self.H, types if out_dtype is None else (out_dtype,), self.device)
             a.out, a.out_dtype = out.data_ptr(), FLOAT_DTYPE.get(out.dtype, -1)
         elif not mxfp8:
             raise ValueError("no output: neither out nor mxfp8")
@@ -896,8 +908,8 @@ class RMSNorm:
         _on_current_device(self.device, stream)
         d16 = self._type16(x, dout, dresidual)
         types = (d16, torch.float32)
-        a = NormGradArgs(H=self.H, dtype=FLOAT_DTYPE[d16], eps=self.eps, weight=self.weight.data_ptr(),
-                         weight_dtype=FLOAT_DTYPE[self.weight.dtype], accumulate=int(accumulate))
+        a = NormGradArgs.from_buffer_copy(self._bwd)
+        a.dtype, a.accumulate = FLOAT_DTYPE[d16], int(accumulate)
         a.dout_stride = _rows("dout", dout, None, self.H, types, self.device)
         T = a.T = dout.shape[0]
         a.x_stride = _rows("x", x, T, self.H, types, self.device)
