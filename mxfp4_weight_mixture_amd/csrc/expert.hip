@@ -99,21 +99,25 @@ __global__ __launch_bounds__(1024) void plan_rows_kernel(const int32_t* offsets,
     }
     const int rest = count % whole, rc = tile_class(rest), full = count / whole;
     const int tiles = full + (rest && rc == wc);   // of the whole tiles' class
-    // those go out by the wave's lanes together: one expert may have any number
-    for (uint64_t has = __ballot(tiles > 0); has; has &= has - 1) {
-      const int l = __ffsll((unsigned long long)has) - 1;
+    // in groups of equal size, the larger ones first
+    auto put_tile = [&](int k, int e, int first, int count, int tiles, int at) {
+      const int groups = (tiles + kTileGroup - 1) / kTileGroup, small = tiles / groups, more = tiles - groups * small;
+      const bool big = k < more * (small + 1);
+      const int size = big ? small + 1 : small;
+      const int begin = big ? k / size * size : more * (small + 1) + (k - more * (small + 1)) / size * size;
+      put(wc, at + k, RowTile{e, first + k * whole, min(count - k * whole, whole), (at + begin) << 4 | size});
+    };
+    // an expert of many goes out by the wave's lanes together
+    constexpr int kMany = 16;
+    for (uint64_t many = __ballot(tiles > kMany); many; many &= many - 1) {
+      const int l = __ffsll((unsigned long long)many) - 1;
       const int le = __builtin_amdgcn_readlane(e, l), lf = __builtin_amdgcn_readlane(first, l);
       const int lc = __builtin_amdgcn_readlane(count, l), lt = __builtin_amdgcn_readlane(tiles, l);
       const int la = __builtin_amdgcn_readlane(at[wc], l);
-      // groups of equal size, the larger ones first
-      const int groups = (lt + kTileGroup - 1) / kTileGroup, small = lt / groups, more = lt - groups * small;
-      for (int k = lane; k < lt; k += 64) {
-        const bool big = k < more * (small + 1);
-        const int size = big ? small + 1 : small;
-        const int begin = big ? k / size * size : more * (small + 1) + (k - more * (small + 1)) / size * size;
-        put(wc, la + k, RowTile{le, lf + k * whole, min(lc - k * whole, whole), (la + begin) << 4 | size});
-      }
+      for (int k = lane; k < lt; k += 64) put_tile(k, le, lf, lc, lt, la);
     }
+    if (tiles <= kMany)
+      for (int k = 0; k < tiles; ++k) put_tile(k, e, first, count, tiles, at[wc]);
     at[wc] += tiles;
     if (rest && rc != wc) {
       put(rc, at[rc], RowTile{e, first + full * whole, rest, at[rc] << 4 | 1});

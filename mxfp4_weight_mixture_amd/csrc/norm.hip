@@ -23,7 +23,6 @@ namespace {
 
 constexpr int kNormMaxH = 32768;
 constexpr int kNormMaxT = (1 << 22) - 1;   // a block of up to 1024 threads a row: fewer than 2^32 threads
-constexpr int kGradBlocks = 512;   // blocks of the backward pass, and parts of dweight
 
 __device__ __forceinline__ float wave_sum(float v) {
 #pragma unroll
@@ -130,78 +129,163 @@ __global__ __launch_bounds__(1024) void norm_kernel(moe_norm_args p) {
   }
 }
 
-template <typename E, int V, bool X32>
-__global__ __launch_bounds__(1024) void norm_grad_kernel(moe_norm_grad_args p, float* part) {
+// Eight values as they are stored, in fp32 or 16 bits.
+struct Raw8 {
+  v4f a, b;
+  template <typename E>
+  __device__ __forceinline__ void load(const void* p, int dtype, size_t i) {
+    if (dtype == MOE_FLOAT_FP32) {
+      const v4f* const q = reinterpret_cast<const v4f*>(static_cast<const float*>(p) + i);
+      a = q[0], b = q[1];
+    } else {
+      a = *reinterpret_cast<const v4f*>(static_cast<const E*>(p) + i);
+    }
+  }
+  template <typename E>
+  __device__ __forceinline__ F8 values(int dtype) const {
+    if (dtype == MOE_FLOAT_FP32) return F8{{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]}};
+    const typename Vec<E>::v8 h = __builtin_bit_cast(typename Vec<E>::v8, a);
+    F8 r;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) r.v[e] = (float)h[e];
+    return r;
+  }
+};
+
+// Short rows (ALONE): every wave of a block has rows of its own, eight V lanes' worth
+// of values, and no barrier but for dweight's parts at the end.  Longer rows: the
+// block's threads share one.  The next row's loads go out before this row's sums
+// meet, where there are registers for it.  8192 x 4096 in bf16 with a residual's
+// gradient 54 us (5.0 TB/s), 64 without the loads ahead; 32768 x 512 36, 119 with a
+// block of one wave for each row.
+constexpr int kAloneWaves = 8;
+template <typename E, int V, bool ALONE>
+__global__ __launch_bounds__(ALONE ? 64 * kAloneWaves : 1024) void norm_grad_kernel(moe_norm_grad_args p, float* part) {
+  constexpr int AHEAD = ALONE || V == 1 ? 2 : 1;
   __shared__ float area[2][16][2];
-  constexpr int XT = X32 ? MOE_FLOAT_FP32 : MOE_FLOAT_BF16;
-  const int nv = p.H >> 3;
+  __shared__ v4f sums[ALONE ? kAloneWaves * V * 128 : 1];
+  const int nv = p.H >> 3, wave = threadIdx.x >> 6;
+  const int lane = ALONE ? threadIdx.x & 63 : threadIdx.x, lanes = ALONE ? 64 : blockDim.x;
+  const bool add = p.dx && p.dresidual;
   F8 w[V], dw[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const int v = i * blockDim.x + threadIdx.x;
+    const int v = i * lanes + lane;
     dw[i] = F8{};
     if (v < nv) w[i] = load8<E>(p.weight, p.weight_dtype, 8 * v);
   }
-  int turn = 0;
-  for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x, turn ^= 1) {
-    F8 x[V], d[V];
+  Raw8 x[AHEAD][V], d[AHEAD][V], q[AHEAD][V];
+  auto load = [&](int at, int64_t row) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int v = i * lanes + lane;
+      if (v >= nv) continue;
+      x[at][i].template load<E>(p.x, p.x_dtype, row * p.x_stride + 8 * v);
+      d[at][i].template load<E>(p.dout, p.dout_dtype, row * p.dout_stride + 8 * v);
+      if (add) q[at][i].template load<E>(p.dresidual, p.dresidual_dtype, row * p.dresidual_stride + 8 * v);
+    }
+  };
+  auto grad = [&](int at, int64_t row, float (*meet)[2]) {
+    F8 xv[V], dv[V];
     float ss = 0.0f, dot = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int v = i * blockDim.x + threadIdx.x;
+      const int v = i * lanes + lane;
       if (v >= nv) continue;
-      x[i] = load8<E>(p.x, XT, row * p.x_stride + 8 * v);
-      d[i] = load8<E>(p.dout, p.dout_dtype, row * p.dout_stride + 8 * v);
-    }
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int v = i * blockDim.x + threadIdx.x;
-      if (v >= nv) continue;
+      xv[i] = x[at][i].template values<E>(p.x_dtype), dv[i] = d[at][i].template values<E>(p.dout_dtype);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        ss = fmaf(x[i].v[e], x[i].v[e], ss);
-        dot = fmaf(d[i].v[e] * w[i].v[e], x[i].v[e], dot);
+        ss = fmaf(xv[i].v[e], xv[i].v[e], ss);
+        dot = fmaf(dv[i].v[e] * w[i].v[e], xv[i].v[e], dot);
       }
     }
-    block_sum2(ss, dot, area[turn]);
+    if constexpr (ALONE) ss = wave_sum(ss), dot = wave_sum(dot);
+    else block_sum2(ss, dot, meet);
     const float inv = 1.0f / sqrtf(ss / (float)p.H + p.eps);
     const float c = dot * inv / (float)p.H;   // mean(g u)
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int v = i * blockDim.x + threadIdx.x;
+      const int v = i * lanes + lane;
       if (v >= nv) continue;
-      F8 q{};
-      if (p.dx && p.dresidual) q = load8<E>(p.dresidual, p.dresidual_dtype, row * p.dresidual_stride + 8 * v);
+      F8 o{};
+      if (add) o = q[at][i].template values<E>(p.dresidual_dtype);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float u = x[i].v[e] * inv;
-        dw[i].v[e] = fmaf(d[i].v[e], u, dw[i].v[e]);
-        q.v[e] = fmaf(inv, fmaf(-u, c, d[i].v[e] * w[i].v[e]), q.v[e]);
+        const float u = xv[i].v[e] * inv;
+        dw[i].v[e] = fmaf(dv[i].v[e], u, dw[i].v[e]);
+        o.v[e] = fmaf(inv, fmaf(-u, c, dv[i].v[e] * w[i].v[e]), o.v[e]);
       }
-      if (p.dx) store8<E>(p.dx, p.dx_dtype, row * p.dx_stride + 8 * v, q);
+      if (p.dx) store8<E>(p.dx, p.dx_dtype, row * p.dx_stride + 8 * v, o);
+    }
+  };
+  const int64_t step = ALONE ? (int64_t)gridDim.x * kAloneWaves : gridDim.x;
+  const int64_t first = ALONE ? (int64_t)blockIdx.x * kAloneWaves + wave : blockIdx.x;
+  if constexpr (AHEAD == 2) {
+    // (dx may be written over dout or dresidual: the next row is another one)
+    if (first < p.T) load(0, first);
+    for (int64_t row = first; row < p.T; row += 2 * step) {
+      if (row + step < p.T) load(1, row + step);
+      grad(0, row, area[0]);
+      if (row + step >= p.T) break;
+      if (row + 2 * step < p.T) load(0, row + 2 * step);
+      grad(1, row + step, area[1]);
+    }
+  } else {
+    int turn = 0;
+    for (int64_t row = first; row < p.T; row += step, turn ^= 1) {
+      load(0, row);
+      grad(0, row, area[turn]);
     }
   }
   if (!part) return;
+  if constexpr (ALONE) {
+    // the waves' parts in order
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      v4f* const o = sums + (wave * V + i) * 128 + lane * 2;
+      o[0] = v4f{dw[i].v[0], dw[i].v[1], dw[i].v[2], dw[i].v[3]};
+      o[1] = v4f{dw[i].v[4], dw[i].v[5], dw[i].v[6], dw[i].v[7]};
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < p.H >> 2; c += 64 * kAloneWaves) {
+      v4f t = sums[c];
+#pragma unroll
+      for (int w = 1; w < kAloneWaves; ++w) t += sums[w * V * 128 + c];
+      *reinterpret_cast<v4f*>(part + (int64_t)blockIdx.x * p.H + 4 * c) = t;
+    }
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const int v = i * blockDim.x + threadIdx.x;
+    const int v = i * lanes + lane;
     if (v < nv) store8<E>(part, MOE_FLOAT_FP32, (int64_t)blockIdx.x * p.H + 8 * v, dw[i]);
   }
 }
 
-// dweight from the blocks' parts: four columns a thread, 16 threads share a
-// column's parts (part s, s + 16, ...), their sums are added in order.
+// dweight from the blocks' parts: four columns a thread, 32 threads share a
+// column's parts (part s, s + 32, ..., eight of them in flight), their sums are
+// added in order.
 template <typename E>
 __global__ __launch_bounds__(256) void norm_weight_kernel(moe_norm_grad_args p, const float* part, int parts) {
-  __shared__ v4f sums[16][16];
-  const int col = threadIdx.x & 15, s = threadIdx.x >> 4, h = (blockIdx.x * 16 + col) * 4;
+  __shared__ v4f sums[32][8];
+  const int col = threadIdx.x & 7, s = threadIdx.x >> 3, h = (blockIdx.x * 8 + col) * 4;
   v4f t{0.0f, 0.0f, 0.0f, 0.0f};
   if (h < p.H)
-    for (int b = s; b < parts; b += 16) t += *reinterpret_cast<const v4f*>(part + (int64_t)b * p.H + h);
+    for (int b0 = s; b0 < parts; b0 += 256) {
+      v4f r[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        r[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+        if (b0 + 32 * i < parts) r[i] = *reinterpret_cast<const v4f*>(part + (int64_t)(b0 + 32 * i) * p.H + h);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) t += r[i];
+    }
   sums[s][col] = t;
   __syncthreads();
   if (s != 0 || h >= p.H) return;
-  for (int i = 1; i < 16; ++i) t += sums[i][col];
+#pragma unroll
+  for (int i = 1; i < 32; ++i) t += sums[i][col];
   for (int e = 0; e < 4; ++e) {
     float v = t[e];
     if (p.dw_dtype == MOE_FLOAT_FP32) {
@@ -214,6 +298,8 @@ __global__ __launch_bounds__(256) void norm_weight_kernel(moe_norm_grad_args p, 
   }
 }
 
+// Rows of up to this many values: a wave each in the backward pass.
+constexpr int kAloneH = 1024;
 int norm_vectors(int H) { return H <= 8192 ? 1 : H <= 16384 ? 2 : 4; }
 int norm_threads(int H, int V) { return ((H / 8 + V - 1) / V + 63) / 64 * 64; }
 
@@ -236,22 +322,32 @@ moe_status launch_norm(const moe_norm_args& a, hipStream_t s) {
   }
 }
 
+// Blocks of the backward pass, and parts of dweight: 1024 threads a CU in whole
+// rounds.  (8192 x 4096 54 us with 512 blocks, 58 with 1024, 74 with 256; x 2048 32 with
+// 1024, 37 with 512; x 7168 110 with 256, 118 with 1024.)
+int grad_blocks(int T, int H) {
+  const bool alone = H <= kAloneH;
+  const int threads = alone ? 64 * kAloneWaves : norm_threads(H, norm_vectors(H));
+  return std::min(alone ? (T + kAloneWaves - 1) / kAloneWaves : T, std::max(256, 262144 / threads / 256 * 256));
+}
+
 template <typename E>
 moe_status launch_norm_grad(const moe_norm_grad_args& a, hipStream_t s) {
-  const int V = norm_vectors(a.H), parts = std::min(a.T, kGradBlocks);
+  const bool alone = a.H <= kAloneH;
+  const int parts = grad_blocks(a.T, a.H);
   float* const part = a.dweight ? static_cast<float*>(a.workspace) : nullptr;
-  const bool x32 = a.x_dtype == MOE_FLOAT_FP32;
   if (a.T > 0) {
-    const dim3 grid((unsigned)parts), block(norm_threads(a.H, V));
-#define MXMOE_LAUNCH(V, X) hipLaunchKernelGGL((norm_grad_kernel<E, V, X>), grid, block, 0, s, a, part)
-    if (V == 1) { if (x32) MXMOE_LAUNCH(1, true); else MXMOE_LAUNCH(1, false); }
-    else if (V == 2) { if (x32) MXMOE_LAUNCH(2, true); else MXMOE_LAUNCH(2, false); }
-    else { if (x32) MXMOE_LAUNCH(4, true); else MXMOE_LAUNCH(4, false); }
-#undef MXMOE_LAUNCH
+    const int V = norm_vectors(a.H);
+    const dim3 grid((unsigned)parts), block(alone ? 64 * kAloneWaves : norm_threads(a.H, V));
+    if (a.H <= 512) hipLaunchKernelGGL((norm_grad_kernel<E, 1, true>), grid, block, 0, s, a, part);
+    else if (alone) hipLaunchKernelGGL((norm_grad_kernel<E, 2, true>), grid, block, 0, s, a, part);
+    else if (V == 1) hipLaunchKernelGGL((norm_grad_kernel<E, 1, false>), grid, block, 0, s, a, part);
+    else if (V == 2) hipLaunchKernelGGL((norm_grad_kernel<E, 2, false>), grid, block, 0, s, a, part);
+    else hipLaunchKernelGGL((norm_grad_kernel<E, 4, false>), grid, block, 0, s, a, part);
     MXMOE_HIP(hipGetLastError());
   }
   if (a.dweight) {
-    hipLaunchKernelGGL((norm_weight_kernel<E>), dim3((a.H + 63) / 64), dim3(256), 0, s, a, part, parts);
+    hipLaunchKernelGGL((norm_weight_kernel<E>), dim3((a.H + 31) / 32), dim3(256), 0, s, a, part, parts);
     MXMOE_HIP(hipGetLastError());
   }
   return MOE_OK;
@@ -335,7 +431,7 @@ moe_status moe_rms_norm_forward(const moe_norm_args* a, void* stream) {
 
 size_t moe_rms_norm_grad_workspace_size(int32_t T, int32_t H) {
   if (T < 0 || T > kNormMaxT || H < 8 || H > kNormMaxH) return 0;
-  return (size_t)std::min(T, kGradBlocks) * H * 4 + 256;
+  return (size_t)grad_blocks(T, H) * H * 4 + 256;
 }
 
 moe_status moe_rms_norm_backward(const moe_norm_grad_args* a, void* stream) {
