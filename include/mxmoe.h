@@ -659,7 +659,7 @@ moe_status moe_route_backward(const float* dtopk_w, const int32_t* topk_ids, con
  *
  * Sizes: 0 <= rows <= 2^28 (0 enqueues nothing), 1 <= E <= 8192, H and I multiples
  * of 8 in [8, 262144], fewer than 2^24 tiles of 64 x 64 in `rows` + 64 * min(E, rows)
- * rows of max(H, 2I); with gather, tokens * x_stride < 2^30.  Strides, alignment and
+ * rows of max(H, 2I) and in the E matrices w1; with gather, tokens * x_stride < 2^30.  Strides, alignment and
  * overlap as for moe_gated_ffn_forward; w1, w2, gate_up are contiguous. */
 typedef struct moe_expert_ffn_args {
   int32_t        rows, H, I, E;

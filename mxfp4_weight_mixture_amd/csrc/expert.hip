@@ -169,60 +169,56 @@ __device__ __forceinline__ RowTile unit_at(const GroupJob& g, int cls, int t, in
 
 __device__ __forceinline__ int up8(int v) { return (v + 7) & ~7; }
 
-// Tiles of 256 columns (128 gate and 128 up ones); each class's blocks begin at
-// a multiple of 8, so that its run on every XCD is contiguous.  Tiles of 256
-// rows go in groups that share an expert's weights in the L2; the other classes
-// have one tile an expert, whose rows stay in the L2 while all its columns pass.
-template <typename E, bool TB, int EPI, bool GATHER>
-__global__ __launch_bounds__(256, 1) void group_tile_kernel(GroupJob g) {
-  __shared__ __attribute__((aligned(1024))) char lds[kTileLds];
-  const int cols = EPI == kEpiGate ? 128 : 256, width = EPI == kEpiGate ? g.job.N >> 1 : g.job.N;
+// One block's unit among a product's, number b from the class of the largest row
+// tiles on; returns what b is behind them all, -1 once it had one (or a gap: each
+// class begins at a multiple of 8, so that its run on every XCD is contiguous).
+// Wide: tiles of 256 columns (128 gate and 128 up ones).  Tiles of 256 rows go in
+// groups that share an expert's weights in the L2; the other classes have one tile
+// an expert, whose rows stay in the L2 while all its columns pass.
+// Narrow: tiles of up to 128 rows and 128 columns, two blocks per CU.
+constexpr int kNarrowLds = 72 << 10;
+template <typename E, bool WIDE, bool TB, int EPI, bool GATHER>
+__device__ __forceinline__ int product_unit(const GroupJob& g, int b, char* lds) {
+  const int cols = (WIDE ? 256 : 128) >> (EPI == kEpiGate ? 1 : 0), width = EPI == kEpiGate ? g.job.N >> 1 : g.job.N;
   const int nts = (width + cols - 1) / cols;
-  const int n0 = g.plan->count[0], n1 = g.plan->count[1], n2 = g.plan->count[2];
-  int b = blockIdx.x;
-  if (b < up8(n0 * nts)) {
-    if (b >= n0 * nts) return;
-    int nt;
-    const DenseJob p = tile_job(g, unit_at(g, 0, xcd_run(b, n0 * nts), nts, &nt));
-    dense_tile<E, false, TB, EPI, false, 4, 4, 4, 32, GATHER>(p, 0, nt, lds);
-    return;
+  const int n0 = WIDE ? g.plan->count[0] : 0, n1 = g.plan->count[1], n2 = g.plan->count[2];
+  int nt;
+  if constexpr (WIDE) {
+    if (b < up8(n0 * nts)) {
+      if (b >= n0 * nts) return -1;
+      const DenseJob p = tile_job(g, unit_at(g, 0, xcd_run(b, n0 * nts), nts, &nt));
+      dense_tile<E, false, TB, EPI, false, 4, 4, 4, 32, GATHER>(p, 0, nt, lds);
+      return -1;
+    }
+    b -= up8(n0 * nts);
   }
-  b -= up8(n0 * nts);
   if (b < up8(n1 * nts)) {
-    if (b >= n1 * nts) return;
+    if (b >= n1 * nts) return -1;
     const int t = xcd_run(b, n1 * nts);
-    const DenseJob p = tile_job(g, g.plan->list(1, g.cap)[t / nts]);
-    dense_tile<E, false, TB, EPI, false, 2, 4, 3, 64, GATHER>(p, 0, t % nts, lds);
-    return;
+    if constexpr (WIDE) {
+      const DenseJob p = tile_job(g, g.plan->list(1, g.cap)[t / nts]);
+      dense_tile<E, false, TB, EPI, false, 2, 4, 3, 64, GATHER>(p, 0, t % nts, lds);
+    } else {
+      const DenseJob p = tile_job(g, unit_at(g, 1, t, nts, &nt));
+      dense_tile<E, false, TB, EPI, false, 2, 2, 4, 32, GATHER>(p, 0, nt, lds);
+    }
+    return -1;
   }
   b -= up8(n1 * nts);
-  if (b >= n2 * nts) return;
-  const int t = xcd_run(b, n2 * nts);
-  const DenseJob p = tile_job(g, g.plan->list(2, g.cap)[t / nts]);
-  dense_tile<E, false, TB, EPI, false, 1, 4, 3, 64, GATHER>(p, 0, t % nts, lds);
+  if (b < up8(n2 * nts)) {
+    if (b >= n2 * nts) return -1;
+    const int t = xcd_run(b, n2 * nts);
+    const DenseJob p = tile_job(g, g.plan->list(2, g.cap)[t / nts]);
+    dense_tile<E, false, TB, EPI, false, 1, WIDE ? 4 : 2, 3, 64, GATHER>(p, 0, t % nts, lds);
+    return -1;
+  }
+  return b - up8(n2 * nts);
 }
 
-// The same in tiles of up to 128 rows and 128 columns, two blocks per CU.
-constexpr int kNarrowLds = 72 << 10;
-template <typename E, bool TB, int EPI, bool GATHER>
-__global__ __launch_bounds__(256, 2) void group_narrow_kernel(GroupJob g) {
-  __shared__ __attribute__((aligned(1024))) char lds[kNarrowLds];
-  const int cols = EPI == kEpiGate ? 64 : 128, width = EPI == kEpiGate ? g.job.N >> 1 : g.job.N;
-  const int nts = (width + cols - 1) / cols;
-  const int n1 = g.plan->count[1], n2 = g.plan->count[2];
-  int b = blockIdx.x;
-  if (b < up8(n1 * nts)) {
-    if (b >= n1 * nts) return;
-    int nt;
-    const DenseJob p = tile_job(g, unit_at(g, 1, xcd_run(b, n1 * nts), nts, &nt));
-    dense_tile<E, false, TB, EPI, false, 2, 2, 4, 32, GATHER>(p, 0, nt, lds);
-    return;
-  }
-  b -= up8(n1 * nts);
-  if (b >= n2 * nts) return;
-  const int t = xcd_run(b, n2 * nts);
-  const DenseJob p = tile_job(g, g.plan->list(2, g.cap)[t / nts]);
-  dense_tile<E, false, TB, EPI, false, 1, 2, 3, 64, GATHER>(p, 0, t % nts, lds);
+template <typename E, bool WIDE, bool TB, int EPI, bool GATHER>
+__global__ __launch_bounds__(256, WIDE ? 1 : 2) void group_tile_kernel(GroupJob g) {
+  __shared__ __attribute__((aligned(1024))) char lds[WIDE ? kTileLds : kNarrowLds];
+  product_unit<E, WIDE, TB, EPI, GATHER>(g, blockIdx.x, lds);
 }
 
 // Row tile y of all experts' in order, found from the offsets by every wave for
@@ -289,14 +285,12 @@ __global__ __launch_bounds__(64 * kGroupFewWaves) void group_few_kernel(GroupJob
   few_block<E, MB, NB, EPI, true, D, GATHER, kGroupFewWaves>(tile_job(g, t), blockIdx.x, lds);
 }
 
-// Weight gradients: C[e] = A^T B over expert e's rows, both stored [rows][..].
-template <typename E, int F>
-__global__ __launch_bounds__(256, F == 4 ? 1 : 2) void group_grad_kernel(GroupJob g, const int32_t* offsets, int experts,
-                                                                         int rows) {
-  __shared__ __attribute__((aligned(1024))) char lds[F == 4 ? kTileLds : kNarrowLds];
+// A weight gradient's tile, number t of the experts' in turn, 64 F rows and
+// columns each: C[e] = A^T B over expert e's rows, both stored [rows][..].
+template <typename E, bool WIDE, int F>
+__device__ __forceinline__ void grad_unit(const GroupJob& g, const int32_t* offsets, int rows, int t, char* lds) {
   constexpr int TILE = 64 * F;
-  const int mts = (g.job.M + TILE - 1) / TILE, nts = (g.job.N + TILE - 1) / TILE;
-  const int t = xcd_run(blockIdx.x, gridDim.x), e = t / (mts * nts);
+  const int mts = (g.job.M + TILE - 1) / TILE, nts = (g.job.N + TILE - 1) / TILE, e = t / (mts * nts);
   int first, mt, nt;
   DenseJob p = g.job;
   expert_rows(offsets, e, rows, &first, &p.K);
@@ -310,7 +304,26 @@ __global__ __launch_bounds__(256, F == 4 ? 1 : 2) void group_grad_kernel(GroupJo
   p.c = static_cast<char*>(p.c) + step;
   if (p.add) p.add = static_cast<const char*>(p.add) + step;
   if constexpr (F == 4) dense_tile<E, true, true, kEpiPlain, false, 4, 4, 4, 32>(p, mt * TILE, nt, lds);
+  else if constexpr (WIDE) dense_tile<E, true, true, kEpiPlain, false, 2, 2, 4, 64>(p, mt * TILE, nt, lds);
   else dense_tile<E, true, true, kEpiPlain, false, 2, 2, 4, 32>(p, mt * TILE, nt, lds);
+}
+
+// dx's rows, dw1 and dw2 in one launch: they need nothing of each other, and the
+// weight gradients' short tiles fill what dx's last ones leave idle.
+struct BackJobs {
+  GroupJob dx, dw[2];
+  int has_dx, units[2];   // tiles of dw1 and dw2
+};
+template <typename E, bool WIDE, int F>
+__global__ __launch_bounds__(256, WIDE ? 1 : 2) void group_back_kernel(BackJobs j, const int32_t* offsets, int rows) {
+  __shared__ __attribute__((aligned(1024))) char lds[WIDE ? kTileLds : kNarrowLds];
+  int b = blockIdx.x;
+  if (j.has_dx) b = product_unit<E, WIDE, true, kEpiPlain, false>(j.dx, b, lds);
+  if (b < 0) return;
+  const int second = b >= up8(j.units[0]);
+  if (second) b -= up8(j.units[0]);
+  if (b >= j.units[second]) return;
+  grad_unit<E, WIDE, F>(j.dw[second], offsets, rows, xcd_run(b, j.units[second]), lds);
 }
 
 // x's rows in expert order (the weight gradient's products take no gather).
@@ -415,28 +428,26 @@ moe_status launch_plan(const Group& g, hipStream_t s) {
   return MOE_OK;
 }
 
+// Blocks that a product's units can need.
+int64_t unit_bound(const Group& g, const DenseJob& j) {
+  const int cols = j.epi == kEpiGate ? g.whole / 2 : g.whole, width = j.epi == kEpiGate ? j.N / 2 : j.N;
+  return (int64_t)(g.rows / g.whole + std::min(g.E, g.rows)) * ((width + cols - 1) / cols) + 24;
+}
+
 template <typename E>
 moe_status launch_group_typed(const Group& g, const DenseJob& j, int64_t b_step, hipStream_t s) {
   if (takes_few(g, j))
     return g.most <= 16 ? launch_few<E, 1, 2, 2>(g, j, b_step, s) : launch_few<E, 2, 2, 1>(g, j, b_step, s);
   const GroupJob q{j, g.plan, tile_cap(g.rows, g.E), b_step};
-  const int cols = j.epi == kEpiGate ? g.whole / 2 : g.whole, width = j.epi == kEpiGate ? j.N / 2 : j.N;
-  const int64_t blocks = (int64_t)(g.rows / g.whole + std::min(g.E, g.rows)) * ((width + cols - 1) / cols) + 16;
-  const dim3 grid((unsigned)blocks), block(256);
-  if (g.whole == 128) {
-    if (j.epi == kEpiGate && j.gather) hipLaunchKernelGGL((group_narrow_kernel<E, false, kEpiGate, true>), grid, block, 0, s, q);
-    else if (j.epi == kEpiGate) hipLaunchKernelGGL((group_narrow_kernel<E, false, kEpiGate, false>), grid, block, 0, s, q);
-    else if (j.epi == kEpiGateGrad) hipLaunchKernelGGL((group_narrow_kernel<E, true, kEpiGateGrad, false>), grid, block, 0, s, q);
-    else if (j.tb) hipLaunchKernelGGL((group_narrow_kernel<E, true, kEpiPlain, false>), grid, block, 0, s, q);
-    else hipLaunchKernelGGL((group_narrow_kernel<E, false, kEpiPlain, false>), grid, block, 0, s, q);
-    MXMOE_HIP(hipGetLastError());
-    return MOE_OK;
-  }
-  if (j.epi == kEpiGate && j.gather) hipLaunchKernelGGL((group_tile_kernel<E, false, kEpiGate, true>), grid, block, 0, s, q);
-  else if (j.epi == kEpiGate) hipLaunchKernelGGL((group_tile_kernel<E, false, kEpiGate, false>), grid, block, 0, s, q);
-  else if (j.epi == kEpiGateGrad) hipLaunchKernelGGL((group_tile_kernel<E, true, kEpiGateGrad, false>), grid, block, 0, s, q);
-  else if (j.tb) hipLaunchKernelGGL((group_tile_kernel<E, true, kEpiPlain, false>), grid, block, 0, s, q);
-  else hipLaunchKernelGGL((group_tile_kernel<E, false, kEpiPlain, false>), grid, block, 0, s, q);
+  const dim3 grid((unsigned)unit_bound(g, j)), block(256);
+#define MXMOE_LAUNCH(TB, EPI, GATHER)                                                                      \
+  if (g.whole == 256) hipLaunchKernelGGL((group_tile_kernel<E, true, TB, EPI, GATHER>), grid, block, 0, s, q); \
+  else hipLaunchKernelGGL((group_tile_kernel<E, false, TB, EPI, GATHER>), grid, block, 0, s, q)
+  if (j.epi == kEpiGate && j.gather) { MXMOE_LAUNCH(false, kEpiGate, true); }
+  else if (j.epi == kEpiGate) { MXMOE_LAUNCH(false, kEpiGate, false); }
+  else if (j.epi == kEpiGateGrad) { MXMOE_LAUNCH(true, kEpiGateGrad, false); }
+  else { MXMOE_LAUNCH(false, kEpiPlain, false); }
+#undef MXMOE_LAUNCH
   MXMOE_HIP(hipGetLastError());
   return MOE_OK;
 }
@@ -445,19 +456,28 @@ moe_status launch_group(const Group& g, const DenseJob& j, int64_t b_step, hipSt
                                    : launch_group_typed<_Float16>(g, j, b_step, s);
 }
 
+// dx, dw1 and dw2; null pointers of c where one is not asked for.
 template <typename E>
-moe_status launch_grad_typed(const Group& g, const DenseJob& j, hipStream_t s) {
-  const GroupJob q{j, nullptr, 0, 0};
-  auto tiles = [&](int n) { return (int64_t)g.E * ((j.M + n - 1) / n) * ((j.N + n - 1) / n); };
-  if (tiles(256) >= 512)   // (315 tiles of 256 x 256 and short K: 150 us the whole training step, in tiles of 128 x 128 134)
-    hipLaunchKernelGGL((group_grad_kernel<E, 4>), dim3((unsigned)tiles(256)), dim3(256), 0, s, q, g.offsets, g.E, g.rows);
-  else
-    hipLaunchKernelGGL((group_grad_kernel<E, 2>), dim3((unsigned)tiles(128)), dim3(256), 0, s, q, g.offsets, g.E, g.rows);
+moe_status launch_back_typed(const Group& g, const DenseJob& dx, int64_t dx_step, const DenseJob& dw1, const DenseJob& dw2,
+                             hipStream_t s) {
+  auto tiles = [&](const DenseJob& j, int n) {
+    return j.c ? (int64_t)g.E * ((j.M + n - 1) / n) * ((j.N + n - 1) / n) : 0;
+  };
+  // (315 and 189 tiles of 256 x 256 and short K: 150 us the whole training step, in tiles of 128 x 128 134)
+  const bool wide = g.whole == 256, big = wide && tiles(dw1, 256) + tiles(dw2, 256) >= 512;
+  BackJobs q{{dx, g.plan, tile_cap(g.rows, g.E), dx_step}, {{dw1, nullptr, 0, 0}, {dw2, nullptr, 0, 0}}, dx.c != nullptr, {}};
+  int64_t blocks = q.has_dx ? unit_bound(g, dx) : 0;
+  for (int i = 0; i < 2; ++i) {
+    q.units[i] = (int)tiles(q.dw[i].job, big ? 256 : 128);
+    blocks += (q.units[i] + 7) / 8 * 8;
+  }
+  if (blocks == 0) return MOE_OK;
+  const dim3 grid((unsigned)blocks), block(256);
+  if (big) hipLaunchKernelGGL((group_back_kernel<E, true, 4>), grid, block, 0, s, q, g.offsets, g.rows);
+  else if (wide) hipLaunchKernelGGL((group_back_kernel<E, true, 2>), grid, block, 0, s, q, g.offsets, g.rows);
+  else hipLaunchKernelGGL((group_back_kernel<E, false, 2>), grid, block, 0, s, q, g.offsets, g.rows);
   MXMOE_HIP(hipGetLastError());
   return MOE_OK;
-}
-moe_status launch_grad(const Group& g, const DenseJob& j, hipStream_t s) {
-  return j.dtype == MOE_FLOAT_BF16 ? launch_grad_typed<__bf16>(g, j, s) : launch_grad_typed<_Float16>(g, j, s);
 }
 
 // ---- checks and workspaces -------------------------------------------------
@@ -469,7 +489,7 @@ moe_status check_experts(const char* what, int rows, int H, int I, int E, int la
   const int64_t wide = std::max(H, 2 * I);
   if (((int64_t)rows / 64 + std::min(E, rows) + 1) * ((wide + 63) / 64) >= 1 << 24)
     return fail(MOE_ERR_SHAPE, "%s: %d rows of %lld are too many for one launch", what, rows, (long long)wide);
-  if ((int64_t)E * ((H + 63) / 64) * ((2 * I + 63) / 64) >= 1ll << 26)
+  if ((int64_t)E * ((H + 63) / 64) * ((2 * I + 63) / 64) >= 1 << 24)
     return fail(MOE_ERR_SHAPE, "%s: %d experts of %d x %d are too many for one launch", what, E, 2 * I, H);
   if (layout != MOE_EPI_SWIGLU_SPLIT && layout != MOE_EPI_SWIGLU_INTERLEAVED)
     return fail(MOE_ERR_INVALID_ARG, "%s: layout %d must be a SWIGLU epilogue", what, layout);
@@ -670,14 +690,47 @@ moe_status moe_expert_ffn_backward(const moe_expert_ffn_grad_args* a, void* stre
   }
   j.epi = kEpiPlain;
   j.gu = j.h = nullptr;
+  DenseJob dx{}, dw1{}, dw2{};
   if (a->dx && any) {
-    j.a = ws + w.dgu, j.lda = 2 * I;
-    j.b = a->w1, j.ldb = H, j.tb = 1;
-    j.N = a->H, j.K = 2 * a->I;
-    if (gathered) j.c = ws + w.dx, j.ldc = H, j.c_dtype = MOE_FLOAT_FP32;
-    else j.c = a->dx, j.ldc = a->dx_stride, j.c_dtype = a->dx_dtype;
-    MXMOE_TRY(launch_group(g, j, 2 * I * H, s));
+    dx = j;
+    dx.a = ws + w.dgu, dx.lda = 2 * I;
+    dx.b = a->w1, dx.ldb = H, dx.tb = 1;
+    dx.N = a->H, dx.K = 2 * a->I;
+    if (gathered) dx.c = ws + w.dx, dx.ldc = H, dx.c_dtype = MOE_FLOAT_FP32;
+    else dx.c = a->dx, dx.ldc = a->dx_stride, dx.c_dtype = a->dx_dtype;
   }
+  // the weights' gradients sum over the expert's rows
+  j.ta = j.tb = 1;
+  j.c_dtype = a->dw_dtype;
+  const bool sums = any || !a->accumulate;
+  if (a->dw1 && sums) {
+    dw1 = j;
+    dw1.a = ws + w.dgu, dw1.lda = 2 * I;
+    dw1.b = a->x, dw1.ldb = a->x_stride;
+    if (gathered && any) {
+      DenseJob q{};
+      q.a = a->x, q.lda = a->x_stride, q.K = a->H;
+      q.gather = a->gather, q.gather_div = a->gather_div, q.gather_rows = a->tokens;
+      hipLaunchKernelGGL((gather_rows_kernel<_Float16>), dim3((unsigned)std::min<int64_t>(rows, 1 << 20)), dim3(256), 0, s,
+                         q, a->expert_offsets, a->E, a->rows, ws + w.x);   // (any 16 bits)
+      MXMOE_HIP(hipGetLastError());
+      dw1.b = ws + w.x, dw1.ldb = H;
+    }
+    dw1.M = 2 * a->I, dw1.N = a->H;
+    dw1.c = a->dw1, dw1.ldc = H;
+    dw1.add = a->accumulate ? a->dw1 : nullptr, dw1.ldadd = H;
+  }
+  if (a->dw2 && sums) {
+    dw2 = j;
+    dw2.a = a->dout, dw2.lda = a->dout_stride;
+    dw2.b = ws + w.h, dw2.ldb = I;
+    dw2.M = a->H, dw2.N = a->I;
+    dw2.c = a->dw2, dw2.ldc = I;
+    dw2.add = a->accumulate ? a->dw2 : nullptr, dw2.ldadd = I;
+  }
+  const int64_t dx_step = 2 * I * H;
+  MXMOE_TRY(a->dtype == MOE_FLOAT_BF16 ? launch_back_typed<__bf16>(g, dx, dx_step, dw1, dw2, s)
+                                       : launch_back_typed<_Float16>(g, dx, dx_step, dw1, dw2, s));
   if (a->dx && gathered && x_rows > 0) {
     const dim3 grid((unsigned)x_rows), block(std::min(512, (a->H / 8 + 63) / 64 * 64));
     const float* const dxr = reinterpret_cast<const float*>(ws + w.dx);
@@ -688,35 +741,6 @@ moe_status moe_expert_ffn_backward(const moe_expert_ffn_grad_args* a, void* stre
       hipLaunchKernelGGL((sum_rows_kernel<_Float16>), grid, block, 0, s, dxr, a->dest_row, a->expert_offsets, a->E,
                          a->rows, a->gather_div, a->H, a->dx, a->dx_dtype, a->dx_stride);
     MXMOE_HIP(hipGetLastError());
-  }
-  // the weights' gradients sum over the expert's rows
-  if (!any && a->accumulate) return MOE_OK;
-  j.ta = j.tb = 1;
-  j.c_dtype = a->dw_dtype;
-  if (a->dw1) {
-    j.a = ws + w.dgu, j.lda = 2 * I;
-    j.b = a->x, j.ldb = a->x_stride;
-    if (gathered && any) {
-      DenseJob q{};
-      q.a = a->x, q.lda = a->x_stride, q.K = a->H;
-      q.gather = a->gather, q.gather_div = a->gather_div, q.gather_rows = a->tokens;
-      hipLaunchKernelGGL((gather_rows_kernel<_Float16>), dim3((unsigned)std::min<int64_t>(rows, 1 << 20)), dim3(256), 0, s, q, a->expert_offsets,
-                         a->E, a->rows, ws + w.x);   // (any 16 bits)
-      MXMOE_HIP(hipGetLastError());
-      j.b = ws + w.x, j.ldb = H;
-    }
-    j.M = 2 * a->I, j.N = a->H;
-    j.c = a->dw1, j.ldc = H;
-    j.add = a->accumulate ? a->dw1 : nullptr, j.ldadd = H;
-    MXMOE_TRY(launch_grad(g, j, s));
-  }
-  if (a->dw2) {
-    j.a = a->dout, j.lda = a->dout_stride;
-    j.b = ws + w.h, j.ldb = I;
-    j.M = a->H, j.N = a->I;
-    j.c = a->dw2, j.ldc = I;
-    j.add = a->accumulate ? a->dw2 : nullptr, j.ldadd = I;
-    MXMOE_TRY(launch_grad(g, j, s));
   }
   return MOE_OK;
 }

@@ -148,7 +148,7 @@ def test_route_backward_refusals(kw, status, needle):
 
 def test_norm_workspace_query():
     q = mx.lib.moe_rms_norm_grad_workspace_size
-    assert q(4, 64) >= 4 * 64 * 4 and q(1 << 20, 7168) == q(1 << 21, 7168)
+    assert q(4, 64) >= 64 * 4 and q(4, 7168) >= 4 * 7168 * 4 and q(1 << 20, 7168) == q(1 << 21, 7168)
     assert q(-1, 64) == q(4, 0) == q(1 << 22, 64) == q(4, 40000) == 0
 
 
