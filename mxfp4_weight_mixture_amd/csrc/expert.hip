@@ -408,16 +408,23 @@ moe_status launch_few(const Group& g, const DenseJob& j, int64_t b_step, hipStre
   return MOE_OK;
 }
 
-// Tiles of 256 columns read the least for their products, but need many of them:
-// narrow ones where, with the rows spread evenly, they would leave a third of
-// the CUs idle (us, wide / narrow: 8 experts of 4096 x 2048, 1024 rows 172 / 135, 2048
-// rows 182 / 207; 16 of 1096 x 776, 1024 rows 48 / 36; 8 of 7168 x 3584, 512 rows, 224
-// tiles, 231 / 276), and where the weights' stream is what counts (256 of 4096 x 2048,
-// 384 rows 1724 / 1685, 6144 rows 2252 / 2224, 24576 rows 2384 / 2993).
+// Tiles of 256 columns read the least for their products, but need many of them and
+// long sums: narrow ones where, with the rows spread evenly, they would leave a
+// third of the CUs idle, where the weights' stream is what counts, and where short
+// sums leave the tiles' ends much of the time, which two blocks a CU hide.  Us,
+// wide / narrow:
+//   8 experts of 4096 x 2048    1024 rows 181 / 137, 2048 rows 193 / 203
+//   24 of 1096 x 776            384 rows 46 / 40, 3000 rows 97 / 79
+//   8 of 7168 x 3584            512 rows (224 tiles) 235 / 276
+//   256 of 4096 x 2048          384 rows 1724 / 1685, 6144 rows 2245 / 2215, 24576 rows 2418 / 2845
+//   32 of 2048 x 1024           2048 rows 114 / 104, 4096 rows 148 / 140
+//   64 of 2048 x 1024           6144 rows 219 / 206, 12288 rows 301 / 326
+// (128 x 256 tiles of 32-deep stages, two blocks a CU, lie between the two.)
 int whole_tile(int rows, int E, int H, int I) {
   const int n = std::max(std::min(E, rows), 1), each = (rows + n - 1) / n;
   const int64_t columns = ((H + 255) / 256 + (I + 127) / 128) / 2;   // of the two products, on average
-  return each <= 32 || n * ((each + 255) / 256) * columns <= 176 ? 128 : 256;
+  const bool idle = n * ((each + 255) / 256) * columns <= 176, brief = H + I < 4096 && each <= 128;
+  return each <= 32 || idle || brief ? 128 : 256;
 }
 
 moe_status launch_plan(const Group& g, hipStream_t s) {
