@@ -151,7 +151,7 @@ __device__ __forceinline__ F8 get_sum8(const char* areas, int area_bytes, int ro
 constexpr int split_k_lds(int BK) { return BK == 32 ? 64 << 10 : 128 << 10; }
 
 // The C tile of 64 rows from m0 and the nt-th 64 columns of B.
-template <typename E, bool TA, bool TB, int EPI, bool LORA, int BK>
+template <typename E, bool TA, bool TB, int EPI, bool LORA, int BK, bool GATHER = false>
 __device__ __forceinline__ void split_k_tile(const DenseJob& p, int m0, int nt, char* lds) {
   constexpr int NST = 2;
   using A = Operand<E, 64, TA, 1, BK>;
@@ -165,7 +165,8 @@ __device__ __forceinline__ void split_k_tile(const DenseJob& p, int m0, int nt, 
 
   A a;
   B b;
-  a.init(p.a, p.lda, p.M, m0, 0, lane);
+  if constexpr (GATHER) a.init_gather(p, m0, 0, lane);
+  else a.init(p.a, p.lda, p.M, m0, 0, lane);
   if constexpr (EPI == kEpiGate) b.init_gate(p, nt, 0, lane);
   else b.init(p.b, p.ldb, p.N, n0, 0, lane);
   v16f acc[2][2];

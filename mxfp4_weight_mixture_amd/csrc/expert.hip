@@ -15,6 +15,7 @@
 #include <algorithm>
 
 #include "dense_few.h"
+#include "dense_small.h"
 #include "dense_tile.h"
 
 namespace mxmoe {
@@ -40,7 +41,7 @@ struct RowPlan {
   }
 };
 // Row tiles that the rows can make at most, in any class.
-int tile_cap(int rows, int E) { return rows / 128 + std::min(E, rows) + 1; }
+int tile_cap(int rows, int E) { return rows / 64 + std::min(E, rows) + 1; }
 size_t plan_bytes(int rows, int E) {
   return align_up(sizeof(RowPlan) + (size_t)kClasses * tile_cap(rows, E) * sizeof(RowTile), 256);
 }
@@ -175,13 +176,16 @@ __device__ __forceinline__ int up8(int v) { return (v + 7) & ~7; }
 // Wide: tiles of 256 columns (128 gate and 128 up ones).  Tiles of 256 rows go in
 // groups that share an expert's weights in the L2; the other classes have one tile
 // an expert, whose rows stay in the L2 while all its columns pass.
-// Narrow: tiles of up to 128 rows and 128 columns, two blocks per CU.
+// Narrow: tiles of up to 128 rows and 128 columns, two blocks per CU.  Split: 64 x 64
+// tiles whose waves split K, two blocks per CU.
 constexpr int kNarrowLds = 72 << 10;
-template <typename E, bool WIDE, bool TB, int EPI, bool GATHER>
+enum Shape { kWide, kNarrow, kSplit };
+template <typename E, int SHAPE, bool TB, int EPI, bool GATHER>
 __device__ __forceinline__ int product_unit(const GroupJob& g, int b, char* lds) {
-  const int cols = (WIDE ? 256 : 128) >> (EPI == kEpiGate ? 1 : 0), width = EPI == kEpiGate ? g.job.N >> 1 : g.job.N;
-  const int nts = (width + cols - 1) / cols;
-  const int n0 = WIDE ? g.plan->count[0] : 0, n1 = g.plan->count[1], n2 = g.plan->count[2];
+  constexpr bool WIDE = SHAPE == kWide;
+  const int cols = (WIDE ? 256 : SHAPE == kNarrow ? 128 : 64) >> (EPI == kEpiGate ? 1 : 0);
+  const int width = EPI == kEpiGate ? g.job.N >> 1 : g.job.N, nts = (width + cols - 1) / cols;
+  const int n0 = WIDE ? g.plan->count[0] : 0, n1 = SHAPE != kSplit ? g.plan->count[1] : 0, n2 = g.plan->count[2];
   int nt;
   if constexpr (WIDE) {
     if (b < up8(n0 * nts)) {
@@ -192,33 +196,43 @@ __device__ __forceinline__ int product_unit(const GroupJob& g, int b, char* lds)
     }
     b -= up8(n0 * nts);
   }
-  if (b < up8(n1 * nts)) {
-    if (b >= n1 * nts) return -1;
-    const int t = xcd_run(b, n1 * nts);
-    if constexpr (WIDE) {
-      const DenseJob p = tile_job(g, g.plan->list(1, g.cap)[t / nts]);
-      dense_tile<E, false, TB, EPI, false, 2, 4, 3, 64, GATHER>(p, 0, t % nts, lds);
-    } else {
-      const DenseJob p = tile_job(g, unit_at(g, 1, t, nts, &nt));
-      dense_tile<E, false, TB, EPI, false, 2, 2, 4, 32, GATHER>(p, 0, nt, lds);
+  if constexpr (SHAPE == kSplit) {
+    if (b < up8(n2 * nts)) {
+      if (b >= n2 * nts) return -1;
+      const DenseJob p = tile_job(g, unit_at(g, 2, xcd_run(b, n2 * nts), nts, &nt));
+      split_k_tile<E, false, TB, EPI, false, 32, GATHER>(p, 0, nt, lds);
+      return -1;
     }
-    return -1;
+    return b - up8(n2 * nts);
+  } else {
+    if (b < up8(n1 * nts)) {
+      if (b >= n1 * nts) return -1;
+      const int t = xcd_run(b, n1 * nts);
+      if constexpr (WIDE) {
+        const DenseJob p = tile_job(g, g.plan->list(1, g.cap)[t / nts]);
+        dense_tile<E, false, TB, EPI, false, 2, 4, 3, 64, GATHER>(p, 0, t % nts, lds);
+      } else {
+        const DenseJob p = tile_job(g, unit_at(g, 1, t, nts, &nt));
+        dense_tile<E, false, TB, EPI, false, 2, 2, 4, 32, GATHER>(p, 0, nt, lds);
+      }
+      return -1;
+    }
+    b -= up8(n1 * nts);
+    if (b < up8(n2 * nts)) {
+      if (b >= n2 * nts) return -1;
+      const int t = xcd_run(b, n2 * nts);
+      const DenseJob p = tile_job(g, g.plan->list(2, g.cap)[t / nts]);
+      dense_tile<E, false, TB, EPI, false, 1, WIDE ? 4 : 2, 3, 64, GATHER>(p, 0, t % nts, lds);
+      return -1;
+    }
+    return b - up8(n2 * nts);
   }
-  b -= up8(n1 * nts);
-  if (b < up8(n2 * nts)) {
-    if (b >= n2 * nts) return -1;
-    const int t = xcd_run(b, n2 * nts);
-    const DenseJob p = tile_job(g, g.plan->list(2, g.cap)[t / nts]);
-    dense_tile<E, false, TB, EPI, false, 1, WIDE ? 4 : 2, 3, 64, GATHER>(p, 0, t % nts, lds);
-    return -1;
-  }
-  return b - up8(n2 * nts);
 }
 
-template <typename E, bool WIDE, bool TB, int EPI, bool GATHER>
-__global__ __launch_bounds__(256, WIDE ? 1 : 2) void group_tile_kernel(GroupJob g) {
-  __shared__ __attribute__((aligned(1024))) char lds[WIDE ? kTileLds : kNarrowLds];
-  product_unit<E, WIDE, TB, EPI, GATHER>(g, blockIdx.x, lds);
+template <typename E, int SHAPE, bool TB, int EPI, bool GATHER>
+__global__ __launch_bounds__(256, SHAPE == kWide ? 1 : 2) void group_tile_kernel(GroupJob g) {
+  __shared__ __attribute__((aligned(1024))) char lds[SHAPE == kWide ? kTileLds : kNarrowLds];
+  product_unit<E, SHAPE, TB, EPI, GATHER>(g, blockIdx.x, lds);
 }
 
 // Row tile y of all experts' in order, found from the offsets by every wave for
@@ -314,16 +328,16 @@ struct BackJobs {
   GroupJob dx, dw[2];
   int has_dx, units[2];   // tiles of dw1 and dw2
 };
-template <typename E, bool WIDE, int F>
-__global__ __launch_bounds__(256, WIDE ? 1 : 2) void group_back_kernel(BackJobs j, const int32_t* offsets, int rows) {
-  __shared__ __attribute__((aligned(1024))) char lds[WIDE ? kTileLds : kNarrowLds];
+template <typename E, int SHAPE, int F>
+__global__ __launch_bounds__(256, SHAPE == kWide ? 1 : 2) void group_back_kernel(BackJobs j, const int32_t* offsets, int rows) {
+  __shared__ __attribute__((aligned(1024))) char lds[SHAPE == kWide ? kTileLds : kNarrowLds];
   int b = blockIdx.x;
-  if (j.has_dx) b = product_unit<E, WIDE, true, kEpiPlain, false>(j.dx, b, lds);
+  if (j.has_dx) b = product_unit<E, SHAPE, true, kEpiPlain, false>(j.dx, b, lds);
   if (b < 0) return;
   const int second = b >= up8(j.units[0]);
   if (second) b -= up8(j.units[0]);
   if (b >= j.units[second]) return;
-  grad_unit<E, WIDE, F>(j.dw[second], offsets, rows, xcd_run(b, j.units[second]), lds);
+  grad_unit<E, SHAPE == kWide, F>(j.dw[second], offsets, rows, xcd_run(b, j.units[second]), lds);
 }
 
 // x's rows in expert order (the weight gradient's products take no gather).
@@ -376,7 +390,8 @@ struct Group {
   int rows, E;
   const int32_t* offsets;
   RowPlan* plan;
-  int whole;  // rows of a whole row tile: 256, or 128 for narrow tiles
+  int shape;  // Shape of the tiles
+  int whole() const { return shape == kWide ? 256 : shape == kNarrow ? 128 : 64; }   // its rows and columns
   int most;   // rows that an expert has at most where a token goes to it once
 };
 
@@ -420,16 +435,22 @@ moe_status launch_few(const Group& g, const DenseJob& j, int64_t b_step, hipStre
 //   32 of 2048 x 1024           2048 rows 114 / 104, 4096 rows 148 / 140
 //   64 of 2048 x 1024           6144 rows 219 / 206, 12288 rows 301 / 326
 // (128 x 256 tiles of 32-deep stages, two blocks a CU, lie between the two.)
-int whole_tile(int rows, int E, int H, int I) {
+// Where even narrow tiles are fewer than the CUs' room for them, a block's time is
+// its K loop's latency: 64 x 64 tiles whose four waves split K (narrow / split: 9
+// experts of 1096 x 776, 512 rows 36 / 23, 1034 rows 38 / 31, 2048 rows 40 / 45; 24 of
+// them, 1000 rows, 504 tiles, 50 / 58).
+int tile_shape(int rows, int E, int H, int I) {
   const int n = std::max(std::min(E, rows), 1), each = (rows + n - 1) / n;
-  const int64_t columns = ((H + 255) / 256 + (I + 127) / 128) / 2;   // of the two products, on average
+  // columns: of the two products, on average
+  if (n * ((each + 63) / 64) * (((H + 63) / 64 + (I + 31) / 32) / 2) <= 400) return kSplit;
+  const int64_t columns = ((H + 255) / 256 + (I + 127) / 128) / 2;
   const bool idle = n * ((each + 255) / 256) * columns <= 176, brief = H + I < 4096 && each <= 128;
-  return each <= 32 || idle || brief ? 128 : 256;
+  return each <= 32 || idle || brief ? kNarrow : kWide;
 }
 
 moe_status launch_plan(const Group& g, hipStream_t s) {
   const dim3 block(std::min(1024, (g.E + 63) / 64 * 64));
-  hipLaunchKernelGGL(plan_rows_kernel, dim3(1), block, 0, s, g.offsets, g.E, g.rows, g.whole,
+  hipLaunchKernelGGL(plan_rows_kernel, dim3(1), block, 0, s, g.offsets, g.E, g.rows, g.whole(),
                      tile_cap(g.rows, g.E), g.plan);
   MXMOE_HIP(hipGetLastError());
   return MOE_OK;
@@ -437,8 +458,8 @@ moe_status launch_plan(const Group& g, hipStream_t s) {
 
 // Blocks that a product's units can need.
 int64_t unit_bound(const Group& g, const DenseJob& j) {
-  const int cols = j.epi == kEpiGate ? g.whole / 2 : g.whole, width = j.epi == kEpiGate ? j.N / 2 : j.N;
-  return (int64_t)(g.rows / g.whole + std::min(g.E, g.rows)) * ((width + cols - 1) / cols) + 24;
+  const int cols = j.epi == kEpiGate ? g.whole() / 2 : g.whole(), width = j.epi == kEpiGate ? j.N / 2 : j.N;
+  return (int64_t)(g.rows / g.whole() + std::min(g.E, g.rows)) * ((width + cols - 1) / cols) + 24;
 }
 
 template <typename E>
@@ -448,8 +469,9 @@ moe_status launch_group_typed(const Group& g, const DenseJob& j, int64_t b_step,
   const GroupJob q{j, g.plan, tile_cap(g.rows, g.E), b_step};
   const dim3 grid((unsigned)unit_bound(g, j)), block(256);
 #define MXMOE_LAUNCH(TB, EPI, GATHER)                                                                      \
-  if (g.whole == 256) hipLaunchKernelGGL((group_tile_kernel<E, true, TB, EPI, GATHER>), grid, block, 0, s, q); \
-  else hipLaunchKernelGGL((group_tile_kernel<E, false, TB, EPI, GATHER>), grid, block, 0, s, q)
+  if (g.shape == kWide) hipLaunchKernelGGL((group_tile_kernel<E, kWide, TB, EPI, GATHER>), grid, block, 0, s, q);         \
+  else if (g.shape == kNarrow) hipLaunchKernelGGL((group_tile_kernel<E, kNarrow, TB, EPI, GATHER>), grid, block, 0, s, q); \
+  else hipLaunchKernelGGL((group_tile_kernel<E, kSplit, TB, EPI, GATHER>), grid, block, 0, s, q)
   if (j.epi == kEpiGate && j.gather) { MXMOE_LAUNCH(false, kEpiGate, true); }
   else if (j.epi == kEpiGate) { MXMOE_LAUNCH(false, kEpiGate, false); }
   else if (j.epi == kEpiGateGrad) { MXMOE_LAUNCH(true, kEpiGateGrad, false); }
@@ -471,7 +493,7 @@ moe_status launch_back_typed(const Group& g, const DenseJob& dx, int64_t dx_step
     return j.c ? (int64_t)g.E * ((j.M + n - 1) / n) * ((j.N + n - 1) / n) : 0;
   };
   // (315 and 189 tiles of 256 x 256 and short K: 150 us the whole training step, in tiles of 128 x 128 134)
-  const bool wide = g.whole == 256, big = wide && tiles(dw1, 256) + tiles(dw2, 256) >= 512;
+  const bool wide = g.shape == kWide, big = wide && tiles(dw1, 256) + tiles(dw2, 256) >= 512;
   BackJobs q{{dx, g.plan, tile_cap(g.rows, g.E), dx_step}, {{dw1, nullptr, 0, 0}, {dw2, nullptr, 0, 0}}, dx.c != nullptr, {}};
   int64_t blocks = q.has_dx ? unit_bound(g, dx) : 0;
   for (int i = 0; i < 2; ++i) {
@@ -480,9 +502,11 @@ moe_status launch_back_typed(const Group& g, const DenseJob& dx, int64_t dx_step
   }
   if (blocks == 0) return MOE_OK;
   const dim3 grid((unsigned)blocks), block(256);
-  if (big) hipLaunchKernelGGL((group_back_kernel<E, true, 4>), grid, block, 0, s, q, g.offsets, g.rows);
-  else if (wide) hipLaunchKernelGGL((group_back_kernel<E, true, 2>), grid, block, 0, s, q, g.offsets, g.rows);
-  else hipLaunchKernelGGL((group_back_kernel<E, false, 2>), grid, block, 0, s, q, g.offsets, g.rows);
+  if (big) hipLaunchKernelGGL((group_back_kernel<E, kWide, 4>), grid, block, 0, s, q, g.offsets, g.rows);
+  else if (wide) hipLaunchKernelGGL((group_back_kernel<E, kWide, 2>), grid, block, 0, s, q, g.offsets, g.rows);
+  else if (g.shape == kNarrow)
+    hipLaunchKernelGGL((group_back_kernel<E, kNarrow, 2>), grid, block, 0, s, q, g.offsets, g.rows);
+  else hipLaunchKernelGGL((group_back_kernel<E, kSplit, 2>), grid, block, 0, s, q, g.offsets, g.rows);
   MXMOE_HIP(hipGetLastError());
   return MOE_OK;
 }
@@ -596,7 +620,7 @@ moe_status moe_expert_ffn_forward(const moe_expert_ffn_args* a, void* stream) {
   const hipStream_t s = (hipStream_t)stream;
   uint8_t* const ws = static_cast<uint8_t*>(a->workspace);
   const Group g{a->rows, a->E, a->expert_offsets, reinterpret_cast<RowPlan*>(ws),
-                whole_tile(a->rows, a->E, a->H, a->I), gathered ? std::min(a->rows, a->tokens) : a->rows};
+                tile_shape(a->rows, a->E, a->H, a->I), gathered ? std::min(a->rows, a->tokens) : a->rows};
 
   DenseJob j{};
   j.dtype = a->dtype;
@@ -676,7 +700,7 @@ moe_status moe_expert_ffn_backward(const moe_expert_ffn_grad_args* a, void* stre
   const hipStream_t s = (hipStream_t)stream;
   uint8_t* const ws = static_cast<uint8_t*>(a->workspace);
   const Group g{a->rows, a->E, a->expert_offsets, reinterpret_cast<RowPlan*>(ws),
-                whole_tile(a->rows, a->E, a->H, a->I), a->rows};
+                tile_shape(a->rows, a->E, a->H, a->I), a->rows};
 
   DenseJob j{};
   j.dtype = a->dtype;
