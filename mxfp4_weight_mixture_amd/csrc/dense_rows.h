@@ -111,7 +111,7 @@ __device__ __forceinline__ void finish_plain(const DenseJob& p, int m, int n, F8
 // product's matrix instructions take.  Two parts of it, as the adapters' small
 // rows have, would double that product, a third of the block's work, for an
 // error of the output 0.7 times as large.
-template <typename E, bool KEEP = true>
+template <typename E>
 __device__ __forceinline__ void finish_gate(const DenseJob& p, int m, int i, F8 g, F8 u) {
   const int I = p.N >> 1;
   if (i + 8 > I) {
@@ -133,7 +133,7 @@ __device__ __forceinline__ void finish_gate(const DenseJob& p, int m, int i, F8 
 #pragma unroll
     for (int e = 0; e < 8; ++e) g.v[e] += a.v[e], u.v[e] += b.v[e];
   }
-  if (KEEP && p.gu) store_pair<E>(p.gu, p.gu_dtype, (size_t)m * p.N, I, i, p.interleaved, g, u);
+  if (p.gu) store_pair<E>(p.gu, p.gu_dtype, (size_t)m * p.N, I, i, p.interleaved, g, u);
   F8 h;
 #pragma unroll
   for (int e = 0; e < 8; ++e) h.v[e] = gate_act(p.act, g.v[e]) * u.v[e];

@@ -450,31 +450,7 @@ __device__ __forceinline__ void dense_tile(const DenseJob& p, int m0, int nt, ch
       const v4f y = *reinterpret_cast<const v4f*>(st + row * PITCH + (((c + 1) ^ (row & (CH - 1))) << 4));
       return F8{{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]}};
     };
-    // fp32 outputs of the sums themselves
-    const bool rows32 = !p.partial && !p.add && (EPI == kEpiGate ? p.gu && p.gu_dtype == MOE_FLOAT_FP32
-                                                                 : EPI == kEpiPlain && p.c_dtype == MOE_FLOAT_FP32);
     if constexpr (EPI == kEpiGate) {
-      if (rows32) {
-        // gate_up, four columns a lane: a store fills whole lines
-        float* const gu = static_cast<float*>(p.gu);
-#pragma unroll
-        for (int it = 0; it < 32 * CH / 64; ++it) {
-          const int row = it * (64 / CH) + lane / CH, x = lane % CH, blk = x >> 4;
-          const size_t at = (size_t)(r0 + row) * p.N;
-          if (!p.interleaved) {
-            const int i = nt * (BN / 2) + (wn >> 1) + blk * 32 + (x & 7) * 4;
-            const v4f v = *reinterpret_cast<const v4f*>(st + row * PITCH + ((x ^ (row & (CH - 1))) << 4));
-            if (r0 + row < p.M && i < width) *reinterpret_cast<v4f*>(gu + at + (x & 8 ? width : 0) + i) = v;
-          } else {
-            // two gate values and the two up ones, 32 columns behind
-            typedef float v2f __attribute__((ext_vector_type(2)));
-            const int i = nt * (BN / 2) + (wn >> 1) + blk * 32 + (x & 15) * 2, c = blk * 16 + ((x & 15) >> 1);
-            const v2f a = *reinterpret_cast<const v2f*>(st + row * PITCH + ((c ^ (row & (CH - 1))) << 4) + (x & 1) * 8);
-            const v2f b = *reinterpret_cast<const v2f*>(st + row * PITCH + (((c + 8) ^ (row & (CH - 1))) << 4) + (x & 1) * 8);
-            if (r0 + row < p.M && i < width) *reinterpret_cast<v4f*>(gu + at + 2 * i) = v4f{a[0], b[0], a[1], b[1]};
-          }
-        }
-      }
       constexpr int LPR = FN * 32 / 16;       // lanes per row: eight gate indices each
 #pragma unroll
       for (int it = 0; it < 32 * LPR / 64; ++it) {
@@ -482,19 +458,7 @@ __device__ __forceinline__ void dense_tile(const DenseJob& p, int m0, int nt, ch
         const int blk = x >> 2, c = blk * 16 + (x & 3) * 2;       // 64-column block: gate, then up
         const int i = nt * (BN / 2) + (wn >> 1) + blk * 32 + (x & 3) * 8;
         const F8 gt = staged8(row, c), up = staged8(row, c + 8);
-        if (r0 + row < p.M && i < width) {
-          if (rows32) finish_gate<E, false>(p, r0 + row, i, gt, up);
-          else finish_gate<E>(p, r0 + row, i, gt, up);
-        }
-      }
-    } else if (rows32) {
-      // four columns a lane: a store fills whole lines
-#pragma unroll
-      for (int it = 0; it < 32 * CH / 64; ++it) {
-        const int row = it * (64 / CH) + lane / CH, c = lane % CH, n = nt * BN + wn + c * 4;
-        const v4f v = *reinterpret_cast<const v4f*>(st + row * PITCH + ((c ^ (row & (CH - 1))) << 4));
-        if (r0 + row < p.M && n < width)
-          *reinterpret_cast<v4f*>(static_cast<float*>(p.c) + (size_t)(r0 + row) * p.ldc + n) = v;
+        if (r0 + row < p.M && i < width) finish_gate<E>(p, r0 + row, i, gt, up);
       }
     } else {
       constexpr int LPR = FN * 32 / 8;
