@@ -11,8 +11,7 @@
 // rows, 65 to 128, up to 64).  Every product of the call then takes its tiles from
 // that list, the large ones first; the grid is what the rows could need at most,
 // and blocks past the list's end return.  Few rows need no list.  A weight gradient
-// has the same tiles for every expert and the expert's rows as its K; dx, dw1 and
-// dw2 go in one launch.
+// has the same tiles for every expert and the expert's rows as its K.
 //
 // What bounds it: with a few rows an expert the reading of its weights (192 rows
 // over 256 experts of 4096 x 2048: 1.08 ms, 6.2 TB/s); with many the dense tiles'
@@ -329,8 +328,8 @@ __device__ __forceinline__ void grad_unit(const GroupJob& g, const int32_t* offs
   else dense_tile<E, true, true, kEpiPlain, false, 2, 2, 4, 32>(p, mt * TILE, nt, lds);
 }
 
-// dx's rows, dw1 and dw2 in one launch: they need nothing of each other, and the
-// weight gradients' short tiles fill what dx's last ones leave idle.
+// dx's rows, dw1 and dw2, which need nothing of each other: those of one launch (or
+// one of them alone), the weight gradients' tiles behind dx's.
 struct BackJobs {
   GroupJob dx, dw[2];
   int has_dx, units[2];   // tiles of dw1 and dw2
@@ -492,7 +491,11 @@ moe_status launch_group(const Group& g, const DenseJob& j, int64_t b_step, hipSt
                                    : launch_group_typed<_Float16>(g, j, b_step, s);
 }
 
-// dx, dw1 and dw2; null pointers of c where one is not asked for.
+// dx, dw1 and dw2; null pointers of c where one is not asked for.  In one launch
+// where they are small: 1034 rows over 9 experts of 1096 x 776, the whole training step
+// 142 -> 122 us.  Wide tiles one after the other: side by side they lose more of what
+// they share in the L2 than their ends leave idle (49152 rows, 32 experts of 4096 x
+// 2048: 4071 us together, 3905 in turn, the best of 24).
 template <typename E>
 moe_status launch_back_typed(const Group& g, const DenseJob& dx, int64_t dx_step, const DenseJob& dw1, const DenseJob& dw2,
                              hipStream_t s) {
@@ -501,20 +504,23 @@ moe_status launch_back_typed(const Group& g, const DenseJob& dx, int64_t dx_step
   };
   // (315 and 189 tiles of 256 x 256 and short K: 150 us the whole training step, in tiles of 128 x 128 134)
   const bool wide = g.shape == kWide, big = wide && tiles(dw1, 256) + tiles(dw2, 256) >= 512;
-  BackJobs q{{dx, g.plan, tile_cap(g.rows, g.E), dx_step}, {{dw1, nullptr, 0, 0}, {dw2, nullptr, 0, 0}}, dx.c != nullptr, {}};
-  int64_t blocks = q.has_dx ? unit_bound(g, dx) : 0;
-  for (int i = 0; i < 2; ++i) {
-    q.units[i] = (int)tiles(q.dw[i].job, big ? 256 : 128);
-    blocks += (q.units[i] + 7) / 8 * 8;
+  for (int part = 0; part < (wide ? 3 : 1); ++part) {
+    BackJobs q{{dx, g.plan, tile_cap(g.rows, g.E), dx_step}, {{dw1, nullptr, 0, 0}, {dw2, nullptr, 0, 0}}, 0, {}};
+    q.has_dx = dx.c != nullptr && part == 0;
+    int64_t blocks = q.has_dx ? unit_bound(g, dx) : 0;
+    for (int i = 0; i < 2; ++i) {
+      q.units[i] = !wide || part == i + 1 ? (int)tiles(q.dw[i].job, big ? 256 : 128) : 0;
+      blocks += (q.units[i] + 7) / 8 * 8;
+    }
+    if (blocks == 0) continue;
+    const dim3 grid((unsigned)blocks), block(256);
+    if (big) hipLaunchKernelGGL((group_back_kernel<E, kWide, 4>), grid, block, 0, s, q, g.offsets, g.rows);
+    else if (wide) hipLaunchKernelGGL((group_back_kernel<E, kWide, 2>), grid, block, 0, s, q, g.offsets, g.rows);
+    else if (g.shape == kNarrow)
+      hipLaunchKernelGGL((group_back_kernel<E, kNarrow, 2>), grid, block, 0, s, q, g.offsets, g.rows);
+    else hipLaunchKernelGGL((group_back_kernel<E, kSplit, 2>), grid, block, 0, s, q, g.offsets, g.rows);
+    MXMOE_HIP(hipGetLastError());
   }
-  if (blocks == 0) return MOE_OK;
-  const dim3 grid((unsigned)blocks), block(256);
-  if (big) hipLaunchKernelGGL((group_back_kernel<E, kWide, 4>), grid, block, 0, s, q, g.offsets, g.rows);
-  else if (wide) hipLaunchKernelGGL((group_back_kernel<E, kWide, 2>), grid, block, 0, s, q, g.offsets, g.rows);
-  else if (g.shape == kNarrow)
-    hipLaunchKernelGGL((group_back_kernel<E, kNarrow, 2>), grid, block, 0, s, q, g.offsets, g.rows);
-  else hipLaunchKernelGGL((group_back_kernel<E, kSplit, 2>), grid, block, 0, s, q, g.offsets, g.rows);
-  MXMOE_HIP(hipGetLastError());
   return MOE_OK;
 }
 
