@@ -143,7 +143,7 @@ struct GroupJob {
 
 // The job of one row tile.  (What memory gives is the same for the whole block
 // but not to the compiler, which would keep the buffer resources' bases in vector
-// registers and read them back for every DMA: 1472 against 1340 us for 49152 x 4096
+// registers and read them back for every DMA: 1472 against 1363 us for 49152 x 4096
 // x 4096.)
 __device__ __forceinline__ DenseJob tile_job(const GroupJob& g, const RowTile& at) {
   const RowTile t{__builtin_amdgcn_readfirstlane(at.expert), __builtin_amdgcn_readfirstlane(at.row),
@@ -290,11 +290,11 @@ __device__ __forceinline__ RowTile nth_tile(const int32_t* offsets, int E, int r
 
 // Few rows (decode): a block takes 16 NB weight rows of one expert for up to 16 MB
 // of its rows, as the dense kernel of few rows does; bound by reading the weights
-// of the experts that have rows.  Four waves split K, not eight: an expert's
-// block is short (8 turns of 64 k a wave at K = 4096 would be 4), and with 48 or 32 KB
-// of LDS three to five blocks a CU cover each other's ends (192 rows, 256 experts
-// of 4096 x 2048: 1143 us, eight waves 1330).  Every block finds its rows by itself
-// from the offsets: no launch ahead of the product.
+// of the experts that have rows.  Four waves split K, not eight: they have 16 turns
+// of 64 k each at K = 4096, not 8, beside a block's ends, and with 48 or 32 KB of LDS
+// three to five blocks a CU cover each other's (192 rows, 256 experts of 4096 x 2048:
+// 1143 us, eight waves 1330).  Every block finds its rows by itself from the offsets:
+// no launch ahead of the product.
 constexpr int kGroupFewWaves = 4;
 template <typename E, int MB, int NB, int EPI, int D, bool GATHER>
 __global__ __launch_bounds__(64 * kGroupFewWaves) void group_few_kernel(GroupJob g, const int32_t* offsets, int experts,
