@@ -75,7 +75,8 @@ typedef enum moe_act_dtype {     /* the A operand of a grouped GEMM */
 typedef enum moe_out_dtype {     /* the output of a grouped GEMM / intermediate */
   MOE_OUT_FP32 = 0,
   MOE_OUT_BF16 = 1,
-  MOE_OUT_MXFP8_E4M3 = 2
+  MOE_OUT_MXFP8_E4M3 = 2,
+  MOE_OUT_FP16 = 3               /* rows of moe_combine only (experts with fp16 weights) */
 } moe_out_dtype;
 
 typedef enum moe_epilogue {
@@ -271,7 +272,8 @@ moe_status moe_mxfp4_untile_weights(const uint8_t* t_packed, const uint8_t* t_sc
 /* Weighted top-k combine that ends the fused MoE (Kimi-K3 page, goal):
  *   out[t][h] = sum_{j = 0..k-1, ascending} topk_w[t][j] * y[dest_row[t*k+j]][h]
  * in fp32.  A gather-reduce: no atomics, run-to-run deterministic.
- *   y        device [T*k][H] in permuted row order, fp32 or bf16 (y_dtype).
+ *   y        device [T*k][H] in permuted row order; y_dtype is a moe_out_dtype:
+ *            MOE_OUT_FP32, MOE_OUT_BF16 or MOE_OUT_FP16.
  *   out      device fp32 [T][H].
  *   x_next   device bf16 [T][H] or NULL: if given, also writes
  *            bf16(out[t] / sqrt(mean_h out[t][h]^2)) (the stacked-layer

@@ -24,7 +24,7 @@ ABI_VERSION = 3
 STATUS = {"MOE_OK": 0, "MOE_ERR_INVALID_ARG": 1, "MOE_ERR_SHAPE": 2, "MOE_ERR_UNSUPPORTED_DEVICE": 3,
           "MOE_ERR_NOT_PINNED": 4, "MOE_ERR_WORKSPACE": 5, "MOE_ERR_HIP": 6, "MOE_ERR_NOT_IMPLEMENTED": 7}
 ACT = {"MOE_ACT_BF16": 0, "MOE_ACT_MXFP8_E4M3": 1}
-OUT = {"MOE_OUT_FP32": 0, "MOE_OUT_BF16": 1, "MOE_OUT_MXFP8_E4M3": 2}
+OUT = {"MOE_OUT_FP32": 0, "MOE_OUT_BF16": 1, "MOE_OUT_MXFP8_E4M3": 2, "MOE_OUT_FP16": 3}
 EPI = {"MOE_EPI_NONE": 0, "MOE_EPI_SWIGLU_SPLIT": 1, "MOE_EPI_SWIGLU_INTERLEAVED": 2}
 CHAIN = {"MOE_CHAIN_RMS": 0, "MOE_CHAIN_INDEPENDENT": 1}
 WFORMAT = {"MOE_W_CANONICAL": 0, "MOE_W_TILED": 1}
@@ -36,6 +36,8 @@ EXPERT_COPY = {"all": COPY["MOE_COPY_ALL"], "routed": COPY["MOE_COPY_ROUTED"], "
 W_FORMAT = {"canonical": WFORMAT["MOE_W_CANONICAL"], "tiled": WFORMAT["MOE_W_TILED"]}
 
 GATE_ACT = {"silu": GATE["MOE_GATE_SILU"], "gelu": GATE["MOE_GATE_GELU"]}
+OUT_DTYPE = {torch.float32: OUT["MOE_OUT_FP32"], torch.bfloat16: OUT["MOE_OUT_BF16"],
+             torch.float16: OUT["MOE_OUT_FP16"]}
 FLOAT_DTYPE = {torch.bfloat16: FLOAT["MOE_FLOAT_BF16"], torch.float16: FLOAT["MOE_FLOAT_FP16"],
                torch.float32: FLOAT["MOE_FLOAT_FP32"]}
 
@@ -364,14 +366,22 @@ def untile_weights(t_packed: torch.Tensor, t_scales: torch.Tensor, epilogue: str
 
 def combine(y: torch.Tensor, dest_row: torch.Tensor, topk_w: torch.Tensor, *, rms_next: bool = False,
             stream=None):
-    """moe_combine: y [T*k][H] (fp32 or bf16) -> out fp32 [T][H] (and bf16 x_next if rms_next)."""
+    """moe_combine: y [T*k][H] (fp32, bf16 or fp16) -> out fp32 [T][H] (and bf16 x_next if rms_next)."""
     T, k = topk_w.shape
+    if y.dim() != 2 or y.shape[0] < T * k or y.dtype not in OUT_DTYPE or not y.is_contiguous() \
+            or y.device != topk_w.device:
+        raise ValueError(f"y must be a contiguous tensor of {T * k} rows in {' or '.join(str(d) for d in OUT_DTYPE)} on "
+                         f"{topk_w.device}: got {y.dtype} {tuple(y.shape)}, strides {y.stride()}, on {y.device}")
+    _flat("topk_w", topk_w, (T, k), (torch.float32,), y.device)
+    if dest_row.numel() != T * k or dest_row.dtype != torch.int32 or not dest_row.is_contiguous() \
+            or dest_row.device != y.device:
+        raise ValueError(f"dest_row must be {T * k} contiguous torch.int32 on {y.device}: got {dest_row.dtype} "
+                         f"{tuple(dest_row.shape)}, strides {dest_row.stride()}, on {dest_row.device}")
     H = y.shape[1]
     with _allocate_on(stream):
         out = torch.empty((T, H), dtype=torch.float32, device=y.device)
         xn = torch.empty((T, H), dtype=torch.bfloat16, device=y.device) if rms_next else None
-    dt = 1 if y.dtype == torch.bfloat16 else 0
-    _check(lib.moe_combine(_ptr(y), dt, _ptr(dest_row), _ptr(topk_w), T, k, H, _ptr(out), _ptr(xn),
+    _check(lib.moe_combine(_ptr(y), OUT_DTYPE[y.dtype], _ptr(dest_row), _ptr(topk_w), T, k, H, _ptr(out), _ptr(xn),
                            _stream(stream)))
     _keep_until_done(stream, out, xn, y, dest_row, topk_w)
     return (out, xn) if rms_next else out
@@ -379,7 +389,7 @@ def combine(y: torch.Tensor, dest_row: torch.Tensor, topk_w: torch.Tensor, *, rm
 
 def combine_backward(dout: torch.Tensor, y: Optional[torch.Tensor], dest_row: torch.Tensor, topk_w: torch.Tensor, *,
                      dy=True, dy_dtype: Optional[torch.dtype] = None, dw: bool = True, stream=None):
-    """moe_combine_backward: dout fp32 [T][H], y [T*k][H] (as the combine took it, or fp16) ->
+    """moe_combine_backward: dout fp32 [T][H], y [T*k][H] (as the combine took it) ->
     (dy [T*k][H], dtopk_w fp32 [T][k]).
 
     dy: True allocates it in dy_dtype (default y's type), a tensor receives it, False or None skips it.  dw:

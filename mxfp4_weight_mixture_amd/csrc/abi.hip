@@ -97,7 +97,8 @@ const char* moe_enum_name(int kind, int v) {
     case MOE_ENUM_OUT:
       return v == MOE_OUT_FP32 ? "MOE_OUT_FP32"
              : v == MOE_OUT_BF16 ? "MOE_OUT_BF16"
-             : v == MOE_OUT_MXFP8_E4M3 ? "MOE_OUT_MXFP8_E4M3" : nullptr;
+             : v == MOE_OUT_MXFP8_E4M3 ? "MOE_OUT_MXFP8_E4M3"
+             : v == MOE_OUT_FP16 ? "MOE_OUT_FP16" : nullptr;
     case MOE_ENUM_EPI:
       return v == MOE_EPI_NONE ? "MOE_EPI_NONE"
              : v == MOE_EPI_SWIGLU_SPLIT ? "MOE_EPI_SWIGLU_SPLIT"
@@ -210,8 +211,8 @@ moe_status moe_mxfp4_untile_weights(const uint8_t* t_packed, const uint8_t* t_sc
 moe_status moe_combine(const void* y, int32_t y_dtype, const int32_t* dest_row, const float* topk_w,
                        int32_t T, int32_t k, int32_t H, float* out, uint16_t* x_next, void* stream) {
   clear_error();
-  if (y_dtype != MOE_OUT_FP32 && y_dtype != MOE_OUT_BF16)
-    return fail(MOE_ERR_INVALID_ARG, "combine: y_dtype %d must be MOE_OUT_FP32 or MOE_OUT_BF16", y_dtype);
+  if (y_dtype != MOE_OUT_FP32 && y_dtype != MOE_OUT_BF16 && y_dtype != MOE_OUT_FP16)
+    return fail(MOE_ERR_INVALID_ARG, "combine: y_dtype %d must be MOE_OUT_FP32, MOE_OUT_BF16 or MOE_OUT_FP16", y_dtype);
   if (T < 0 || k < 1 || H < 1) return fail(MOE_ERR_SHAPE, "combine: T %d, k %d, H %d out of range", T, k, H);
   if (H % 8) return fail(MOE_ERR_SHAPE, "combine: H = %d must be a multiple of 8", H);
   if (T > 0 && (!y || !dest_row || !topk_w || !out)) return fail(MOE_ERR_INVALID_ARG, "combine: null pointer");

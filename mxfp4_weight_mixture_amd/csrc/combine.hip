@@ -1,10 +1,10 @@
 // Weighted top-k combine (the end of a fused MoE: "Kimi-K3 SM120 FlashInfer
 // MXFP4 MoE", goal section):
 //   out[t][h] = sum_{j ascending} w[t][j] * y[dest_row[t*k + j]][h]   (fp32)
-// One workgroup per token; each thread owns 8 consecutive h (16-byte bf16
-// or 32-byte fp32 loads), so every row of y is read once, coalesced, and
+// One workgroup per token; each thread owns 8 consecutive h (16-byte bf16 or
+// fp16 or 32-byte fp32 loads), so every row of y is read once, coalesced, and
 // no atomics are involved.  The workgroup is sized to the row (at most 1024
-// threads for bf16 rows, 512 for fp32 ones, whose 32-byte loads take twice
+// threads for 16-bit rows, 512 for fp32 ones, whose 32-byte loads take twice
 // the registers; whole waves, every pass over the row full but the last), and a
 // thread has up to 16 rows of y in flight.  Optionally also writes the next
 // stacked layer's input bf16(out[t] / rms(out[t])).
@@ -13,11 +13,13 @@
 namespace mxmoe {
 namespace {
 
-// raw 8-element vectors: bf16 as one 16-byte load, fp32 as two
+// raw 8-element vectors: bf16 and fp16 as one 16-byte load, fp32 as two
 struct Raw8Bf16 { uint4 q; };
+typedef _Float16 Raw8Fp16 __attribute__((ext_vector_type(8)));
 struct Raw8F32 { float4 a, b; };
 
 __device__ inline Raw8Bf16 load_raw(const uint16_t* p) { return {*reinterpret_cast<const uint4*>(p)}; }
+__device__ inline Raw8Fp16 load_raw(const _Float16* p) { return *reinterpret_cast<const Raw8Fp16*>(p); }
 __device__ inline Raw8F32 load_raw(const float* p) {
   return {*reinterpret_cast<const float4*>(p), *reinterpret_cast<const float4*>(p + 4)};
 }
@@ -29,6 +31,10 @@ __device__ inline void widen(const Raw8Bf16& r, float* v) {
     v[2 * i] = __uint_as_float(u[i] << 16);
     v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
   }
+}
+__device__ inline void widen(const Raw8Fp16& r, float* v) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = (float)r[i];
 }
 __device__ inline void widen(const Raw8F32& r, float* v) {
   v[0] = r.a.x; v[1] = r.a.y; v[2] = r.a.z; v[3] = r.a.w;
@@ -127,6 +133,9 @@ moe_status launch_combine(const void* y, int y_dtype, const int32_t* dest_row, c
   if (y_dtype == MOE_OUT_BF16)
     hipLaunchKernelGGL(combine_kernel<uint16_t>, dim3(T), dim3(combine_threads(H, max_threads<uint16_t>())), 0, s,
                        static_cast<const uint16_t*>(y), dest_row, w, k, H, out, x_next);
+  else if (y_dtype == MOE_OUT_FP16)
+    hipLaunchKernelGGL(combine_kernel<_Float16>, dim3(T), dim3(combine_threads(H, max_threads<_Float16>())), 0, s,
+                       static_cast<const _Float16*>(y), dest_row, w, k, H, out, x_next);
   else
     hipLaunchKernelGGL(combine_kernel<float>, dim3(T), dim3(combine_threads(H, max_threads<float>())), 0, s,
                        static_cast<const float*>(y), dest_row, w, k, H, out, x_next);
