@@ -274,6 +274,9 @@ moe_status moe_mxfp4_untile_weights(const uint8_t* t_packed, const uint8_t* t_sc
  * in fp32.  A gather-reduce: no atomics, run-to-run deterministic.
  *   y        device [T*k][H] in permuted row order; y_dtype is a moe_out_dtype:
  *            MOE_OUT_FP32, MOE_OUT_BF16 or MOE_OUT_FP16.
+ *   dest_row a row outside [0, T*k) is not there and adds nothing (another
+ *            device holds its expert: each device's out is its experts' part
+ *            of the sum).
  *   out      device fp32 [T][H].
  *   x_next   device bf16 [T][H] or NULL: if given, also writes
  *            bf16(out[t] / sqrt(mean_h out[t][h]^2)) (the stacked-layer
@@ -656,7 +659,9 @@ moe_status moe_route_backward(const float* dtopk_w, const int32_t* topk_ids, con
  * outside [0, tokens) counts as zeros.  Experts may have any number of rows, none
  * included; rows outside [expert_offsets[0], expert_offsets[E]) are not read and
  * their outputs are left as they were (a part of the experts that one device
- * holds; a padded batch).  Offsets ascend; what exceeds [0, rows] is cut.
+ * holds; a padded batch).  moe_combine and moe_combine_backward take every row
+ * that dest_row names: give them a dest_row with -1 in the place of rows that are
+ * not the experts'.  Offsets ascend; what exceeds [0, rows] is cut.
  * Accumulation and roundings as in moe_gated_ffn_forward.
  *
  * Sizes: 0 <= rows <= 2^28 (0 enqueues nothing), 1 <= E <= 8192, H and I multiples

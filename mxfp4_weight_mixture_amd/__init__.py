@@ -366,7 +366,9 @@ def untile_weights(t_packed: torch.Tensor, t_scales: torch.Tensor, epilogue: str
 
 def combine(y: torch.Tensor, dest_row: torch.Tensor, topk_w: torch.Tensor, *, rms_next: bool = False,
             stream=None):
-    """moe_combine: y [T*k][H] (fp32, bf16 or fp16) -> out fp32 [T][H] (and bf16 x_next if rms_next)."""
+    """moe_combine: y [T*k][H] (fp32, bf16 or fp16) -> out fp32 [T][H] (and bf16 x_next if rms_next).
+
+    A dest_row outside [0, T*k) adds nothing: -1 for rows whose experts another device holds."""
     T, k = topk_w.shape
     if y.dim() != 2 or y.shape[0] < T * k or y.dtype not in OUT_DTYPE or not y.is_contiguous() \
             or y.device != topk_w.device:
@@ -699,7 +701,9 @@ class ExpertFFN:
     of it.  permute's results are what the calls take: expert_offsets, gather=perm_src with gather_div=k, and
     dest_row.  w1 [E][2I][H], w2 [E][H][I]; layouts, activations, types and rounding as in GatedFFN, which also
     says what the object holds and what autograd sees.  Rows of no expert (before the first offset or behind the
-    last) are neither read nor written.
+    last) are neither read nor written.  A device's share, experts [a, b) of all, takes offsets[a:b + 1]; combine
+    and combine_backward then take torch.where((dest >= offsets[a]) & (dest < offsets[b]), dest, -1), and give the
+    share's part of the sum and its rows' gradients.
     """
 
     def __init__(self, w1: torch.Tensor, w2: torch.Tensor, layout: str = "split", act: str = "silu"):

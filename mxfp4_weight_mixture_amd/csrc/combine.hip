@@ -1,6 +1,7 @@
 // Weighted top-k combine (the end of a fused MoE: "Kimi-K3 SM120 FlashInfer
 // MXFP4 MoE", goal section):
 //   out[t][h] = sum_{j ascending} w[t][j] * y[dest_row[t*k + j]][h]   (fp32)
+// over the rows that are there: a dest_row outside [0, T*k) adds nothing.
 // One workgroup per token; each thread owns 8 consecutive h (16-byte bf16 or
 // fp16 or 32-byte fp32 loads), so every row of y is read once, coalesced, and
 // no atomics are involved.  The workgroup is sized to the row (at most 1024
@@ -8,6 +9,9 @@
 // the registers; whole waves, every pass over the row full but the last), and a
 // thread has up to 16 rows of y in flight.  Optionally also writes the next
 // stacked layer's input bf16(out[t] / rms(out[t])).
+#include <algorithm>
+#include <type_traits>
+
 #include "internal.h"
 
 namespace mxmoe {
@@ -66,11 +70,15 @@ int combine_threads(int H, int max_threads) {
   return (per_pass + 63) / 64 * 64;
 }
 
-template <typename YT>
+// CHECKED: a dest_row may name no row; tokens that have all of theirs, which a wave
+// sees at once, take their loads without asking (T 8192, k 16, H 7168 in bf16: 414 us
+// against 441 with the question at every load, 415 unchecked; T 32: 4.9, 4.8 and
+// 4.65).  The layer's own rows come from its own permutation and go unchecked.
+template <typename YT, bool CHECKED>
 __global__ __launch_bounds__(max_threads<YT>()) void combine_kernel(const YT* __restrict__ y,
                                                       const int32_t* __restrict__ dest_row,
-                                                      const float* __restrict__ w, int k, int H,
-                                                      float* __restrict__ out,
+                                                      const float* __restrict__ w, uint32_t n_rows, int k,
+                                                      int H, float* __restrict__ out,
                                                       uint16_t* __restrict__ x_next) {
   using Raw = decltype(load_raw(y));
   const int t = blockIdx.x;
@@ -79,25 +87,35 @@ __global__ __launch_bounds__(max_threads<YT>()) void combine_kernel(const YT* __
   const int32_t* rows = dest_row + (size_t)t * k;
   const float* wt = w + (size_t)t * k;
   const int nthr = blockDim.x;
+  bool all = true;
+  if constexpr (CHECKED) {
+    for (int j = threadIdx.x & 63; j < k; j += 64) all = all && (uint32_t)rows[j] < n_rows;
+    all = __all(all);
+  }
   float ss = 0.f;
   for (int v = threadIdx.x; v < nv; v += nthr) {
     float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int j0 = 0; j0 < k; j0 += kBatch) {
-      Raw raw[kBatch];
+    auto sum = [&](auto ALL) {
+      for (int j0 = 0; j0 < k; j0 += kBatch) {
+        Raw raw[kBatch];
 #pragma unroll
-      for (int b = 0; b < kBatch; ++b)
-        if (j0 + b < k) raw[b] = load_raw(y + (size_t)rows[j0 + b] * H + 8 * v);
+        for (int b = 0; b < kBatch; ++b)
+          if (j0 + b < k && (ALL || (uint32_t)rows[j0 + b] < n_rows))
+            raw[b] = load_raw(y + (size_t)rows[j0 + b] * H + 8 * v);
 #pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        if (j0 + b < k) {
-          const float wj = wt[j0 + b];
-          float yv[8];
-          widen(raw[b], yv);
+        for (int b = 0; b < kBatch; ++b) {
+          if (j0 + b < k && (ALL || (uint32_t)rows[j0 + b] < n_rows)) {
+            const float wj = wt[j0 + b];
+            float yv[8];
+            widen(raw[b], yv);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) acc[i] = fmaf(wj, yv[i], acc[i]);
+            for (int i = 0; i < 8; ++i) acc[i] = fmaf(wj, yv[i], acc[i]);
+          }
         }
       }
-    }
+    };
+    if (!CHECKED || all) sum(std::true_type());
+    else sum(std::false_type());
     *reinterpret_cast<float4*>(orow + 8 * v) = make_float4(acc[0], acc[1], acc[2], acc[3]);
     *reinterpret_cast<float4*>(orow + 8 * v + 4) = make_float4(acc[4], acc[5], acc[6], acc[7]);
 #pragma unroll
@@ -127,20 +145,26 @@ __global__ __launch_bounds__(max_threads<YT>()) void combine_kernel(const YT* __
 
 }  // namespace
 
+template <typename YT, bool CHECKED>
+static moe_status launch_typed(const void* y, const int32_t* dest_row, const float* w, int T, int k, int H, float* out,
+                               uint16_t* x_next, hipStream_t s) {
+  const uint32_t n_rows = (uint32_t)std::min((int64_t)T * k, (int64_t)1 << 31);   // (indices are int32)
+  hipLaunchKernelGGL((combine_kernel<YT, CHECKED>), dim3(T), dim3(combine_threads(H, max_threads<YT>())), 0, s,
+                     static_cast<const YT*>(y), dest_row, w, n_rows, k, H, out, x_next);
+  MXMOE_HIP(hipGetLastError());
+  return MOE_OK;
+}
+
 moe_status launch_combine(const void* y, int y_dtype, const int32_t* dest_row, const float* w,
                           int T, int k, int H, float* out, uint16_t* x_next, hipStream_t s) {
   if (T == 0) return MOE_OK;
-  if (y_dtype == MOE_OUT_BF16)
-    hipLaunchKernelGGL(combine_kernel<uint16_t>, dim3(T), dim3(combine_threads(H, max_threads<uint16_t>())), 0, s,
-                       static_cast<const uint16_t*>(y), dest_row, w, k, H, out, x_next);
-  else if (y_dtype == MOE_OUT_FP16)
-    hipLaunchKernelGGL(combine_kernel<_Float16>, dim3(T), dim3(combine_threads(H, max_threads<_Float16>())), 0, s,
-                       static_cast<const _Float16*>(y), dest_row, w, k, H, out, x_next);
-  else
-    hipLaunchKernelGGL(combine_kernel<float>, dim3(T), dim3(combine_threads(H, max_threads<float>())), 0, s,
-                       static_cast<const float*>(y), dest_row, w, k, H, out, x_next);
-  MXMOE_HIP(hipGetLastError());
-  return MOE_OK;
+  if (y_dtype == MOE_OUT_BF16) return launch_typed<uint16_t, true>(y, dest_row, w, T, k, H, out, x_next, s);
+  if (y_dtype == MOE_OUT_FP16) return launch_typed<_Float16, true>(y, dest_row, w, T, k, H, out, x_next, s);
+  return launch_typed<float, true>(y, dest_row, w, T, k, H, out, x_next, s);
+}
+moe_status launch_layer_combine(const void* y, const int32_t* dest_row, const float* w, int T, int k, int H, float* out,
+                                uint16_t* x_next, hipStream_t s) {
+  return T == 0 ? MOE_OK : launch_typed<uint16_t, false>(y, dest_row, w, T, k, H, out, x_next, s);
 }
 
 }  // namespace mxmoe

@@ -45,8 +45,11 @@ size_t gemm_ws_bytes(int rows, int E);
 // max_rows: a bound on any expert's row count (-1: the call's rows); row-tile
 // classes no expert can fill are not launched.
 moe_status launch_gemm(const moe_gemm_args& a, void* ws, hipStream_t s, int reserve = 0, int max_rows = -1);
+// (dest_row outside [0, T*k): nothing is added; the layer's bf16 rows are all there)
 moe_status launch_combine(const void* y, int y_dtype, const int32_t* dest_row, const float* w,
                           int T, int k, int H, float* out, uint16_t* x_next, hipStream_t s);
+moe_status launch_layer_combine(const void* y, const int32_t* dest_row, const float* w, int T, int k, int H, float* out,
+                                uint16_t* x_next, hipStream_t s);
 moe_status validate_gemm(const moe_gemm_args& a);
 // routed expert copy (expert_copy.hip): copies expert e's byte range of each of
 // the four sections when expert_offsets[e + 1] > expert_offsets[e]; `blocks`

@@ -179,7 +179,7 @@ moe_status run_experts(const moe_layer_args& a, const Routing& r, hipStream_t s,
   g2.w_format = a.w_format;
   MXMOE_TRY(launch_gemm(g2, ws + L.gemm_ws, s, reserve, a.T));
 
-  return launch_combine(ws + L.y, MOE_OUT_BF16, r.dest_row, r.w, a.T, a.k, a.H, a.out, a.x_next, s);
+  return launch_layer_combine(ws + L.y, r.dest_row, r.w, a.T, a.k, a.H, a.out, a.x_next, s);
 }
 
 // The body of a layer, all arguments valid; pointers into `ws`.
