@@ -272,7 +272,8 @@ moe_status moe_mxfp4_untile_weights(const uint8_t* t_packed, const uint8_t* t_sc
 /* Weighted top-k combine that ends the fused MoE (Kimi-K3 page, goal):
  *   out[t][h] = sum_{j = 0..k-1, ascending} topk_w[t][j] * y[dest_row[t*k+j]][h]
  * in fp32.  A gather-reduce: no atomics, run-to-run deterministic.
- *   y        device [T*k][H] in permuted row order; y_dtype is a moe_out_dtype:
+ *   y        device [T*k][H] in permuted row order; y_dtype is a moe_out_dtype
+ *            (moe_combine_backward's is a moe_float_dtype, with other numbers):
  *            MOE_OUT_FP32, MOE_OUT_BF16 or MOE_OUT_FP16.
  *   dest_row a row outside [0, T*k) is not there and adds nothing (another
  *            device holds its expert: each device's out is its experts' part
@@ -631,6 +632,8 @@ moe_status moe_rms_norm_backward(const moe_norm_grad_args* args, void* stream);
 /* The combine's gradients (out[t] = sum_j topk_w[t][j] * y[dest_row[t*k + j]]):
  *   dy[dest_row[t*k + j]] = topk_w[t][j] * dout[t]
  *   dtopk_w[t][j]         = sum_h y[dest_row[t*k + j]][h] * dout[t][h]
+ * y_dtype and dy_dtype are moe_float_dtypes (moe_combine's y_dtype is a
+ * moe_out_dtype, with other numbers).
  * dout is fp32, as the combine's out; dy is rounded once, dtopk_w is fp32.  Either
  * may be NULL; y is read for dtopk_w only.  A dest_row outside [0, T*k) has no
  * row: nothing is written for it and its dtopk_w is 0.  Rows of dy that no
@@ -733,6 +736,22 @@ size_t     moe_expert_ffn_grad_workspace_size(int32_t rows, int32_t H, int32_t I
 moe_status moe_expert_ffn_backward(const moe_expert_ffn_grad_args* args, void* stream);
 
 #ifdef __cplusplus
-}
+} /* extern "C" */
+#if __cplusplus >= 201103L
+
+/* moe_combine counts its types by moe_out_dtype, moe_combine_backward by
+ * moe_float_dtype: 0 and 1 are valid in both and mean other types.  The other
+ * call's names do not compile (C++). */
+moe_status moe_combine(const void* y, moe_float_dtype y_dtype, const int32_t* dest_row, const float* topk_w, int32_t T,
+                       int32_t k, int32_t H, float* out, uint16_t* x_next, void* stream) = delete;
+template <typename Dy>
+moe_status moe_combine_backward(const float* dout, const void* y, moe_out_dtype y_dtype, const int32_t* dest_row,
+                                const float* topk_w, int32_t T, int32_t k, int32_t H, void* dy, Dy dy_dtype,
+                                float* dtopk_w, void* stream) = delete;
+template <typename Y>
+moe_status moe_combine_backward(const float* dout, const void* y, Y y_dtype, const int32_t* dest_row,
+                                const float* topk_w, int32_t T, int32_t k, int32_t H, void* dy, moe_out_dtype dy_dtype,
+                                float* dtopk_w, void* stream) = delete;
+#endif
 #endif
 #endif /* MXMOE_H */
