@@ -720,11 +720,11 @@ class ExpertFFN:
         self.dtype, self.device = w1.dtype, w1.device
         self._dtypes = (self.dtype, torch.float32)
         same = dict(H=self.H, I=self.I, E=self.E, layout=LAYOUT[layout], gate_act=GATE_ACT[act],
-                    dtype=FLOAT_DTYPE[self.dtype], w1=w1.data_ptr(), w2=w2.data_ptr())
+                    dtype=FLOAT_DTYPE[self.dtype])
         self._fwd, self._bwd = ExpertFfnArgs(**same), ExpertFfnGradArgs(**same)
 
     def _take_rows(self, a, x, expert_offsets, gather, gather_div):
-        """x, its gather and the offsets into the arguments `a`; returns the number of rows."""
+        """x, its gather, the offsets and the weights into the arguments `a`; returns the number of rows."""
         _flat("expert_offsets", expert_offsets, (self.E + 1,), (torch.int32,), self.device)
         a.x_stride = _rows("x", x, None, self.H, (self.dtype,), self.device)
         rows = x.shape[0]
@@ -735,6 +735,7 @@ class ExpertFFN:
         elif gather_div != 1:
             raise ValueError("gather_div without gather")
         a.rows, a.x, a.expert_offsets = rows, x.data_ptr(), expert_offsets.data_ptr()
+        a.w1, a.w2 = self.w1.data_ptr(), self.w2.data_ptr()
         return rows
 
     def forward(self, x: torch.Tensor, expert_offsets: torch.Tensor, *, gather: Optional[torch.Tensor] = None,
@@ -849,7 +850,7 @@ class RMSNorm:
             raise ValueError("weight must be a contiguous device tensor")
         self.weight, self.eps = weight, float(eps)
         self.H, self.device = weight.shape[0], weight.device
-        same = dict(H=self.H, eps=self.eps, weight=weight.data_ptr(), weight_dtype=FLOAT_DTYPE[weight.dtype])
+        same = dict(H=self.H, eps=self.eps, weight_dtype=FLOAT_DTYPE[weight.dtype])
         self._fwd, self._bwd = NormArgs(**same), NormGradArgs(**same)
 
     def _type16(self, *tensors):
@@ -875,7 +876,7 @@ class RMSNorm:
         a.dtype = FLOAT_DTYPE[d16]
         a.x_stride = _rows("x", x, None, self.H, types, self.device)
         T = a.T = x.shape[0]
-        a.x, a.x_dtype = x.data_ptr(), FLOAT_DTYPE[x.dtype]
+        a.x, a.x_dtype, a.weight = x.data_ptr(), FLOAT_DTYPE[x.dtype], self.weight.data_ptr()
         if residual is not None:
             a.residual_stride = _rows("residual", residual, T, self.H, types, self.device)
             if residual_out is None:
@@ -929,6 +930,7 @@ class RMSNorm:
         a.x_stride = _rows("x", x, T, self.H, types, self.device)
         a.dout, a.dout_dtype, a.x, a.x_dtype = (dout.data_ptr(), FLOAT_DTYPE[dout.dtype], x.data_ptr(),
                                                 FLOAT_DTYPE[x.dtype])
+        a.weight = self.weight.data_ptr()
         if dresidual is not None:
             a.dresidual_stride = _rows("dresidual", dresidual, T, self.H, types, self.device)
             a.dresidual, a.dresidual_dtype = dresidual.data_ptr(), FLOAT_DTYPE[dresidual.dtype]
