@@ -375,15 +375,12 @@ def combine(y: torch.Tensor, dest_row: torch.Tensor, topk_w: torch.Tensor, *, rm
         raise ValueError(f"y must be a contiguous tensor of {T * k} rows in {' or '.join(str(d) for d in OUT_DTYPE)} on "
                          f"{topk_w.device}: got {y.dtype} {tuple(y.shape)}, strides {y.stride()}, on {y.device}")
     _flat("topk_w", topk_w, (T, k), (torch.float32,), y.device)
-    if dest_row.numel() != T * k or dest_row.dtype != torch.int32 or not dest_row.is_contiguous() \
-            or dest_row.device != y.device:
-        raise ValueError(f"dest_row must be {T * k} contiguous torch.int32 on {y.device}: got {dest_row.dtype} "
-                         f"{tuple(dest_row.shape)}, strides {dest_row.stride()}, on {dest_row.device}")
+    dest = _slots("dest_row", dest_row, T * k, y.device, stream)
     H = y.shape[1]
     with _allocate_on(stream):
         out = torch.empty((T, H), dtype=torch.float32, device=y.device)
         xn = torch.empty((T, H), dtype=torch.bfloat16, device=y.device) if rms_next else None
-    _check(lib.moe_combine(_ptr(y), OUT_DTYPE[y.dtype], _ptr(dest_row), _ptr(topk_w), T, k, H, _ptr(out), _ptr(xn),
+    _check(lib.moe_combine(_ptr(y), OUT_DTYPE[y.dtype], _ptr(dest), _ptr(topk_w), T, k, H, _ptr(out), _ptr(xn),
                            _stream(stream)))
     _keep_until_done(stream, out, xn, y, dest_row, topk_w)
     return (out, xn) if rms_next else out
@@ -406,9 +403,7 @@ def combine_backward(dout: torch.Tensor, y: Optional[torch.Tensor], dest_row: to
         raise ValueError(f"dout has shape {tuple(dout.shape)}, not ({T}, H)")
     H = dout.shape[1]
     _flat("dout", dout, (T, H), (torch.float32,), dev)
-    if dest_row.dim() == 2:
-        dest_row = dest_row.reshape(-1)
-    _flat("dest_row", dest_row, (T * k,), (torch.int32,), dev)
+    dest = _slots("dest_row", dest_row, T * k, dev, stream)
     if dw or y is not None:
         if y is None:
             raise ValueError("dtopk_w needs y")
@@ -421,7 +416,7 @@ def combine_backward(dout: torch.Tensor, y: Optional[torch.Tensor], dest_row: to
         dtopk_w = torch.empty((T, k), dtype=torch.float32, device=dev) if dw else None
     if dy is not None:
         _flat("dy", dy, (T * k, H), any_float if dy_dtype is None else (dy_dtype,), dev)
-    _check(lib.moe_combine_backward(_ptr(dout), _ptr(y), 0 if y is None else FLOAT_DTYPE[y.dtype], _ptr(dest_row),
+    _check(lib.moe_combine_backward(_ptr(dout), _ptr(y), 0 if y is None else FLOAT_DTYPE[y.dtype], _ptr(dest),
                                     _ptr(topk_w), T, k, H, _ptr(dy), 0 if dy is None else FLOAT_DTYPE.get(dy.dtype, -1),
                                     _ptr(dtopk_w), _stream(stream)))
     _keep_until_done(stream, dy, dtopk_w, dout, y, dest_row, topk_w)
@@ -466,6 +461,17 @@ def _flat(name, t, shape, dtypes, device):
                          f"{tuple(shape)} on {device}: got {t.dtype} {tuple(t.shape)}, strides {t.stride()}, "
                          f"on {t.device}")
     return t
+
+
+def _slots(name, t, n, device, stream):
+    """The int32 of n slots, [n] or [T][k], as they lie in memory; else a copy, made on the call's stream (the current
+    one's would not be waited for)."""
+    if t.shape != (n,) and (t.dim() != 2 or t.numel() != n) or t.dtype != torch.int32 or t.device != device:
+        raise ValueError(f"{name} must be {n} torch.int32 on {device}: got {t.dtype} {tuple(t.shape)} on {t.device}")
+    if t.is_contiguous():
+        return t
+    with _allocate_on(stream):
+        return t.contiguous()
 
 
 def _on_current_device(device, stream):
@@ -794,9 +800,8 @@ class ExpertFFN:
         if gather is not None and dx is not None and dx is not False:
             if dest_row is None:
                 raise ValueError("dx of gathered rows needs dest_row")
-            dest_row = dest_row.reshape(-1) if dest_row.dim() == 2 else dest_row
-            _flat("dest_row", dest_row, (x.shape[0] * gather_div,), (torch.int32,), self.device)
-            a.dest_row = dest_row.data_ptr()
+            dest = _slots("dest_row", dest_row, x.shape[0] * gather_div, self.device, stream)
+            a.dest_row = dest.data_ptr()
         dw_dtype = dw_dtype or next((g.dtype for g in (dw1, dw2) if isinstance(g, torch.Tensor)), self.dtype)
         n = lib.moe_expert_ffn_grad_workspace_size(rows, self.H, self.I, self.E, int(gather is not None))
 
