@@ -59,7 +59,10 @@ __device__ __forceinline__ void expert_rows(const int32_t* offsets, int e, int r
 __device__ __forceinline__ int tile_class(int rows) { return rows > 128 ? 0 : rows > 64 ? 1 : 2; }
 
 // One block; thread t lists experts [t per, (t + 1) per) behind those of the
-// threads before it.
+// threads before it.  Ascending offsets make cap tiles of a class at most.  Others can
+// claim up to 2^22 tiles for each of 8192 experts, past 2^31 together: every sum stops
+// at cap (64 lanes of up to cap < 2^23 each stay below 2^29, 16 waves below 2^27), and
+// nothing is listed from there on.
 __global__ __launch_bounds__(1024) void plan_rows_kernel(const int32_t* offsets, int E, int rows, int whole, int cap,
                                                          RowPlan* plan) {
   __shared__ int sums[16][kClasses];
@@ -74,13 +77,14 @@ __global__ __launch_bounds__(1024) void plan_rows_kernel(const int32_t* offsets,
   }
 #pragma unroll
   for (int c = 0; c < kClasses; ++c) {
+    n[c] = min(n[c], cap);
     int v = n[c];   // inclusive sum over the wave's lanes
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
       const int u = __shfl_up(v, off);
       if (lane >= off) v += u;
     }
-    if (lane == 63) sums[wave][c] = v;
+    if (lane == 63) sums[wave][c] = min(v, cap);
     at[c] = v - n[c];
   }
   __syncthreads();
@@ -92,8 +96,8 @@ __global__ __launch_bounds__(1024) void plan_rows_kernel(const int32_t* offsets,
       total += sums[w][c];
     }
     if (threadIdx.x == 0) plan->count[c] = min(total, cap);
+    at[c] = min(at[c], cap);
   }
-  // (offsets that do not ascend could ask for more than the list holds)
   auto put = [&](int c, int i, const RowTile& t) {
     if (i < cap) plan->list(c, cap)[i] = t;
   };
@@ -120,14 +124,14 @@ __global__ __launch_bounds__(1024) void plan_rows_kernel(const int32_t* offsets,
       const int le = __builtin_amdgcn_readlane(e, l), lf = __builtin_amdgcn_readlane(first, l);
       const int lc = __builtin_amdgcn_readlane(count, l), lt = __builtin_amdgcn_readlane(tiles, l);
       const int la = __builtin_amdgcn_readlane(at[wc], l);
-      for (int k = lane; k < lt; k += 64) put_tile(k, le, lf, lc, lt, la);
+      for (int k = lane; k < min(lt, cap - la); k += 64) put_tile(k, le, lf, lc, lt, la);
     }
     if (tiles <= kMany)
       for (int k = 0; k < tiles; ++k) put_tile(k, e, first, count, tiles, at[wc]);
-    at[wc] += tiles;
+    at[wc] = min(at[wc] + tiles, cap);
     if (rest && rc != wc) {
       put(rc, at[rc], RowTile{e, first + full * whole, rest, at[rc] << 4 | 1});
-      ++at[rc];
+      at[rc] = min(at[rc] + 1, cap);
     }
   }
 }

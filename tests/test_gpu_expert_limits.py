@@ -1,0 +1,54 @@
+"""The experts at the limits of their sizes, and offsets that break their rule there: whatever is asked for, other
+memory is not touched."""
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+mx = pytest.importorskip("mxfp4_weight_mixture_amd")
+BF, F = torch.bfloat16, torch.float32
+GUARD = 4096
+
+
+def _guarded(n, dtype=BF):
+    """n values of 0 between guards."""
+    buf = torch.full((n + 2 * GUARD,), 7.0, dtype=dtype, device="cuda")
+    buf[GUARD: GUARD + n] = 0
+    return buf, buf[GUARD: GUARD + n]
+
+
+def _intact(buf):
+    return bool((buf[:GUARD] == 7.0).all()) and bool((buf[-GUARD:] == 7.0).all())
+
+
+@pytest.mark.parametrize("rows", [1 << 28, (1 << 27) + 12345])
+def test_claims_past_2_31_tiles(rows):
+    """8192 experts, every second one claims all of 2^28 rows: 2^32 row tiles of 256 (a sum that has to stop at what
+    the list holds).  Weights and rows are 0, so that experts that claim the same rows write the same."""
+    E, H, I = 8192, 8, 8
+    f = mx.ExpertFFN(torch.zeros((E, 2 * I, H), dtype=BF, device="cuda"), torch.zeros((E, H, I), dtype=BF, device="cuda"))
+    off = torch.tensor([0, rows] * (E // 2) + [0], dtype=torch.int32, device="cuda")
+    x = torch.zeros((rows, H), dtype=BF, device="cuda")
+    buf, out = _guarded(rows * H)
+    # the call's workspace between guards, too: the list lies at its beginning
+    n = mx.lib.moe_expert_ffn_workspace_size(rows, H, I, E)
+    ws = torch.full((n + 2 * GUARD,), 9, dtype=torch.uint8, device="cuda")
+    a = mx.ExpertFfnArgs.from_buffer_copy(f._fwd)
+    a.w1, a.w2, a.rows, a.x, a.x_stride, a.out, a.out_stride = (f.w1.data_ptr(), f.w2.data_ptr(), rows, x.data_ptr(), H,
+                                                                out.data_ptr(), H)
+    a.expert_offsets, a.workspace, a.workspace_bytes = off.data_ptr(), ws.data_ptr() + GUARD, n
+    mx._check(mx.lib.moe_expert_ffn_forward(a, mx._stream()))
+    torch.cuda.synchronize()
+    assert _intact(buf) and not out.any()
+    assert (ws[:GUARD] == 9).all() and (ws[-GUARD:] == 9).all()
+    # what the rule allows still comes out at this size: every row of one expert in the middle
+    f.w1.fill_(1.0 / 8), f.w2.fill_(1.0 / 8), x.fill_(1.0)
+    off = torch.tensor([0] * (E // 2 + 1) + [rows] * (E // 2), dtype=torch.int32, device="cuda")
+    a.expert_offsets = off.data_ptr()
+    mx._check(mx.lib.moe_expert_ffn_forward(a, mx._stream()))
+    want = np.float32(1.0) / (1.0 + np.exp(-1.0))     # silu(1) * 1, eight eighths of it
+    torch.cuda.synchronize()
+    got = out.float()
+    assert abs(float(got.min()) - want) <= 2.0 ** -7 and abs(float(got.max()) - want) <= 2.0 ** -7
+    assert _intact(buf) and (ws[:GUARD] == 9).all() and (ws[-GUARD:] == 9).all()
