@@ -508,13 +508,18 @@ moe_status launch_back_typed(const Group& g, const DenseJob& dx, int64_t dx_step
   };
   // (315 and 189 tiles of 256 x 256 and short K: 150 us the whole training step, in tiles of 128 x 128 134)
   const bool wide = g.shape == kWide, big = wide && tiles(dw1, 256) + tiles(dw2, 256) >= 512;
-  for (int part = 0; part < (wide ? 3 : 1); ++part) {
+  auto units = [&](const DenseJob& j) { return (tiles(j, big ? 256 : 128) + 7) / 8 * 8; };
+  // Each of them has fewer than 2^24 blocks (check_experts), a launch may have no more:
+  // its threads are counted in 32 bits, and what passes them is not run, without an error.
+  const bool apart = wide || (dx.c ? unit_bound(g, dx) : 0) + units(dw1) + units(dw2) >= 1 << 24;
+  for (int part = 0; part < (apart ? 3 : 1); ++part) {
     BackJobs q{{dx, g.plan, tile_cap(g.rows, g.E), dx_step}, {{dw1, nullptr, 0, 0}, {dw2, nullptr, 0, 0}}, 0, {}};
     q.has_dx = dx.c != nullptr && part == 0;
     int64_t blocks = q.has_dx ? unit_bound(g, dx) : 0;
     for (int i = 0; i < 2; ++i) {
-      q.units[i] = !wide || part == i + 1 ? (int)tiles(q.dw[i].job, big ? 256 : 128) : 0;
-      blocks += (q.units[i] + 7) / 8 * 8;
+      const bool now = !apart || part == i + 1;
+      q.units[i] = now ? (int)tiles(q.dw[i].job, big ? 256 : 128) : 0;
+      if (now) blocks += units(q.dw[i].job);
     }
     if (blocks == 0) continue;
     const dim3 grid((unsigned)blocks), block(256);

@@ -4,6 +4,8 @@ import numpy as np
 import pytest
 import torch
 
+from tests import dense_util as du
+
 pytestmark = pytest.mark.gpu
 
 mx = pytest.importorskip("mxfp4_weight_mixture_amd")
@@ -52,3 +54,22 @@ def test_claims_past_2_31_tiles(rows):
     got = out.float()
     assert abs(float(got.min()) - want) <= 2.0 ** -7 and abs(float(got.max()) - want) <= 2.0 ** -7
     assert _intact(buf) and (ws[:GUARD] == 9).all() and (ws[-GUARD:] == 9).all()
+
+
+def test_gradients_whose_tiles_are_many_together():
+    """dx's, dw1's and dw2's tiles are each within one launch's limit (2^24 blocks of 256 threads), not together."""
+    E, H, I = 8192, 90112, 8
+    g = torch.Generator(device="cuda").manual_seed(1)
+    normal = lambda shape, scale: torch.empty(shape, dtype=BF, device="cuda").normal_(0.0, scale, generator=g)
+    f = mx.ExpertFFN(normal((E, 2 * I, H), H ** -0.5), normal((E, H, I), I ** -0.5))
+    x, dout = normal((E, H), 1.0), normal((E, H), 1.0)
+    off = torch.arange(E + 1, dtype=torch.int32, device="cuda")     # a row an expert
+    _, gu = f.forward(x, off, save=True)
+    grads = [torch.full(s, float("nan"), dtype=BF, device="cuda") for s in ((E, H), (E, 2 * I, H), (E, H, I))]
+    f.backward(dout, x, off, gu, dx=grads[0], dw1=grads[1], dw2=grads[2])
+    assert all(bool(t.isfinite().all()) for t in grads)
+    for e in (0, 1, 4097, E - 1):
+        x64, d64 = du.f64(x[e: e + 1]), du.f64(dout[e: e + 1])
+        refs = du.ffn_grad_bounds(d64, x64, du.f64(f.w1[e]), du.f64(f.w2[e]), "split", "silu", BF, F, BF, BF)
+        for what, got, (ref, bound) in zip(("dx", "dw1", "dw2"), (grads[0][e: e + 1], grads[1][e], grads[2][e]), refs):
+            du.assert_within(got, ref, bound, f"{what} of expert {e}")
