@@ -142,7 +142,8 @@ int         moe_device_supported(void);
  *            -0.0 equals +0.0; NaN sorts after every number.
  *   topk_w   device fp32 [T][k] out: softmax over the E logits,
  *            renormalised over the k kept = exp(l_j - max) / sum_j'.
- * Sizes: T >= 0 (T == 0 enqueues nothing), 1 <= E <= 1024, 1 <= k <= min(E, 64).
+ * Sizes: 0 <= T <= 2^26 - 4 (T == 0 enqueues nothing), 1 <= E <= 1024,
+ * 1 <= k <= min(E, 64).
  */
 moe_status moe_route(const float* logits, int32_t T, int32_t E, int32_t k,
                      int32_t* topk_ids, float* topk_w, void* stream);
@@ -647,8 +648,7 @@ moe_status moe_combine_backward(const float* dout, const void* y, int32_t y_dtyp
 /* The routing's gradient: topk_w is the softmax over a token's k kept logits, so
  *   dlogits[t][topk_ids[t][j]] = w_j * (dtopk_w_j - sum_i w_i * dtopk_w_i)
  * and 0 for the experts that were not kept.  An id outside [0, E) has no logit;
- * an id that a token lists twice gets the sum.  0 <= T < 2^26, E and k as for
- * moe_route. */
+ * an id that a token lists twice gets the sum.  T, E and k as for moe_route. */
 moe_status moe_route_backward(const float* dtopk_w, const int32_t* topk_ids, const float* topk_w, int32_t T,
                               int32_t E, int32_t k, float* dlogits, void* stream);
 

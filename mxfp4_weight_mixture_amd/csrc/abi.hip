@@ -130,7 +130,7 @@ int moe_device_supported(void) {
 moe_status moe_route(const float* logits, int32_t T, int32_t E, int32_t k, int32_t* topk_ids,
                      float* topk_w, void* stream) {
   clear_error();
-  if (T < 0) return fail(MOE_ERR_SHAPE, "route: T = %d < 0", T);
+  if (T < 0 || T > kMaxRouted) return fail(MOE_ERR_SHAPE, "route: T = %d outside [0, %d]", T, kMaxRouted);
   if (E < 1 || E > 1024) return fail(MOE_ERR_SHAPE, "route: E = %d outside [1, 1024]", E);
   if (k < 1 || k > E || k > 64) return fail(MOE_ERR_SHAPE, "route: k = %d outside [1, min(E=%d, 64)]", k, E);
   if (T > 0 && (!logits || !topk_ids || !topk_w)) return fail(MOE_ERR_INVALID_ARG, "route: null pointer");

@@ -34,6 +34,9 @@ int num_cus();
 
 inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
+// Tokens of a routing launch, four a block of 256 threads: below 2^32 threads.
+constexpr int kMaxRouted = (1 << 26) - 4;
+
 // ---- launchers (arguments already validated) --------------------------
 moe_status launch_route(const float* logits, int T, int E, int k, int32_t* ids, float* w,
                         hipStream_t s);

@@ -213,7 +213,8 @@ moe_status moe_route_backward(const float* dtopk_w, const int32_t* topk_ids, con
                               int32_t k, float* dlogits, void* stream) {
   const char* what = "route backward";
   clear_error();
-  if (T < 0 || T >= 1 << 26) return fail(MOE_ERR_SHAPE, "%s: T = %d out of range", what, T);
+  // (four tokens a block: fewer than 2^24 blocks, 2^32 threads; a launch of more does not run, without an error)
+  if (T < 0 || T > kMaxRouted) return fail(MOE_ERR_SHAPE, "%s: T = %d outside [0, %d]", what, T, kMaxRouted);
   if (E < 1 || E > 1024) return fail(MOE_ERR_SHAPE, "%s: E = %d outside [1, 1024]", what, E);
   if (k < 1 || k > E || k > 64) return fail(MOE_ERR_SHAPE, "%s: k = %d outside [1, min(E=%d, 64)]", what, k, E);
   if (T > 0) {
