@@ -283,7 +283,9 @@ moe_status moe_mxfp4_untile_weights(const uint8_t* t_packed, const uint8_t* t_sc
  *   x_next   device bf16 [T][H] or NULL: if given, also writes
  *            bf16(out[t] / sqrt(mean_h out[t][h]^2)) (the stacked-layer
  *            rule MOE_CHAIN_RMS).
- * Sizes: T >= 0, k >= 1, H >= 1, H % 8 == 0.
+ * Sizes: T >= 0, k >= 1, H >= 1, H % 8 == 0, fewer than 2^32 threads: a token
+ * takes H / 8 of them, in whole waves, 1024 at most (fp32 rows: 512), so that
+ * T < 2^22 always fits.
  */
 moe_status moe_combine(const void* y, int32_t y_dtype, const int32_t* dest_row,
                        const float* topk_w, int32_t T, int32_t k, int32_t H,

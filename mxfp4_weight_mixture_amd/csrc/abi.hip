@@ -215,6 +215,8 @@ moe_status moe_combine(const void* y, int32_t y_dtype, const int32_t* dest_row, 
     return fail(MOE_ERR_INVALID_ARG, "combine: y_dtype %d must be MOE_OUT_FP32, MOE_OUT_BF16 or MOE_OUT_FP16", y_dtype);
   if (T < 0 || k < 1 || H < 1) return fail(MOE_ERR_SHAPE, "combine: T %d, k %d, H %d out of range", T, k, H);
   if (H % 8) return fail(MOE_ERR_SHAPE, "combine: H = %d must be a multiple of 8", H);
+  if (!combine_fits(T, H, y_dtype))
+    return fail(MOE_ERR_SHAPE, "combine: T = %d rows of %d are too many for one launch", T, H);
   if (T > 0 && (!y || !dest_row || !topk_w || !out)) return fail(MOE_ERR_INVALID_ARG, "combine: null pointer");
   MXMOE_TRY(check_device());
   return launch_combine(y, y_dtype, dest_row, topk_w, T, k, H, out, x_next, (hipStream_t)stream);

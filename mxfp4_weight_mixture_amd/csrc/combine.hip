@@ -145,6 +145,11 @@ __global__ __launch_bounds__(max_threads<YT>()) void combine_kernel(const YT* __
 
 }  // namespace
 
+bool combine_fits(int T, int H, int y_dtype) {
+  const int threads = combine_threads(H, y_dtype == MOE_OUT_FP32 ? max_threads<float>() : max_threads<uint16_t>());
+  return (int64_t)T * threads < 1ll << 32;
+}
+
 template <typename YT, bool CHECKED>
 static moe_status launch_typed(const void* y, const int32_t* dest_row, const float* w, int T, int k, int H, float* out,
                                uint16_t* x_next, hipStream_t s) {

@@ -51,6 +51,8 @@ moe_status launch_gemm(const moe_gemm_args& a, void* ws, hipStream_t s, int rese
 // (dest_row outside [0, T*k): nothing is added; the layer's bf16 rows are all there)
 moe_status launch_combine(const void* y, int y_dtype, const int32_t* dest_row, const float* w,
                           int T, int k, int H, float* out, uint16_t* x_next, hipStream_t s);
+// one workgroup a token: whether the launch stays below 2^32 threads
+bool combine_fits(int T, int H, int y_dtype);
 moe_status launch_layer_combine(const void* y, const int32_t* dest_row, const float* w, int T, int k, int H, float* out,
                                 uint16_t* x_next, hipStream_t s);
 moe_status validate_gemm(const moe_gemm_args& a);
