@@ -706,7 +706,9 @@ moe_status moe_expert_ffn_forward(const moe_expert_ffn_args* args, void* stream)
  *   dx[t] = sum_{j < gather_div} dx_row[dest_row[t * gather_div + j]]
  * with moe_permute's dest_row; a dest_row outside the experts' rows counts as
  * none.  The rows' gradients are held in fp32 until they are summed.
- * Any of dx, dw1, dw2 may be NULL.  Deterministic: no atomics. */
+ * Any of dx, dw1, dw2 may be NULL.  Deterministic: no atomics.
+ * Sizes as for the forward pass, with gather tokens * gather_div < 2^31 for dx and
+ * tokens * x_stride < 2^30 for dw1. */
 typedef struct moe_expert_ffn_grad_args {
   int32_t        rows, H, I, E;
   int32_t        layout, gate_act;

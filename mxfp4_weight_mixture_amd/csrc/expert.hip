@@ -370,28 +370,29 @@ __global__ __launch_bounds__(256) void gather_rows_kernel(DenseJob p, const int3
 template <typename E>
 __global__ __launch_bounds__(512) void sum_rows_kernel(const float* __restrict__ dxr, const int32_t* __restrict__ dest,
                                                        const int32_t* __restrict__ offsets, int experts, int rows,
-                                                       int div, int H, void* __restrict__ dx, int dx_dtype,
+                                                       int tokens, int div, int H, void* __restrict__ dx, int dx_dtype,
                                                        int64_t dx_stride) {
-  const int64_t t = blockIdx.x;
   const int lo = max(offsets[0], 0), hi = min(offsets[experts], rows);
-  for (int v = threadIdx.x; v < H >> 3; v += blockDim.x) {
-    F8 s{};
-    for (int j0 = 0; j0 < div; j0 += 8) {
-      F8 r[8];
-      bool in[8];
+  for (int64_t t = blockIdx.x; t < tokens; t += gridDim.x) {
+    for (int v = threadIdx.x; v < H >> 3; v += blockDim.x) {
+      F8 s{};
+      for (uint32_t j0 = 0; j0 < (uint32_t)div; j0 += 8) {
+        F8 r[8];
+        bool in[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int d = j0 + j < div ? dest[t * div + j0 + j] : -1;
-        in[j] = d >= lo && d < hi;
-        if (in[j]) r[j] = load8<E>(dxr, MOE_FLOAT_FP32, (size_t)d * H + 8 * v);
+        for (int j = 0; j < 8; ++j) {
+          const int d = j0 + j < (uint32_t)div ? dest[t * div + j0 + j] : -1;
+          in[j] = d >= lo && d < hi;
+          if (in[j]) r[j] = load8<E>(dxr, MOE_FLOAT_FP32, (size_t)d * H + 8 * v);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (in[j])
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s.v[e] += r[j].v[e];
       }
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (in[j])
-#pragma unroll
-          for (int e = 0; e < 8; ++e) s.v[e] += r[j].v[e];
+      store8<E>(dx, dx_dtype, t * dx_stride + 8 * v, s);
     }
-    store8<E>(dx, dx_dtype, t * dx_stride + 8 * v, s);
   }
 }
 
@@ -689,13 +690,12 @@ moe_status moe_expert_ffn_backward(const moe_expert_ffn_grad_args* a, void* stre
   if (a->dx) MXMOE_TRY(check_stride(what, "dx_stride", a->dx_stride, a->H));
   MXMOE_TRY(check_gather(what, a->gather, a->rows, a->tokens, a->gather_div, a->dw1 ? a->x_stride : 0));
   const bool gathered = a->gather_div > 0;
-  if (gathered && (int64_t)a->tokens * a->gather_div >= 1ll << 31)
+  if (gathered && a->dx && (int64_t)a->tokens * a->gather_div >= 1ll << 31)
     return fail(MOE_ERR_SHAPE, "%s: tokens * gather_div overflows int32", what);
   const int64_t rows = a->rows, H = a->H, I = a->I, E = a->E;
   const int64_t x_rows = gathered ? a->tokens : rows, slots = gathered ? x_rows * a->gather_div : 0;
   const GradWs w = grad_ws(a->rows, a->H, a->I, a->E, gathered);
   if (gathered && a->dx && x_rows > 0 && !a->dest_row) return fail(MOE_ERR_INVALID_ARG, "%s: dx with gather needs dest_row", what);
-  if (gathered && x_rows >= 1 << 22) return fail(MOE_ERR_SHAPE, "%s: tokens = %d, past 2^22", what, a->tokens);
   if (rows > 0) {
     if (!a->dout || !a->expert_offsets || !a->w2 || !a->gate_up || (a->dw1 && !a->x && x_rows > 0) || (a->dx && !a->w1))
       return fail(MOE_ERR_INVALID_ARG, "%s: null pointer", what);
@@ -785,14 +785,15 @@ moe_status moe_expert_ffn_backward(const moe_expert_ffn_grad_args* a, void* stre
   MXMOE_TRY(a->dtype == MOE_FLOAT_BF16 ? launch_back_typed<__bf16>(g, dx, dx_step, dw1, dw2, s)
                                        : launch_back_typed<_Float16>(g, dx, dx_step, dw1, dw2, s));
   if (a->dx && gathered && x_rows > 0) {
-    const dim3 grid((unsigned)x_rows), block(std::min(512, (a->H / 8 + 63) / 64 * 64));
+    // (up to 512 threads a block: the launch stays below 2^32)
+    const dim3 grid((unsigned)std::min<int64_t>(x_rows, 1 << 22)), block(std::min(512, (a->H / 8 + 63) / 64 * 64));
     const float* const dxr = reinterpret_cast<const float*>(ws + w.dx);
     if (a->dtype == MOE_FLOAT_BF16)
       hipLaunchKernelGGL((sum_rows_kernel<__bf16>), grid, block, 0, s, dxr, a->dest_row, a->expert_offsets, a->E, a->rows,
-                         a->gather_div, a->H, a->dx, a->dx_dtype, a->dx_stride);
+                         a->tokens, a->gather_div, a->H, a->dx, a->dx_dtype, a->dx_stride);
     else
       hipLaunchKernelGGL((sum_rows_kernel<_Float16>), grid, block, 0, s, dxr, a->dest_row, a->expert_offsets, a->E,
-                         a->rows, a->gather_div, a->H, a->dx, a->dx_dtype, a->dx_stride);
+                         a->rows, a->tokens, a->gather_div, a->H, a->dx, a->dx_dtype, a->dx_stride);
     MXMOE_HIP(hipGetLastError());
   }
   return MOE_OK;

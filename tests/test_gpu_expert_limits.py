@@ -73,3 +73,31 @@ def test_gradients_whose_tiles_are_many_together():
         refs = du.ffn_grad_bounds(d64, x64, du.f64(f.w1[e]), du.f64(f.w2[e]), "split", "silu", BF, F, BF, BF)
         for what, got, (ref, bound) in zip(("dx", "dw1", "dw2"), (grads[0][e: e + 1], grads[1][e], grads[2][e]), refs):
             du.assert_within(got, ref, bound, f"{what} of expert {e}")
+
+
+def test_gradients_of_more_tokens_than_blocks():
+    """A token's rows are summed by blocks that take several tokens from 2^22 on; forward takes as many."""
+    T, E, H, I, rows = (1 << 22) + 77, 5, 8, 8, 3000
+    g = torch.Generator().manual_seed(3)
+    counts = [700, 0, 1300, 999, 1]
+    off = torch.tensor(np.concatenate([[0], np.cumsum(counts)]), dtype=torch.int32, device="cuda")
+    # every row is a token's only one (gather_div 1); the last tokens and those around 2^22 among them
+    token = torch.randperm(T - 200, generator=g)[:rows]
+    token[:200] = torch.arange(T - 200, T)
+    token = token[torch.randperm(rows, generator=g)].to("cuda")
+    dest = torch.full((T,), -1, dtype=torch.int32, device="cuda")
+    dest[token] = torch.arange(rows, dtype=torch.int32, device="cuda")
+    f = mx.ExpertFFN(du.normal((E, 2 * I, H), H ** -0.5, BF, 1), du.normal((E, H, I), I ** -0.5, BF, 2))
+    x = torch.zeros((T, H), dtype=BF, device="cuda")
+    x[token] = du.normal((rows, H), 1.0, BF, 4)
+    dout = du.normal((rows, H), 1.0, BF, 5)
+    how = dict(gather=token.to(torch.int32), gather_div=1)
+    out, gu = f.forward(x, off, save=True, **how)
+    dx = torch.full((T, H), float("nan"), dtype=F, device="cuda")
+    _, dw1, dw2 = f.backward(dout, x, off, gu, dest_row=dest, dx=dx, **how)
+    plain = x[token]
+    want, v1, v2 = f.backward(dout, plain, off, gu, dx=torch.empty((rows, H), dtype=F, device="cuda"))
+    assert torch.equal(f.forward(plain, off), out) and torch.equal(dw1, v1) and torch.equal(dw2, v2)
+    assert torch.equal(dx[token], want)
+    dx[token] = 0.0
+    assert not dx.any()

@@ -31,3 +31,25 @@ def test_combine(y_dtype, H, most):
     for T in (most + 1, 2 ** 31 - 1):
         assert f"T = {T}" in _refusal(call(T, P))
     assert "null" in _refusal(call(most, None))
+
+
+def _expert_grad(**kw):
+    p = 1 << 20
+    d = dict(rows=8, H=64, I=32, E=3, layout=1, gate_act=0, dtype=0, save_dtype=2, dx_dtype=0, dw_dtype=0, accumulate=0,
+             tokens=1 << 22, gather_div=2, dout=p, x=2 * p, gather=3 * p, dest_row=4 * p, expert_offsets=5 * p, w1=6 * p,
+             w2=7 * p, gate_up=8 * p, dx=9 * p, dw1=10 * p, dw2=11 * p, dout_stride=64, x_stride=64, dx_stride=64,
+             workspace=12 * p, workspace_bytes=64)
+    d.update(kw)
+    return _refusal(mx.lib.moe_expert_ffn_backward(ctypes.byref(mx.ExpertFfnGradArgs(**d)), None))
+
+
+@pytest.mark.parametrize("kw,needle", [
+    # what forward takes, backward takes: as many tokens as x may have, and any number without dx
+    (dict(), "workspace 64 bytes"), (dict(tokens=(1 << 24) - 1), "workspace 64 bytes"),
+    (dict(tokens=1 << 27, x_stride=8, H=8, dx_stride=8, dout_stride=8, dw1=None), "workspace 64 bytes"),
+    (dict(dx=None, dest_row=None), "workspace 64 bytes"),
+    (dict(tokens=1 << 22, gather_div=1 << 10, dx=None, dest_row=None), "workspace 64 bytes"),
+    (dict(tokens=1 << 22, gather_div=1 << 9), "overflows"), (dict(tokens=1 << 24), "2^30"),
+])
+def test_tokens_of_the_experts_backward(kw, needle):
+    assert needle in _expert_grad(**kw)
