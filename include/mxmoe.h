@@ -563,7 +563,8 @@ moe_status moe_adapter_linear(const moe_adapter_args* args, void* stream);
  * smallest power of two that brings its 32 values to 448 or below, so none
  * saturates; codes are rounded to nearest even; a block that holds an infinity
  * or NaN has scale byte 255 and NaN codes.  Squares are summed in fp32: rows
- * whose sum of squares passes 3.4e38 come out as zeros.
+ * whose sum of squares passes 3.4e38 come out as zeros, and with eps 0 rows whose
+ * sum of squares is below 2^-126 lose precision, at 2^-150 all of it.
  *
  * Sizes: 0 <= T < 2^22 (T == 0 enqueues nothing), H a multiple of 8 in
  * [8, 32768], of 32 with codes.  Row strides are in elements, multiples of 8, at
@@ -640,7 +641,8 @@ moe_status moe_rms_norm_backward(const moe_norm_grad_args* args, void* stream);
  * dout is fp32, as the combine's out; dy is rounded once, dtopk_w is fp32.  Either
  * may be NULL; y is read for dtopk_w only.  A dest_row outside [0, T*k) has no
  * row: nothing is written for it and its dtopk_w is 0.  Rows of dy that no
- * dest_row names are left as they were.  0 <= T < 2^22, 1 <= k <= 64, H a multiple
+ * dest_row names are left as they were; a row is named once at most (of two
+ * gradients one would be kept, either of them).  0 <= T < 2^22, 1 <= k <= 64, H a multiple
  * of 8 in [8, 262144]; y, dout and dy contiguous and 16-byte aligned;
  * no output may overlap an input or the other output. */
 moe_status moe_combine_backward(const float* dout, const void* y, int32_t y_dtype /* moe_float_dtype */,

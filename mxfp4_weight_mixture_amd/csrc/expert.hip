@@ -14,9 +14,10 @@
 // has the same tiles for every expert and the expert's rows as its K.
 //
 // What bounds it: with a few rows an expert the reading of its weights (192 rows
-// over 256 experts of 4096 x 2048: 1.08 ms, 6.2 TB/s); with many the dense tiles'
-// K loop (dense_tile.h) and their ends (49152 rows over 32 experts, forward and
-// backward: 7.7 to 7.9 ms, 0.95 PFLOP/s).
+// over 137 of 256 experts of 4096 x 2048: 1.07 to 1.14 ms, 6.0 to 6.4 TB/s); with
+// many the dense tiles' K loop (dense_tile.h) and their ends, which one block a CU
+// does not hide (49152 rows over 32 experts, forward and backward: 7.8 to 8.0 ms,
+// 0.93 PFLOP/s).
 #include <algorithm>
 
 #include "dense_few.h"
@@ -296,9 +297,11 @@ __device__ __forceinline__ RowTile nth_tile(const int32_t* offsets, int E, int r
 // of its rows, as the dense kernel of few rows does; bound by reading the weights
 // of the experts that have rows.  Four waves split K, not eight: they have 16 turns
 // of 64 k each at K = 4096, not 8, beside a block's ends, and with 48 or 32 KB of LDS
-// three to five blocks a CU cover each other's (192 rows, 256 experts of 4096 x 2048:
-// 1143 us, eight waves 1330).  Every block finds its rows by itself from the offsets:
-// no launch ahead of the product.
+// three to five blocks a CU cover each other's.  Us with four / eight waves, forward:
+// 256 experts of 4096 x 2048, 6 rows 58 / 68, 24 rows 208 / 213; 64 of 2048 x 1024, 64
+// rows 149 / 168; 8 of 4096 x 3584, 16 rows 123 / 142, and the other way 128 rows 131 /
+// 128.  Every block finds its rows by itself from the offsets: no launch ahead of the
+// product.
 constexpr int kGroupFewWaves = 4;
 template <typename E, int MB, int NB, int EPI, int D, bool GATHER>
 __global__ __launch_bounds__(64 * kGroupFewWaves) void group_few_kernel(GroupJob g, const int32_t* offsets, int experts,
@@ -408,11 +411,15 @@ struct Group {
 
 // A few rows an expert, and too few experts with rows for narrow tiles to fill the
 // chip: the weights stream in tiles of 32 rows of them.  Us with these kernels / in
-// narrow tiles: 256 experts of 4096 x 2048, 6 rows 61 / 67, 24 rows 198 / 207, 192
-// rows 1221 / 1081 (6.3 TB/s); 64 of 2048 x 1024, 64 rows 105 / 120; 8 of 4096 x
-// 3584, 2 rows 35 / 69, 16 rows 108 / 123, 128 rows 132 / 139.  Short rows of the
-// weights are better off in narrow tiles (64 of 1024 x 768, 512 rows 62 / 58), and
-// so are more than 16 rows an expert (16 of 1096 x 776, 256 rows 24.8 / 25.5).
+// narrow tiles, whole forward passes, rows spread evenly: 256 experts of 4096 x 2048, 6
+// rows 58 / 60, 24 rows 208 / 207, 48 rows (past the bound) 415 / 404; 64 of 2048 x
+// 1024, 64 rows 149 / 166, 256 rows 151 / 167; 8 of 4096 x 3584, 2 rows 33 / 49, 16 rows
+// 123 / 138, 128 rows 131 / 138; 6 of 1096 x 1032, 96 rows 14 / 23.  Short rows of the
+// weights gain nothing: both products of 64 of 1024 x 768, 512 rows, 61 / 55 (its FC1,
+// with rows of just 1024, still comes here: 60), of 16 of 1096 x 776, 256 rows, 23.9 /
+// 23.9.  Past 32 rows an expert a second tile would read its weights again; from 16 to
+// 32 the two are within 3 % (8 of 4096 x 3584, 192 rows 135 / 139; 16 of 1096 x 776, 320
+// rows 24.4 / 24.7).
 // A block's rows (of a split gate also their up rows) lie within 31 bits of the first.
 bool takes_few(const Group& g, const DenseJob& j) {
   const int64_t reach = j.epi == kEpiGate && !j.interleaved ? (int64_t)(j.N / 2 + 16) * j.ldb * 2 : 0;
@@ -438,18 +445,22 @@ moe_status launch_few(const Group& g, const DenseJob& j, int64_t b_step, hipStre
 // long sums: narrow ones where, with the rows spread evenly, they would leave a
 // third of the CUs idle, where the weights' stream is what counts, and where short
 // sums leave the tiles' ends much of the time, which two blocks a CU hide.  Us,
-// wide / narrow:
-//   8 experts of 4096 x 2048    1024 rows 181 / 137, 2048 rows 193 / 203
-//   24 of 1096 x 776            384 rows 46 / 40, 3000 rows 97 / 79
-//   8 of 7168 x 3584            512 rows (224 tiles) 235 / 276
-//   256 of 4096 x 2048          384 rows 1724 / 1685, 6144 rows 2245 / 2215, 24576 rows 2418 / 2845
-//   32 of 2048 x 1024           2048 rows 114 / 104, 4096 rows 148 / 140
-//   64 of 2048 x 1024           6144 rows 219 / 206, 12288 rows 301 / 326
+// wide / narrow, whole forward passes, rows spread evenly (an asterisk: what the rule
+// takes):
+//   8 experts of 4096 x 2048    1024 rows 126 / 112*, 2048 rows 192 / 168*, 2560 rows 198* / 234
+//   11 of 4096 x 2048           1408 rows 156 / 175*, 2816 rows 210 / 227* (176 tiles: just at the bound)
+//   24 of 1096 x 776            384 rows 33 / 33*, 3000 rows 49 / 52*
+//   8 of 7168 x 3584            512 rows (224 tiles) 223* / 237
+//   256 of 4096 x 2048          384 rows 2184 / 2123*, 6144 rows 2260 / 2220*, 24576 rows 2378* / 2796
+//   32 of 2048 x 1024           2048 rows 105 / 96*, 4096 rows 117 / 113*, 5120 rows 146* / 168
+//   64 of 2048 x 1024           6144 rows 212 / 205*, 12288 rows 282* / 364
 // (128 x 256 tiles of 32-deep stages, two blocks a CU, lie between the two.)
 // Where even narrow tiles are fewer than the CUs' room for them, a block's time is
 // its K loop's latency: 64 x 64 tiles whose four waves split K (narrow / split: 9
-// experts of 1096 x 776, 512 rows 36 / 23, 1034 rows 38 / 31, 2048 rows 40 / 45; 24 of
-// them, 1000 rows, 504 tiles, 50 / 58).
+// experts of 1096 x 776, 512 rows 24.8 / 21.4*, 1034 rows 36.8 / 29.4*, 1400 rows 35.1* /
+// 33.8, 2048 rows 37.0* / 43.4; 24 of them, 1000 rows, 504 tiles, 35.2* / 40.0; 16 of
+// them, 64 to 320 rows, 336 tiles, 24 / 28*: with one row tile an expert two blocks
+// a CU of narrow tiles would do).
 int tile_shape(int rows, int E, int H, int I) {
   const int n = std::max(std::min(E, rows), 1), each = (rows + n - 1) / n;
   // columns: of the two products, on average

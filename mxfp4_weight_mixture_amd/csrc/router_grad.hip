@@ -164,7 +164,7 @@ moe_status moe_combine_backward(const float* dout, const void* y, int32_t y_dtyp
                                 float* dtopk_w, void* stream) {
   const char* what = "combine backward";
   clear_error();
-  if (T < 0 || T >= 1 << 22 || k < 1 || k > 64)   // a block of up to 512 threads a token
+  if (T < 0 || T >= 1 << 22 || k < 1 || k > 64)   // a block of up to 256 threads a token
     return fail(MOE_ERR_SHAPE, "%s: T = %d, k = %d out of range", what, T, k);
   MXMOE_TRY(check_width(what, "H", H));
   const int64_t rows = (int64_t)T * k;
