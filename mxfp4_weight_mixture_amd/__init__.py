@@ -296,6 +296,14 @@ def permute(topk_ids: torch.Tensor, E: int, stream=None):
     return off, ps, dr
 
 
+def _activations(name, x, scales=None):
+    """What the MXFP4 products read: bf16 (or its bits), with scales E4M3 codes.  fp16 or fp32 values (a norm's output
+    beside fp16 weights, a layer's sum) would be taken for others."""
+    if x.element_size() != (2 if scales is None else 1) or x.dtype == torch.float16:
+        raise ValueError(f"{name} is {x.dtype}, not " + ("torch.bfloat16" if scales is None else
+                                                         "E4M3 codes of one byte, as its scales say"))
+
+
 def grouped_gemm(a: torch.Tensor, w_packed: torch.Tensor, w_scales: torch.Tensor,
                  expert_offsets: torch.Tensor, *, a_scales: Optional[torch.Tensor] = None,
                  a_gather: Optional[torch.Tensor] = None, a_gather_div: int = 1, rows: Optional[int] = None,
@@ -307,6 +315,7 @@ def grouped_gemm(a: torch.Tensor, w_packed: torch.Tensor, w_scales: torch.Tensor
     (fp32 or bf16), or for out_dtype "mxfp8" the pair (E4M3 codes uint8
     [rows][N/2], E8M0 scales uint8 [rows][N/64]).
     """
+    _activations("a", a, a_scales)
     E, N, K2 = w_packed.shape
     K = 2 * K2
     if rows is None:
@@ -1028,6 +1037,7 @@ class Layer:
                 out: Optional[torch.Tensor] = None, x_next: Optional[torch.Tensor] = None, stream=None,
                 x_shared: Optional[torch.Tensor] = None):
         """x_shared: the shared expert's activations where x does not hold them (MXFP8 x, or another type)."""
+        _activations("x", x, x_scales)
         x_shared = self._shared_input(x, x_scales, x_shared, x_next)
         T = logits.shape[0]
         n = self.workspace_bytes(T)
@@ -1091,6 +1101,7 @@ class LayerGraph:
     """
 
     def __init__(self, layer: Layer, logits, x, x_scales=None, out=None, x_next=None, x_shared=None):
+        _activations("x", x, x_scales)
         x_shared = layer._shared_input(x, x_scales, x_shared, x_next)
         T = logits.shape[0]
         dev = logits.device
@@ -1168,6 +1179,7 @@ def prefill_streamed(host_blobs: Sequence[torch.Tensor], slots: Sequence[torch.T
     side stream per device (never the compute stream, which would serialise the
     pipeline).
     """
+    _activations("x", x)
     nb = len(host_blobs)
     arr = (_vp * nb)(*[b.data_ptr() for b in host_blobs])
     need = lib.moe_streamed_workspace_size(T, H, I, E, k)
