@@ -269,8 +269,15 @@ def device_supported() -> bool:
 
 # ----------------------------------------------------------------- calls
 
+def _read_as(name, t, dtype):
+    """A tensor that the library reads as contiguous `dtype`, whatever it holds."""
+    if t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {dtype}: got {t.dtype}, shape {tuple(t.shape)}, strides {t.stride()}")
+
+
 def route(logits: torch.Tensor, k: int, stream=None):
     """moe_route: logits fp32 [T][E] -> (topk_ids int32 [T][k], topk_w fp32 [T][k])."""
+    _read_as("logits", logits, torch.float32)
     T, E = logits.shape
     with _allocate_on(stream):
         ids = torch.empty((T, k), dtype=torch.int32, device=logits.device)
@@ -282,6 +289,7 @@ def route(logits: torch.Tensor, k: int, stream=None):
 
 def permute(topk_ids: torch.Tensor, E: int, stream=None):
     """moe_permute: topk_ids [T][k] -> (expert_offsets [E+1], perm_src [T*k], dest_row [T*k])."""
+    _read_as("topk_ids", topk_ids, torch.int32)
     T, k = topk_ids.shape
     dev = topk_ids.device
     n = lib.moe_permute_workspace_size(T, E, k)
@@ -1037,6 +1045,7 @@ class Layer:
                 out: Optional[torch.Tensor] = None, x_next: Optional[torch.Tensor] = None, stream=None,
                 x_shared: Optional[torch.Tensor] = None):
         """x_shared: the shared expert's activations where x does not hold them (MXFP8 x, or another type)."""
+        _read_as("logits", logits, torch.float32)
         _activations("x", x, x_scales)
         x_shared = self._shared_input(x, x_scales, x_shared, x_next)
         T = logits.shape[0]
@@ -1101,6 +1110,7 @@ class LayerGraph:
     """
 
     def __init__(self, layer: Layer, logits, x, x_scales=None, out=None, x_next=None, x_shared=None):
+        _read_as("logits", logits, torch.float32)
         _activations("x", x, x_scales)
         x_shared = layer._shared_input(x, x_scales, x_shared, x_next)
         T = logits.shape[0]
@@ -1179,6 +1189,7 @@ def prefill_streamed(host_blobs: Sequence[torch.Tensor], slots: Sequence[torch.T
     side stream per device (never the compute stream, which would serialise the
     pipeline).
     """
+    _read_as("logits", logits, torch.float32)
     _activations("x", x)
     nb = len(host_blobs)
     arr = (_vp * nb)(*[b.data_ptr() for b in host_blobs])
